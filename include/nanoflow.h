@@ -433,6 +433,121 @@ nf_status nf_gemm_wrows(const void* A, const void* B, void* C, const void* R, in
                         int32_t N, int32_t K, int32_t epilogue, int32_t splits, int32_t max_sms,
                         void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A 4-bit paged KV cache.  Decode attention is bound by the bytes of K and V
+ * it reads ("NanoFlow: Towards Optimal LLM Serving Throughput", "The
+ * Intra-Device Parallelism Mechanism": the memory-bound operation); this cache
+ * holds them in 4.5 bits a value instead of 16.  The entry points build its
+ * block tables on the GPU, fill it, take rows out again and attend over it.
+ *
+ * NF_KV_FP4 format.  A block is 16 consecutive channels of K or V of one
+ * (position, KV head).  With E = k_exp for K and v_exp for V:
+ *   a = max |x_i|;  s = e4m3(a / (6 * 2^E)), n_i = e2m1(x_i / (s * 2^E)), both
+ *   rounded to nearest, ties to even, saturating at 448 and 6; n_i = 0 where
+ *   s = 0; a NaN anywhere in the block makes s NaN; the block stands for
+ *   n_i * s * 2^E.  Infinities saturate.
+ * These products have 6 significant bits, so they are exact in bf16.  The
+ * decisions are those of the formulas in 64-bit arithmetic.
+ * Pool: uint8 [num_pages, n_kv, 2 (K, V), 9 * head_dim]: the page's 16 rows of
+ * head_dim / 2 code bytes (channel 2i in the low half of byte i), then 16 rows
+ * of head_dim / 16 scale bytes.  16-byte aligned.
+ * NF_KV_BF16: the pools of nf_layer_step. */
+typedef enum { NF_KV_BF16 = 0, NF_KV_FP4 = 1 } nf_kv_format;
+typedef struct {
+  int32_t format;    /* nf_kv_format */
+  int32_t num_pages; /* pages of the pool(s) */
+  void* k;           /* BF16: the K pool; FP4: the packed pool */
+  void* v;           /* BF16: the V pool; FP4: NULL */
+  int32_t k_exp;     /* FP4: exponents E of K and V, -64 ... 64 */
+  int32_t v_exp;
+} nf_kv_cache;
+
+/* Bytes of an NF_KV_FP4 pool. */
+nf_status nf_kv4_pool_bytes(const nf_model_shape* shape, int32_t num_pages, size_t* bytes);
+
+/* Block tables and slot maps of a step from request lengths, on the GPU
+ * ("Inside nano-vLLM", 4.2 Paged KV: block table and slot mapping).  All
+ * pointers device int32.
+ * held, seq_lens: [n_seq] positions request s holds pages for, and those it
+ *   shall hold after this step (clamped to [0, 16 * max_pages]).  A longer
+ *   request takes pages, a shorter one (0: a finished one) gives pages back;
+ *   pages belong to one request (none are shared).
+ * block_table: [n_seq, max_pages], in and out.  Entries of new pages are
+ *   written; every other entry stays as it is, also those given back.
+ * ring: [num_pages], in and out: the free pages are ring[(head + i) % num_pages]
+ *   for i < count, {head, count} = state_in[0 .. 1].  New pages are taken from
+ *   its front in the order of requests, then pages; pages given back go behind
+ *   its end in the same order, and are free from the next call on.
+ * state_out: [4] = {head, count} after the call, the step's tokens, and the
+ *   pages missing.  It must not overlap state_in, which the call only reads.
+ *   If the free pages do not suffice (missing > 0) no page changes hands: head
+ *   and count stay, the entries of new pages and the slots in them are -1.
+ * The step's tokens are the positions held[s] ... seq_lens[s] - 1 of request 0,
+ *   then request 1, ...: tok_begin [n_seq + 1] gives each request's first,
+ *   tok_seq, tok_pos, tok_slot [tok_cap] each token's request, position and
+ *   cache slot (page * 16 + position % 16, -1 without a valid page).  Rows past
+ *   the last token stay as they are; tokens past tok_cap are not written.
+ * The call reads nothing that it writes, so repeating it with the same
+ * state_in gives the same result. */
+nf_status nf_block_tables(const int32_t* held, const int32_t* seq_lens, int32_t n_seq,
+                          int32_t* block_table, int32_t max_pages, int32_t* ring,
+                          int32_t num_pages, const int32_t* state_in, int32_t* state_out,
+                          int32_t* tok_begin, int32_t* tok_seq, int32_t* tok_pos,
+                          int32_t* tok_slot, int32_t tok_cap, void* stream);
+
+/* Per-head RMSNorm and RoPE of a step's queries and keys, and the append of its
+ * keys and values to the cache, in one pass.
+ * qkv: device bf16 [n_tok, ld], each row the q heads, then the k heads, then
+ *   the v heads; ld >= (n_q + 2 n_kv) * head_dim, a multiple of 8.
+ * q_gain, k_gain: device bf16 [head_dim], or NULL: those heads are not normed.
+ *   Normed heads become u * gain / sqrt(mean(u^2) + shape->rms_eps).
+ * tok_pos, tok_slot: device int32 [n_tok].  Rotation as in nf_layer_step (pairs
+ *   i and i + head_dim / 2, angle pos * rope_theta^(-2i / head_dim)), accurate
+ *   at every 32-bit position.  A token whose slot is outside
+ *   [0, 16 * num_pages) stores nothing; no two tokens may share a slot.
+ * q: device bf16 [n_tok, n_q, head_dim], not overlapping qkv.
+ * cache: the rotated k and the v go to the tokens' slots, rounded to bf16, or
+ *   to 4 bits straight from the fp32 values (borderline codes from 64 bits). */
+nf_status nf_qk_norm_rope(const nf_model_shape* shape, const void* qkv, int32_t ld,
+                          const void* q_gain, const void* k_gain, const int32_t* tok_pos,
+                          const int32_t* tok_slot, int32_t n_tok, void* q,
+                          const nf_kv_cache* cache, void* stream);
+
+/* Rows of an NF_KV_FP4 cache by slot: slots device int32 [n], k and v device
+ * bf16 [n, n_kv, head_dim].  A slot outside the pool gives a zero row. */
+nf_status nf_kv4_read(const nf_model_shape* shape, const nf_kv_cache* cache, const int32_t* slots,
+                      int32_t n, void* k, void* v, void* stream);
+
+/* Attention over an NF_KV_FP4 cache.  The handle owns the device workspace and
+ * the status word, made on the current device; like a plan it serves one stream
+ * at a time, and two captured graphs that use it must not run at once.
+ * Shapes as nf_model_shape allows; 1 <= max_pages_per_seq. */
+typedef struct nf_kv4_s* nf_kv4;
+nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t max_pages_per_seq,
+                        nf_kv4* out);
+void nf_kv4_destroy(nf_kv4 h);
+/* As nf_plan_poll, for the calls on this handle. */
+nf_status nf_kv4_poll(nf_kv4 h, int wait);
+
+/* Causal GQA attention of a step's tokens over the cache, which must already
+ * hold the step's K and V.
+ * q, o: device bf16 [n_tok, n_q, head_dim].  block_table: device int32
+ *   [n_seq, max_pages_per_seq].  seq_lens: device int32 [n_seq], lengths after
+ *   the step.  tok_begin: device int32 [n_seq + 1], request s owns the rows
+ *   [tok_begin[s], tok_begin[s + 1]), or NULL: one row each (n_tok = n_seq).
+ * Row i of the n rows of a request sits at position seq_lens[s] - n + i and sees
+ * positions 0 ... its own; a row without any (a padding row of a request of
+ * length 0) becomes zero.  Rows from tok_begin[n_seq] on stay as they are, so
+ * a batch padded to n_tok rows is fine.
+ * A page id outside the pool reads page 0, a length outside
+ * [0, 16 * max_pages_per_seq] counts as 0, rows outside [0, n_tok) are left
+ * out; each sets the status that nf_kv4_poll reports.
+ * NF_ERR_INVALID_ARG if another device than the handle's is current. */
+nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
+                           const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* tok_begin, int32_t n_seq, int32_t n_tok, void* o,
+                           void* stream);
+
 /* Copy one of the plan's device buffers (written by the last step or
  * metadata call on the plan's device) to dst (host or device), synchronously.
  * bytes must not exceed the buffer size (nf_plan_buffer_size). */

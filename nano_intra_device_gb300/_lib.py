@@ -21,6 +21,7 @@ NF_OK, NF_ERR_INVALID_ARG, NF_ERR_UNSUPPORTED, NF_ERR_OOM, NF_ERR_CUDA, NF_ERR_T
 NF_EXEC_SEQUENTIAL, NF_EXEC_STREAMS = 0, 1
 NF_ATTN_AUTO, NF_ATTN_MMA = 0, 2
 NF_EPI_STORE, NF_EPI_RESID, NF_EPI_SWIGLU = 0, 1, 2
+NF_KV_BF16, NF_KV_FP4 = 0, 1
 (NF_BUF_TOK_SEQ, NF_BUF_TOK_POS, NF_BUF_TOK_SLOT, NF_BUF_ITEMS, NF_BUF_ITEM_SEG, NF_BUF_N1,
  NF_BUF_Q, NF_BUF_O, NF_BUF_H, NF_BUF_N2, NF_BUF_A, NF_BUF_MOE_OFF, NF_BUF_MOE_PERM,
  NF_BUF_MOE_PAIR_ROW, NF_BUF_MOE_PAIR_W) = range(15)
@@ -76,6 +77,11 @@ class nf_layer_weights(Structure):
                                         "w_experts_gate_up", "w_experts_down", "router_logits")]
 
 
+class nf_kv_cache(Structure):
+    _fields_ = [("format", c_int32), ("num_pages", c_int32), ("k", c_void_p), ("v", c_void_p),
+                ("k_exp", c_int32), ("v_exp", c_int32)]
+
+
 class nf_stack_weights(Structure):
     _fields_ = [("embed", c_void_p), ("norm_f", c_void_p), ("lm_head", c_void_p),
                 ("vocab", c_int32), ("n_layers", c_int32), ("layers", POINTER(nf_layer_weights))]
@@ -119,6 +125,18 @@ _SIGS = {
     "nf_gemm": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p]),
     "nf_gemm_wrows": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
                               c_int32, c_int32, c_void_p]),
+    "nf_kv4_pool_bytes": (c_int, [POINTER(nf_model_shape), c_int32, POINTER(c_size_t)]),
+    "nf_block_tables": (c_int, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_int32, c_void_p,
+                                c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p]),
+    "nf_qk_norm_rope": (c_int, [POINTER(nf_model_shape), c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                                c_void_p, c_int32, c_void_p, POINTER(nf_kv_cache), c_void_p]),
+    "nf_kv4_read": (c_int, [POINTER(nf_model_shape), POINTER(nf_kv_cache), c_void_p, c_int32, c_void_p,
+                            c_void_p, c_void_p]),
+    "nf_kv4_create": (c_int, [POINTER(nf_model_shape), c_int32, c_int32, POINTER(c_void_p)]),
+    "nf_kv4_destroy": (None, [c_void_p]),
+    "nf_kv4_poll": (c_int, [c_void_p, c_int]),
+    "nf_attention_kv4": (c_int, [c_void_p, c_void_p, POINTER(nf_kv_cache), c_void_p, c_void_p, c_void_p,
+                                 c_int32, c_int32, c_void_p, c_void_p]),
     "nf_plan_buffer_size": (c_int, [c_void_p, c_int32, POINTER(c_size_t)]),
     "nf_plan_copy_buffer": (c_int, [c_void_p, c_int32, c_void_p, c_size_t]),
     "nf_plan_trace_enable": (c_int, [c_void_p, c_int32]),
@@ -181,6 +199,8 @@ def stream_handle(stream=None):
 
 
 def make_shape(shape) -> nf_model_shape:
+    if isinstance(shape, nf_model_shape):
+        return shape
     return nf_model_shape(shape.hidden, shape.n_q, shape.n_kv, shape.head_dim, shape.ffn,
                           shape.page_size, shape.rms_eps, shape.rope_theta,
                           getattr(shape, "n_experts", 0), getattr(shape, "top_k", 0))
@@ -419,6 +439,126 @@ def gemm_wrows(A, B, C, R=None, epilogue=NF_EPI_STORE, splits=0, max_sms=0, stre
     N = C.shape[1]
     check(lib().nf_gemm_wrows(ptr(A), ptr(B), ptr(C), ptr(R), M, N, K, epilogue, splits, max_sms,
                               stream_handle(stream)))
+
+
+# ------------------------------------------------------ the 4-bit KV cache
+
+def _dense(name, t, dtype, *shape):
+    """Check a tensor that a call's addresses are taken from (None in shape: any extent)."""
+    if t.dtype != dtype or not t.is_contiguous() or t.dim() != len(shape) or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {list(shape)}, "
+                         f"got {t.dtype} {list(t.shape)}")
+
+
+class KvCache:
+    """The nf_kv_cache of one layer, and the tensors it points to.
+
+    NF_KV_BF16: k, v as make_pools makes them.  NF_KV_FP4: k the packed pool
+    (kv4_pool), v None, and the exponents of K and V."""
+
+    def __init__(self, shape, num_pages, fmt, k, v=None, k_exp=0, v_exp=0):
+        import torch
+        s = make_shape(shape)
+        if fmt == NF_KV_FP4:
+            _dense("packed pool", k, torch.uint8, num_pages, s.n_kv_heads, 2, 9 * s.head_dim)
+        else:
+            for n, t in (("K pool", k), ("V pool", v)):
+                _dense(n, t, torch.bfloat16, num_pages, s.n_kv_heads, s.page_size, s.head_dim)
+        self.k, self.v = k, v
+        self.c = nf_kv_cache(fmt, num_pages, k.data_ptr(), None if v is None else v.data_ptr(), k_exp, v_exp)
+
+
+def kv4_pool_bytes(shape, num_pages):
+    """nf_kv4_pool_bytes: the size of a 4-bit pool."""
+    s, n = make_shape(shape), c_size_t()
+    check(lib().nf_kv4_pool_bytes(ctypes.byref(s), num_pages, ctypes.byref(n)))
+    return n.value
+
+
+def kv4_pool(shape, num_pages, device="cuda"):
+    """A zeroed 4-bit pool: uint8 [num_pages, n_kv, 2, 9 * head_dim]."""
+    import torch
+    s = make_shape(shape)
+    return torch.zeros(kv4_pool_bytes(s, num_pages), dtype=torch.uint8,
+                       device=device).view(num_pages, s.n_kv_heads, 2, -1)
+
+
+class BlockTables:
+    """The arguments of nf_block_tables (device int32 tensors, kept alive): held, seq_lens [n_seq],
+    block_table [n_seq, max_pages], ring [num_pages], state_in [2], state_out [4], tok_begin
+    [n_seq + 1], tok_seq, tok_pos, tok_slot [tok_cap]."""
+
+    def __init__(self, held, seq_lens, block_table, ring, state_in, state_out, tok_begin, tok_seq,
+                 tok_pos, tok_slot):
+        import torch
+        n, cap = held.numel(), tok_seq.numel()
+        i = torch.int32
+        for name, t, *shape in (("held", held, n), ("seq_lens", seq_lens, n), ("block_table", block_table, n, None),
+                                ("ring", ring, None), ("state_in", state_in, 2), ("state_out", state_out, 4),
+                                ("tok_begin", tok_begin, n + 1), ("tok_seq", tok_seq, cap), ("tok_pos", tok_pos, cap),
+                                ("tok_slot", tok_slot, cap)):
+            _dense(name, t, i, *shape)
+        self._keep = (held, seq_lens, block_table, ring, state_in, state_out, tok_begin, tok_seq, tok_pos, tok_slot)
+        self.a = (ptr(held), ptr(seq_lens), n, ptr(block_table), block_table.shape[1], ptr(ring), ring.numel(),
+                  ptr(state_in), ptr(state_out), ptr(tok_begin), ptr(tok_seq), ptr(tok_pos), ptr(tok_slot), cap)
+
+
+def block_tables(args: BlockTables, stream=None):
+    """nf_block_tables: block tables and slot maps of a step from request lengths."""
+    check(lib().nf_block_tables(*args.a, stream_handle(stream)))
+
+
+def qk_norm_rope(shape, qkv, q_gain, k_gain, tok_pos, tok_slot, q, cache: KvCache, stream=None):
+    """nf_qk_norm_rope: per-head norm (gains None: none) and rotation of q and k, k and v appended
+    to the cache.  qkv [n_tok, >= (n_q + 2 n_kv) d], rows may be strided."""
+    if qkv.stride(-1) != 1:
+        raise ValueError("qkv: the rows must be contiguous")
+    s = make_shape(shape)
+    if qkv.shape[1] < (s.n_q_heads + 2 * s.n_kv_heads) * s.head_dim:
+        raise ValueError("qkv: rows too short for the shape")
+    check(lib().nf_qk_norm_rope(ctypes.byref(s), ptr(qkv), qkv.stride(0), ptr(q_gain), ptr(k_gain), ptr(tok_pos),
+                                ptr(tok_slot), qkv.shape[0], ptr(q), ctypes.byref(cache.c), stream_handle(stream)))
+
+
+def kv4_read(shape, cache: KvCache, slots, k, v, stream=None):
+    """nf_kv4_read: rows of the 4-bit cache by slot, as bf16 k, v [n, n_kv, d]."""
+    s = make_shape(shape)
+    check(lib().nf_kv4_read(ctypes.byref(s), ctypes.byref(cache.c), ptr(slots), slots.numel(), ptr(k), ptr(v),
+                            stream_handle(stream)))
+
+
+class Kv4:
+    """Owns an nf_kv4: workspace and status of attention over a 4-bit cache."""
+
+    def __init__(self, shape, num_pages, max_pages):
+        self.h = c_void_p()
+        self.max_pages = max_pages
+        s = make_shape(shape)
+        check(lib().nf_kv4_create(ctypes.byref(s), num_pages, max_pages, ctypes.byref(self.h)))
+
+    def poll(self, wait=True):
+        check(lib().nf_kv4_poll(self.h, 1 if wait else 0))
+
+    def close(self):
+        if self.h:
+            lib().nf_kv4_destroy(self.h)
+            self.h = c_void_p()
+
+    def __del__(self):  # pragma: no cover
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def attention_kv4(handle: Kv4, q, cache: KvCache, block_table, seq_lens, o, tok_begin=None, stream=None):
+    """nf_attention_kv4: attention of a step's tokens over the 4-bit cache (tok_begin None: one row
+    per request)."""
+    if block_table.shape[1] != handle.max_pages:
+        raise ValueError(f"block_table: need rows of {handle.max_pages} entries, got {block_table.shape[1]}")
+    check(lib().nf_attention_kv4(handle.h, ptr(q), ctypes.byref(cache.c), ptr(block_table), ptr(seq_lens),
+                                 ptr(tok_begin), seq_lens.numel(), q.shape[0], ptr(o), stream_handle(stream)))
 
 
 def plan_search(shape, batch, profile_json=None, num_sms=152, n_layers=1):
