@@ -14,7 +14,10 @@
 struct nf_kv4_s {
   nf_model_shape shape{};
   int num_pages = 0, max_pages = 0, device = 0, num_sms = 0;
+  // one allocation: status word (256 bytes), arrival counters, split records
   uint32_t* status = nullptr;
+  int* counters = nullptr;
+  float* records = nullptr;
 };
 
 namespace {
@@ -229,11 +232,16 @@ nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t 
   h->max_pages = max_pages_per_seq;
   h->device = dev;
   h->num_sms = sms;
-  if (cudaMalloc(&h->status, 256) != cudaSuccess || cudaMemset(h->status, 0, 256) != cudaSuccess) {
+  const size_t cnt = ((size_t)sms * 4 + 255) / 256 * 256;
+  const size_t rec = (size_t)sms * 2 * nf::kv4_record_bytes(shape->head_dim);
+  if (cudaMalloc(&h->status, 256 + cnt + rec) != cudaSuccess ||
+      cudaMemset(h->status, 0, 256 + cnt) != cudaSuccess) {
     cudaGetLastError();
     nf_kv4_destroy(h);
     return fail4(NF_ERR_OOM, "cudaMalloc of the workspace failed");
   }
+  h->counters = reinterpret_cast<int*>(reinterpret_cast<char*>(h->status) + 256);
+  h->records = reinterpret_cast<float*>(reinterpret_cast<char*>(h->status) + 256 + cnt);
   *out = h;
   return NF_OK;
 }
@@ -301,6 +309,9 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
   a.v_scale = nf::exp2_int(cache->v_exp);
   a.status = h->status;
   a.timeout_ns = 2000000000ULL;
+  a.grid = h->num_sms;
+  a.records = h->records;
+  a.counters = h->counters;
   NF_CUDA4(nf::launch_attention_kv4(a, static_cast<cudaStream_t>(stream)));
   return NF_OK;
 }

@@ -64,7 +64,11 @@ struct Kv4AttnArgs {
   float v_scale;     // 2^v_exp
   uint32_t* status;
   unsigned long long timeout_ns;
+  int grid;              // CTAs, one an SM
+  float* records;        // [grid][2] records of kv4_record_bytes
+  int* counters;         // [grid], zero between launches
 };
+size_t kv4_record_bytes(int head_dim);
 cudaError_t launch_attention_kv4(const Kv4AttnArgs& a, cudaStream_t stream);
 
 }  // namespace nf
