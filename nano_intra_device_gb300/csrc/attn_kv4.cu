@@ -34,6 +34,8 @@
 // CTA, one cut between CTAs through a record in the handle's workspace by the
 // CTA that arrives last, in the order of the pieces either way: the result does
 // not depend on timing.  The arrival counters are zero between launches.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kv4.cuh"
 #include "kv4.h"
@@ -44,7 +46,8 @@ namespace {
 
 constexpr int KA_WARPS = 16;
 constexpr int KA_THREADS = KA_WARPS * 32;
-constexpr int KA_RING = 9216;      // ring bytes of a warp: 4 pages at d = 128, 8 at d = 64
+constexpr int KA_PG = 2;           // pages a warp works on at once (a ring stage)
+constexpr int KA_RING = 9216;      // ring bytes of a warp: 2 stages at d = 128, 4 at d = 64
 constexpr int KA_COLS = 8;
 constexpr int KA_FIXED = 2;        // slots a unit costs beside its pages
 constexpr int KA_MIN_QUOTA = 4;    // fewest slots of a warp
@@ -54,12 +57,12 @@ constexpr float KA_SHIFT = 7.f;
 template <int D>
 struct KaLayout {
   static constexpr int SLOT = 18 * D;
-  static constexpr int STAGES = KA_RING / SLOT;
+  static constexpr int STAGES = KA_RING / (KA_PG * SLOT);
   static constexpr int REC = KA_COLS * D + 2 * KA_COLS;  // floats: O [column][d], m, l
   static constexpr int REC_OFF = KA_WARPS * KA_RING;
   static constexpr int BAR_OFF = REC_OFF + KA_WARPS * REC * 4;
   static constexpr int SMEM = BAR_OFF + KA_WARPS * STAGES * 8;
-  static_assert(KA_RING % SLOT == 0 && REC * 4 <= KA_RING, "a record fits a drained ring");
+  static_assert(KA_RING % (KA_PG * SLOT) == 0 && REC * 4 <= KA_RING, "a record fits a drained ring");
 };
 
 // Page row of operand row r: neighbours (K: the two rows of eight lanes) differ
@@ -107,6 +110,13 @@ __device__ __forceinline__ KaSeq ka_seq(const Kv4AttnArgs& a, int s, bool report
 }
 __device__ __forceinline__ long long ka_slots(const KaSeq& q, int n_kv) {
   return static_cast<long long>(q.pages + KA_FIXED) * q.groups * n_kv;
+}
+
+// a / b for a >= 0, b > 0; a 64-bit division costs several hundred clocks, and
+// slot numbers past 32 bits are rare.
+__device__ __forceinline__ long long udiv(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
   }
   const long long total = s_warp[KA_WARPS];
   const long long n_warps = static_cast<long long>(gridDim.x) * KA_WARPS;
-  const long long quota = max((total + n_warps - 1) / n_warps, static_cast<long long>(KA_MIN_QUOTA));
+  const long long quota = max(udiv(total + n_warps - 1, n_warps), static_cast<long long>(KA_MIN_QUOTA));
   const long long wid = static_cast<long long>(blockIdx.x) * KA_WARPS + warp;
   if (static_cast<long long>(blockIdx.x) * KA_WARPS * quota >= total) return;  // nothing for this CTA
   const long long end = min((wid + 1) * quota, total);
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
       if (++s < a.n_seq) sq = ka_seq<RG>(a, s, false);
       continue;
     }
-    const int k = static_cast<int>((x - base) / per);
+    const int k = static_cast<int>(udiv(x - base, per));
     KaUnit u;
     u.key = base + k * per;
     u.s = s;
@@ -311,23 +321,30 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
         return page;
       };
       int ids = load_ids(0), ids_next = load_ids(32);
-      int issued = 0;
-      auto issue = [&](uint32_t st) {  // the piece's next page into stage st (every lane calls)
+      int issued = 0;  // pages
+      auto issue = [&](uint32_t st) {  // the piece's next pages into stage st (every lane calls)
         if (issued > 0 && (issued & 31) == 0) {
           ids = ids_next;
           ids_next = load_ids(issued + 32);
         }
-        const int page = __shfl_sync(0xffffffffu, ids, issued & 31);
+        int page[KA_PG];
+#pragma unroll
+        for (int i = 0; i < KA_PG; ++i) page[i] = __shfl_sync(0xffffffffu, ids, (issued + i) & 31);
+        const int n = min(KA_PG, npg - issued);
         if (lane == 0) {
-          mbar_arrive_expect_tx(&bar[st], SLOT);
-          bulk_g2s(ring + st * SLOT, a.pool + (static_cast<size_t>(page) * a.n_kv + u.g) * SLOT, SLOT, &bar[st]);
+          mbar_arrive_expect_tx(&bar[st], n * SLOT);
+#pragma unroll
+          for (int i = 0; i < KA_PG; ++i)
+            if (i < n)
+              bulk_g2s(ring + (st * KA_PG + i) * SLOT, a.pool + (static_cast<size_t>(page[i]) * a.n_kv + u.g) * SLOT,
+                       SLOT, &bar[st]);
         }
-        ++issued;
+        issued += n;
       };
       if (lane == 0) fence_proxy_async_smem();  // the previous piece's reads come first
 #pragma unroll
       for (int i = 0; i < STAGES; ++i)
-        if (i < npg) issue((gk + i) % STAGES);
+        if (i * KA_PG < npg) issue((gk + i) % STAGES);
 
       // Q^T as the B operand: column lr, this thread's channels [lc d/4, ..) in
       // pairs 4 j + {0, 1} and 4 j + {2, 3}
@@ -369,22 +386,20 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
       const int kr = pos_of(lr);                       // page row of this thread's K rows kr, kr + 8
       const int va = pos_of(2 * lc), vb = pos_of(2 * lc + 1);
 
-      for (int kp = 0; kp < npg; ++kp) {
-        const uint32_t st = gk % STAGES;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar[st], (gk / STAGES) & 1, a.timeout_ns))) {
-          if (lane == 0)  // what is still in flight lands before shared memory is used again
-            for (int j = kp; j < issued; ++j)
-              mbar_wait(&bar[(gk + j - kp) % STAGES], ((gk + j - kp) / STAGES) & 1, a.timeout_ns);
-          failed = true;
-          break;
-        }
-        const uint8_t* slot = ring + st * SLOT;
-        float sc[4] = {0.f, 0.f, 0.f, 0.f};
-        {
+      const int plim = p1 * KV4_P;  // positions past the piece are another warp's
+
+      // one ring stage: KA_PG pages from position pb on.  EDGE: some column does
+      // not see all of their positions (a request's last pages, a piece's end).
+      auto step = [&](const uint8_t* slot, const int pb, auto edge_) {
+        constexpr bool EDGE = decltype(edge_)::value;
+        float sc[KA_PG][4];
+#pragma unroll
+        for (int p = 0; p < KA_PG; ++p) {
+          const uint8_t* sl = slot + p * SLOT;
           uint32_t ka[KW], kb[KW];
-          lds_words(slot + kr * (D / 2) + lc * (D / 8), ka);
-          lds_words(slot + (kr + 8) * (D / 2) + lc * (D / 8), kb);
-          const uint8_t* ks = slot + 8 * D + kr * (D / 16) + lc * (D / 64);
+          lds_words(sl + kr * (D / 2) + lc * (D / 8), ka);
+          lds_words(sl + (kr + 8) * (D / 2) + lc * (D / 8), kb);
+          const uint8_t* ks = sl + 8 * D + kr * (D / 16) + lc * (D / 64);
           uint32_t sa[D / 64], sb[D / 64];  // scales as f16 pairs, one a 16-channel block
           if (D == 128) {
             const uint32_t ra = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks));
@@ -394,41 +409,44 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
             sb[0] = __byte_perm(rb, rb, 0x1010);
             sb[D / 64 - 1] = __byte_perm(rb, rb, 0x3232);
           } else {
-            const uint32_t both = e4m3x2_to_f16x2(ks[0] | (static_cast<uint32_t>(ks[8 * (D / 16)]) << 8));
+            const uint32_t both = e4m3x2_to_f16x2(__byte_perm(ks[0], ks[8 * (D / 16)], 0x0040));
             sa[0] = __byte_perm(both, both, 0x1010);
             sb[0] = __byte_perm(both, both, 0x3232);
           }
-          float s2[4] = {0.f, 0.f, 0.f, 0.f};
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < KS; ++j) {
             const uint32_t fa = sa[j / 4], fb = sb[j / 4];
-            const uint32_t a0 = hmul2_u(code_pair(ka, 2 * j), fa), a2 = hmul2_u(code_pair(ka, 2 * j + 1), fa);
-            const uint32_t a1 = hmul2_u(code_pair(kb, 2 * j), fb), a3 = hmul2_u(code_pair(kb, 2 * j + 1), fb);
-            if (j & 1) mma_f16(s2, a0, a1, a2, a3, qb[j][0], qb[j][1]);
-            else mma_f16(sc, a0, a1, a2, a3, qb[j][0], qb[j][1]);
+            mma_f16(acc, hmul2_u(code_pair(ka, 2 * j), fa), hmul2_u(code_pair(kb, 2 * j), fb),
+                    hmul2_u(code_pair(ka, 2 * j + 1), fa), hmul2_u(code_pair(kb, 2 * j + 1), fb), qb[j][0], qb[j][1]);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[i] = (sc[i] + s2[i]) * ((i & 1) ? sc1 : sc0);
+          for (int i = 0; i < 4; ++i) sc[p][i] = acc[i] * ((i & 1) ? sc1 : sc0);
         }
         // scaled scores, base 2: (position kr, h0), (kr, h1), (kr + 8, h0), (kr + 8, h1)
-        const int pb = (p0 + kp) * KV4_P;
-        const bool edge = pb + KV4_P > u.len;  // warp-uniform: some column sees less than the page
-        bool bad0 = false, bad1 = false;       // NaN values of V at the two positions
-        if (edge) {
-          sc[0] = pb + kr < lim0 ? sc[0] : -INFINITY;
-          sc[1] = pb + kr < lim1 ? sc[1] : -INFINITY;
-          sc[2] = pb + kr + 8 < lim0 ? sc[2] : -INFINITY;
-          sc[3] = pb + kr + 8 < lim1 ? sc[3] : -INFINITY;
-          // A NaN there must reach the columns that see it and no other, so it
+        unsigned bad = 0;  // NaN values of V at this thread's positions: bit 2 page + half
+        if (EDGE) {
+          // A NaN of V must reach the columns that see it and no other, so it
           // goes through P instead of V (0 * NaN is NaN).
-          const uint8_t* vs = slot + 17 * D + kr * (D / 16);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            bad0 |= scale_nan(vs[i]);
-            bad1 |= scale_nan(vs[8 * (D / 16) + i]);
-          }
+          for (int p = 0; p < KA_PG; ++p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int pos = pb + p * KV4_P + kr + 8 * i;
+              if (pos >= min(lim0, plim)) sc[p][2 * i] = -INFINITY;
+              if (pos >= min(lim1, plim)) sc[p][2 * i + 1] = -INFINITY;
+              const uint8_t* vs = slot + p * SLOT + 17 * D + (kr + 8 * i) * (D / 16);
+#pragma unroll
+              for (int b = 0; b < D / 16; ++b)
+                if (scale_nan(vs[b])) bad |= 1u << (2 * p + i);
+            }
         }
-        const float x0 = fmaxf(sc[0], sc[2]), x1 = fmaxf(sc[1], sc[3]);
+        float x0 = fmaxf(sc[0][0], sc[0][2]), x1 = fmaxf(sc[0][1], sc[0][3]);
+#pragma unroll
+        for (int p = 1; p < KA_PG; ++p) {
+          x0 = fmaxf(x0, fmaxf(sc[p][0], sc[p][2]));
+          x1 = fmaxf(x1, fmaxf(sc[p][1], sc[p][3]));
+        }
         if (__any_sync(0xffffffffu, x0 > m0 + KA_LAZY || x1 > m1 + KA_LAZY)) {
           float y0 = x0, y1 = x1;
 #pragma unroll
@@ -454,51 +472,85 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
           n0 = m0 == -INFINITY ? KA_SHIFT : KA_SHIFT - m0;
           n1 = m1 == -INFINITY ? KA_SHIFT : KA_SHIFT - m1;
         }
-        // the scaled scores are rounded before the maximum is taken off (no fused
-        // step), so that the largest is at most 2^8 of it at any magnitude
-        float e0 = ex2_approx(sc[0] + n0), e1 = ex2_approx(sc[1] + n1);
-        float e2 = ex2_approx(sc[2] + n0), e3 = ex2_approx(sc[3] + n1);
-        if (edge) {
-          const float nan = __int_as_float(0x7FC00000);
-          if (bad0 && pb + kr < lim0) e0 = nan;
-          if (bad0 && pb + kr < lim1) e1 = nan;
-          if (bad1 && pb + kr + 8 < lim0) e2 = nan;
-          if (bad1 && pb + kr + 8 < lim1) e3 = nan;
+        uint32_t pt[KA_PG][2];
+#pragma unroll
+        for (int p = 0; p < KA_PG; ++p) {
+          // the scaled scores are rounded before the maximum is taken off (no fused
+          // step), so that the largest is at most 2^8 of it at any magnitude
+          float e0 = ex2_approx(sc[p][0] + n0), e1 = ex2_approx(sc[p][1] + n1);
+          float e2 = ex2_approx(sc[p][2] + n0), e3 = ex2_approx(sc[p][3] + n1);
+          if (EDGE && bad) {
+            const float nan = __int_as_float(0x7FC00000);
+            const int pos = pb + p * KV4_P + kr;
+            if ((bad >> (2 * p)) & 1) {
+              if (pos < min(lim0, plim)) e0 = nan;
+              if (pos < min(lim1, plim)) e1 = nan;
+            }
+            if ((bad >> (2 * p + 1)) & 1) {
+              if (pos + 8 < min(lim0, plim)) e2 = nan;
+              if (pos + 8 < min(lim1, plim)) e3 = nan;
+            }
+          }
+          l0 += e0 + e2;
+          l1 += e1 + e3;
+          pt[p][0] = movmatrix_trans(pack_f16(e0, e1));  // positions 2 lc (+1), column lr
+          pt[p][1] = movmatrix_trans(pack_f16(e2, e3));  // and 8 on
         }
-        l0 += e0 + e2;
-        l1 += e1 + e3;
-        const uint32_t pb0 = movmatrix_trans(pack_f16(e0, e1));  // positions 2 lc (+1), column lr
-        const uint32_t pb1 = movmatrix_trans(pack_f16(e2, e3));  // and 8 on
-        {
-          const uint8_t* v = slot + 9 * D + lr * (D / 16);
+#pragma unroll
+        for (int p = 0; p < KA_PG; ++p) {
+          const uint8_t* v = slot + p * SLOT + 9 * D + lr * (D / 16);
           uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
           lds_words(v + va * (D / 2), v0);
           lds_words(v + vb * (D / 2), v1);
           lds_words(v + (va + 8) * (D / 2), v2);
           lds_words(v + (vb + 8) * (D / 2), v3);
-          const uint8_t* vs = slot + 17 * D + (lr * (D / 8)) / 16;
+          const uint8_t* vs = slot + p * SLOT + 17 * D + (lr * (D / 8)) / 16;
           uint32_t b0 = vs[va * (D / 16)], b1 = vs[vb * (D / 16)];
           uint32_t b2 = vs[(va + 8) * (D / 16)], b3 = vs[(vb + 8) * (D / 16)];
-          if (edge) {  // positions no column sees, and NaNs (P has them): nothing
-            if (pb + va >= most || scale_nan(b0)) b0 = 0;
-            if (pb + vb >= most || scale_nan(b1)) b1 = 0;
-            if (pb + va + 8 >= most || scale_nan(b2)) b2 = 0;
-            if (pb + vb + 8 >= most || scale_nan(b3)) b3 = 0;
+          if (EDGE) {  // positions no column sees, and NaNs (P has them): nothing
+            const int pos = pb + p * KV4_P, lim = min(most, plim);
+            if (pos + va >= lim || scale_nan(b0)) b0 = 0;
+            if (pos + vb >= lim || scale_nan(b1)) b1 = 0;
+            if (pos + va + 8 >= lim || scale_nan(b2)) b2 = 0;
+            if (pos + vb + 8 >= lim || scale_nan(b3)) b3 = 0;
           }
-          const uint32_t f01 = e4m3x2_to_f16x2(b0 | (b1 << 8)), f23 = e4m3x2_to_f16x2(b2 | (b3 << 8));
+          const uint32_t f01 = e4m3x2_to_f16x2(__byte_perm(b0, b1, 0x0040));
+          const uint32_t f23 = e4m3x2_to_f16x2(__byte_perm(b2, b3, 0x0040));
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
             const uint32_t c0 = code_pair(v0, i), c1 = code_pair(v1, i);
             const uint32_t c2 = code_pair(v2, i), c3 = code_pair(v3, i);
             mma_f16(o[i], hmul2_u(__byte_perm(c0, c1, 0x5410), f01), hmul2_u(__byte_perm(c0, c1, 0x7632), f01),
-                    hmul2_u(__byte_perm(c2, c3, 0x5410), f23), hmul2_u(__byte_perm(c2, c3, 0x7632), f23), pb0, pb1);
+                    hmul2_u(__byte_perm(c2, c3, 0x5410), f23), hmul2_u(__byte_perm(c2, c3, 0x7632), f23), pt[p][0], pt[p][1]);
           }
         }
+      };
+      uint32_t st = gk % STAGES, ph = (gk / STAGES) & 1;
+      for (int kp = 0; kp < npg; kp += KA_PG) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar[st], ph, a.timeout_ns))) {
+          if (lane == 0)  // what is still in flight lands before shared memory is used again
+            for (int j = kp; j < issued; j += KA_PG) {
+              mbar_wait(&bar[st], ph, a.timeout_ns);
+              if (++st == STAGES) {
+                st = 0;
+                ph ^= 1;
+              }
+            }
+          failed = true;
+          break;
+        }
+        const int pb = (p0 + kp) * KV4_P;
+        if (pb + KA_PG * KV4_P <= min(u.len, plim)) step(ring + st * (KA_PG * SLOT), pb, std::false_type{});
+        else step(ring + st * (KA_PG * SLOT), pb, std::true_type{});
         ++gk;
         __syncwarp();
         if (issued < npg) {
           if (lane == 0) fence_proxy_async_smem();
           issue(st);
+        }
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
         }
       }
     }
@@ -551,81 +603,125 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
   }
   __syncthreads();
 
-  // ---- join the pieces of the CTA's warps: entries 2 w + (0 head, 1 tail), a
-  // unit's pieces stand next to one another
+  // ---- join the pieces of the CTA's warps.  Entry 2 w is the head piece of
+  // warp w, 2 w + 1 its tail: a unit's pieces stand next to one another.  A warp
+  // takes a column of a run of pieces at a time.
+  const KaUnit* piece = &s_piece[0][0];
   auto rec_of = [&](int e) {
     return reinterpret_cast<const float*>((e & 1) ? smem + (e >> 1) * KA_RING
                                                   : smem + Lay::REC_OFF + (e >> 1) * Lay::REC * 4);
   };
-  auto key_of = [&](int e) { return s_piece[e >> 1][e & 1].key; };
-  for (int e = 0; e < 2 * KA_WARPS;) {
-    const long long key = key_of(e);
-    if (key < 0) {
-      ++e;
-      continue;
-    }
-    int e1 = e + 1;
-    while (e1 < 2 * KA_WARPS && (key_of(e1) < 0 || key_of(e1) == key)) ++e1;
-    const KaUnit u = s_piece[e >> 1][e & 1];
-    const int first = static_cast<int>((key + KA_FIXED) / quota / KA_WARPS);
-    const int last = static_cast<int>((key + KA_FIXED + u.pages - 1) / quota / KA_WARPS);
+  const long long my_key = lane < 2 * KA_WARPS ? piece[lane].key : -1;
+  const unsigned valid = __ballot_sync(0xffffffffu, my_key >= 0);
+  const unsigned before = valid & ((1u << lane) - 1);
+  const long long prev = __shfl_sync(0xffffffffu, my_key, before ? 31 - __clz(before) : lane);
+  const unsigned starts = __ballot_sync(0xffffffffu, my_key >= 0 && (!before || prev != my_key));
+  const long long cta_begin = static_cast<long long>(blockIdx.x) * KA_WARPS * quota;
+  const long long cta_end = cta_begin + KA_WARPS * quota;
+  // the pages of a unit start, end in this CTA's slots
+  auto starts_here = [&](const KaUnit& u) { return u.key + KA_FIXED >= cta_begin; };
+  auto ends_here = [&](const KaUnit& u) { return u.key + KA_FIXED + u.pages <= cta_end; };
+  constexpr int V = D / 32;  // floats of a lane
+  int run = 0;
+  for (unsigned left = starts; left; left &= left - 1, ++run) {
+    const int e = __ffs(left) - 1;
+    const unsigned more = left & (left - 1);
+    const unsigned mine = valid & ~((1u << e) - 1) & (more ? (1u << (__ffs(more) - 1)) - 1 : ~0u);
+    const KaUnit& u = piece[e];
+    const bool from = starts_here(u), here = from && ends_here(u);
     const int cols = u.rows * GRP;
-    const bool here = first == last;
-    float* out = a.records + (static_cast<size_t>(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == first ? 1 : 0)) * Lay::REC;
-    for (int i = tid; i < cols * D; i += KA_THREADS) {
-      const int col = i / D, ch = i % D;
-      float M = -INFINITY, L = 0.f, O = 0.f;
-      for (int j = e; j < e1; ++j)
-        if (key_of(j) >= 0) M = fmaxf(M, rec_of(j)[KA_COLS * D + col]);
-      for (int j = e; j < e1; ++j)
-        if (key_of(j) >= 0) {
-          const float* r = rec_of(j);
-          const float mj = r[KA_COLS * D + col];
-          const float w = mj == -INFINITY ? 0.f : exp2f(mj - M);
-          L += mj == -INFINITY ? r[KA_COLS * D + KA_COLS + col] : w * r[KA_COLS * D + KA_COLS + col];
-          O += mj == -INFINITY ? r[i] : w * r[i];
-        }
+    for (int col = (warp + KA_WARPS - (run * KA_COLS) % KA_WARPS) % KA_WARPS; col < cols; col += KA_WARPS) {
+      float M = -INFINITY, L = 0.f, O[V] = {};
+      for (unsigned b = mine; b; b &= b - 1) M = fmaxf(M, rec_of(__ffs(b) - 1)[KA_COLS * D + col]);
+      for (unsigned b = mine; b; b &= b - 1) {
+        const float* r = rec_of(__ffs(b) - 1);
+        const float mj = r[KA_COLS * D + col];
+        const float w = mj == -INFINITY ? 1.f : exp2f(mj - M);  // a piece that saw nothing holds zeros (or NaN)
+        L = fmaf(w, r[KA_COLS * D + KA_COLS + col], L);
+#pragma unroll
+        for (int i = 0; i < V; ++i) O[i] = fmaf(w, r[col * D + lane * V + i], O[i]);
+      }
       if (here) {
-        a.o[(static_cast<size_t>(u.row0 + col / GRP) * a.n_q + u.g * GRP + col % GRP) * D + ch] =
-            __float2bfloat16_rn(L == 0.f ? 0.f : O / L * a.v_scale);
+        const float inv = L == 0.f ? 0.f : a.v_scale / L;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(
+            a.o + (static_cast<size_t>(u.row0 + col / GRP) * a.n_q + u.g * GRP + col % GRP) * D + lane * V);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) dst[i] = pack_bf16(O[2 * i] * inv, O[2 * i + 1] * inv);
       } else {
-        out[i] = O;
-        if (ch == 0) {
+        float* out = a.records + (static_cast<size_t>(blockIdx.x) * 2 + (from ? 1 : 0)) * Lay::REC;
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[col * D + lane * V + i] = O[i];
+        if (lane == 0) {
           out[KA_COLS * D + col] = M;
           out[KA_COLS * D + KA_COLS + col] = L;
         }
       }
     }
-    if (!here) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int n = last - first + 1;
-        s_last = atomicAdd(&a.counters[first], 1) == n - 1;
-        if (s_last) a.counters[first] = 0;  // as the next launch expects it
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        auto part = [&](int b) { return a.records + (static_cast<size_t>(b) * 2 + (b == first ? 1 : 0)) * Lay::REC; };
-        for (int i = tid; i < cols * D; i += KA_THREADS) {
-          const int col = i / D, ch = i % D;
-          float M = -INFINITY, L = 0.f, O = 0.f;
-          for (int b = first; b <= last; ++b) M = fmaxf(M, __ldcg(part(b) + KA_COLS * D + col));
-          for (int b = first; b <= last; ++b) {
-            const float* r = part(b);
-            const float mj = __ldcg(r + KA_COLS * D + col);
-            const float w = mj == -INFINITY ? 1.f : exp2f(mj - M);
-            L += w * __ldcg(r + KA_COLS * D + KA_COLS + col);
-            O += w * __ldcg(r + i);
-          }
-          a.o[(static_cast<size_t>(u.row0 + col / GRP) * a.n_q + u.g * GRP + col % GRP) * D + ch] =
-              __float2bfloat16_rn(L == 0.f ? 0.f : O / L * a.v_scale);
-        }
-      }
-      __syncthreads();
+  }
+
+  // ---- units cut between CTAs: at most the first and the last run
+  __threadfence();
+  __syncthreads();
+  if (starts == 0) return;
+  const int e_first = __ffs(starts) - 1, e_last = 31 - __clz(starts);
+  for (int k = 0; k < 2; ++k) {
+    if (k == 1 && e_last == e_first) break;
+    const KaUnit& u = piece[k == 0 ? e_first : e_last];
+    if (starts_here(u) && ends_here(u)) continue;
+    const int first = static_cast<int>(udiv(u.key + KA_FIXED, quota * KA_WARPS));
+    const int last = static_cast<int>(udiv(u.key + KA_FIXED + u.pages - 1, quota * KA_WARPS));
+    if (tid == 0) {
+      s_last = atomicAdd(&a.counters[first], 1) == last - first;
+      if (s_last) a.counters[first] = 0;  // as the next launch expects it
     }
-    e = e1;
+    __syncthreads();
+    if (s_last) {
+      __threadfence();
+      const int cols = u.rows * GRP, n = last - first + 1;
+      auto part = [&](int b) { return a.records + (static_cast<size_t>(first + b) * 2 + (b == 0 ? 1 : 0)) * Lay::REC; };
+      // the ring is free: weights [column][n], then 1 / denominators
+      float* w = reinterpret_cast<float*>(smem);
+      float* inv = w + KA_COLS * gridDim.x;
+      for (int col = warp; col < cols; col += KA_WARPS) {
+        float M = -INFINITY;
+        for (int b = lane; b < n; b += 32) M = fmaxf(M, w[col * n + b] = __ldcg(part(b) + KA_COLS * D + col));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        float L = 0.f;
+        for (int b = lane; b < n; b += 32) {
+          const float x = w[col * n + b] == -INFINITY ? 1.f : exp2f(w[col * n + b] - M);
+          w[col * n + b] = x;
+          L = fmaf(x, __ldcg(part(b) + KA_COLS * D + KA_COLS + col), L);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+        if (lane == 0) inv[col] = L == 0.f ? 0.f : a.v_scale / L;
+      }
+      __syncthreads();
+      for (int i = tid; i < cols * D / 4; i += KA_THREADS) {
+        const int col = i * 4 / D;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b0 = 0; b0 < n; b0 += 8) {  // 8 loads in flight
+          float4 x[8];
+#pragma unroll
+          for (int b = 0; b < 8; ++b) x[b] = __ldcg(reinterpret_cast<const float4*>(part(min(b0 + b, n - 1))) + i);
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+            if (b0 + b < n) {
+              const float wb = w[col * n + b0 + b];
+              O.x = fmaf(wb, x[b].x, O.x);
+              O.y = fmaf(wb, x[b].y, O.y);
+              O.z = fmaf(wb, x[b].z, O.z);
+              O.w = fmaf(wb, x[b].w, O.w);
+            }
+        }
+        const float s1 = inv[col];
+        const int ch = i * 4 % D;
+        *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(u.row0 + col / GRP) * a.n_q + u.g * GRP + col % GRP) * D + ch) =
+            make_uint2(pack_bf16(O.x * s1, O.y * s1), pack_bf16(O.z * s1, O.w * s1));
+      }
+    }
+    __syncthreads();
   }
 }
 
