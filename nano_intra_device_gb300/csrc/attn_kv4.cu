@@ -44,7 +44,7 @@
 namespace nf {
 namespace {
 
-constexpr int KA_WARPS = 16;
+constexpr int KA_WARPS = 12;
 constexpr int KA_THREADS = KA_WARPS * 32;
 constexpr int KA_COLS = 8;
 constexpr int KA_STAGES = 2;       // ring stages of a warp
@@ -87,7 +87,7 @@ struct __align__(16) KaPiece {
 };
 constexpr uint32_t KA_NONE = ~0u;
 
-// Rows, visible length and pages of request s (0 rows: not ours).
+// Rows, visible length, pages and column groups of request s (0 groups: not ours).
 struct KaSeq {
   int b0, rows, len, pages, groups;
 };
@@ -112,7 +112,7 @@ __device__ __forceinline__ KaSeq ka_seq(const Kv4AttnArgs& a, int s, bool report
     q.len = 0;
   }
   q.pages = (q.len + KV4_P - 1) / KV4_P;
-  q.groups = (q.rows + RG - 1) / RG;
+  q.groups = q.rows > a.small_rows ? 0 : (q.rows + RG - 1) / RG;
   return q;
 }
 __device__ __forceinline__ long long ka_slots(const KaSeq& q, int n_kv) {
@@ -130,6 +130,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// the same with nothing to add to
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 template <int B>
 __device__ __forceinline__ uint32_t code_pair(const uint32_t (&w)[B], int i) {
@@ -453,10 +461,13 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
           sa = e4m3x2_to_f16x2(my_ks[at_p]);
           sb = e4m3x2_to_f16x2(my_ks[at_p + 8 * (D / 16)]);
         }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4];
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
-          if (j < 4)
+          if (j == 0)
+            mma_f16_zero(acc, hmul2_half<0>(code_pair(ka, 0), sa), hmul2_half<0>(code_pair(kb, 0), sb),
+                         hmul2_half<0>(code_pair(ka, 1), sa), hmul2_half<0>(code_pair(kb, 1), sb), qb[0][0], qb[0][1]);
+          else if (j < 4)
             mma_f16(acc, hmul2_half<0>(code_pair(ka, 2 * j), sa), hmul2_half<0>(code_pair(kb, 2 * j), sb),
                     hmul2_half<0>(code_pair(ka, 2 * j + 1), sa), hmul2_half<0>(code_pair(kb, 2 * j + 1), sb), qb[j][0], qb[j][1]);
           else

@@ -1,0 +1,776 @@
+// Causal attention of the rows of longer chunks over the 4-bit KV cache, on the
+// 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
+//
+// A tile is 128 query vectors: 128 / GRP consecutive rows of one request and the
+// GRP query heads of one KV head.  Per key block of 128 positions
+//   S = Q K^T   (M 128, N 128, K d),   O += P V   (M 128, N d, K 128),
+// both with fp16 operands and fp32 accumulators.
+//  * Four warps turn codes into fp16 operands: a lane loads half a row of a page
+//    (a scale for every 16 channels), converts a byte an instruction, multiplies
+//    by the scale (exact, see attn_kv4.cu) and stores 16-byte chunks in the
+//    128-byte swizzle the products read; K has a ring of its own, V another.
+//    The next block's codes are in registers while the ring is full.
+//  * One thread issues the products.  S of the next block runs while the softmax
+//    of this one does.
+//  * Eight warps own half a vector each: online softmax with a lazily raised
+//    maximum (base 2), P written as fp16 of 2^7 times its share of the running
+//    maximum, denominators summed in fp32.
+// Q is scaled by a power of two a vector so that fp16 holds all of bf16's bits.
+//
+// Work split: the key blocks of all (tile, KV head) units are laid end to end
+// (closed-form sums, as a tile's blocks grow with its position) and every CTA
+// takes the same number.  A unit cut between CTAs is joined by the CTA that
+// arrives last, from fp32 records in the handle's workspace, in the order of the
+// pieces.  So a short chunk over a long prefix fills the GPU like a long prompt.
+// The rings run on over the ends of units.
+//
+// Every wait is bounded; on expiry the kernel flags ST_TIMEOUT, every role
+// leaves its loop, and the products issued finish before tensor memory is freed.
+#include "common.cuh"
+#include "kv4.cuh"
+#include "kv4.h"
+#include "mma_frag.cuh"
+
+namespace nf {
+namespace {
+
+constexpr int KP_DQ_WARPS = 4;       // warps that make operands: two for K, two for V
+constexpr int KP_SM_WARPS = 8;       // softmax warps: two per tensor-memory lane quarter
+constexpr int KP_MMA_WARP = KP_DQ_WARPS + KP_SM_WARPS;
+constexpr int KP_WARPS = 16;         // registers are dealt by warpgroups of four: the last holds the
+                                     // MMA warp and three that only take part in the prologue
+constexpr int KP_THREADS = KP_WARPS * 32;
+// 512 = 4 x 128 registers a thread at launch, dealt again by role
+constexpr int KP_DQ_REGS = 112, KP_SM_REGS = 160, KP_MMA_REGS = 80;
+static_assert(KP_DQ_REGS + 2 * KP_SM_REGS + KP_MMA_REGS == 512, "the shares of the launch's registers");
+constexpr int KP_SM_THREADS = KP_SM_WARPS * 32;
+constexpr int KP_M = 128;            // query vectors of a tile (tensor-memory lanes)
+constexpr int KP_N = 128;            // positions of a key block
+constexpr int KP_H = KP_N / 2;       // positions of a block one softmax thread owns
+constexpr int KP_REGION = 128 * 128; // 128 rows x 128 bytes: 64 fp16 columns of 128 rows
+constexpr int KP_FIXED = 1;          // blocks' worth of a unit's fixed cost
+constexpr float KP_SLACK = 8.f;
+constexpr float KP_SHIFT = 7.f;
+constexpr uint32_t KP_TMEM_COLS = 512;
+constexpr int KP_KST = 2, KP_VST = 2;  // ring stages of K and V
+
+struct KpBars {
+  uint64_t q_full;                           // KP_SM_THREADS arrivals: Q of a piece written
+  uint64_t k_full[KP_KST], k_empty[KP_KST];  // full: 64 arrivals (two warps)
+  uint64_t v_full[KP_VST], v_empty[KP_VST];
+  uint64_t s_full[2], s_free[2];             // S accumulators (free: KP_SM_THREADS arrivals)
+  uint64_t p_full;                           // KP_SM_THREADS arrivals: P written (and O rescaled)
+  uint64_t p_free;                           // a PV product finished
+  uint64_t drain;
+  uint64_t meet;                             // KP_SM_THREADS arrivals: the softmax threads
+  uint32_t tmem_base;
+  int abort, last;
+  uint32_t v_nan[KP_VST][4];                 // positions whose V holds a NaN that not every row sees
+  float xch[2][KP_M];                        // the two halves of a row exchange their sums
+  long long warp_sum[KP_WARPS];
+  long long base;                            // where this CTA starts: a request's first slot
+  int seq;                                   // and the request
+};
+
+template <int NCH>
+struct KpLayout {
+  static constexpr int D = NCH * 64;
+  static constexpr int Q_BYTES = NCH * KP_REGION;   // [d/64][128 vectors][128 B]
+  static constexpr int KV_BYTES = NCH * KP_REGION;  // 16 groups of 8 positions, each [d/64][8][128 B]
+  static constexpr int KV_GROUP = NCH * 1024;
+  static constexpr int P_BYTES = 2 * KP_REGION;     // [keys/64][128 vectors][128 B]
+  static constexpr int K_OFF = Q_BYTES;
+  static constexpr int V_OFF = K_OFF + KP_KST * KV_BYTES;
+  static constexpr int P_OFF = V_OFF + KP_VST * KV_BYTES;
+  static constexpr int BAR_OFF = P_OFF + P_BYTES;
+  static constexpr int SMEM = 1024 + BAR_OFF + static_cast<int>(sizeof(KpBars));
+  static constexpr int REC = KP_M * D + 2 * KP_M;   // floats of a record: O, m, l
+};
+
+__device__ __forceinline__ uint32_t kp_sw128(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void kp_st16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t kp_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void kp_regs_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void kp_regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float kp_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 D; B K-major or MN-major.
+constexpr uint32_t kp_idesc(int M, int N, bool b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24) | (b_mn ? 1u << 16 : 0u);
+}
+
+// Blocks of the tile whose last row's limit is k steps of R = 128 / g positions
+// (at least one), and their sum over 1 .. m (m <= 0: minus one a step).
+__device__ __forceinline__ long long kp_blocks(long long k, int g) { return k <= 0 ? 1 : (k + g - 1) / g; }
+__device__ __forceinline__ long long kp_sum(long long m, int g) {
+  if (m <= 0) return m;
+  const long long q = m / g, r = m % g;
+  return g * q * (q + 1) / 2 + r * (q + 1);
+}
+
+struct KpSeq {
+  int b0, rows, len, tiles;
+  long long c;  // steps of R up to the last row of tile 0
+};
+template <int GRP>
+__device__ __forceinline__ KpSeq kp_seq(const Kv4AttnArgs& a, int s) {
+  constexpr int R = KP_M / GRP;
+  KpSeq q;
+  const int b0 = a.tok_begin[s], b1 = a.tok_begin[s + 1];
+  q.b0 = b0;
+  q.rows = b0 < 0 || b1 < b0 || b1 > a.n_tok ? 0 : b1 - b0;
+  q.len = a.seq_lens[s];
+  if (q.len < 0 || q.len > static_cast<long long>(a.max_pages) * KV4_P) q.len = 0;
+  q.tiles = q.rows > a.small_rows ? (q.rows + R - 1) / R : 0;
+  const int first = q.len - q.rows;  // position of the first row
+  q.c = (first >= 0 ? (first + R - 1) / R : -(-first / R)) + 1;
+  return q;
+}
+// Slots before tile i of a request.
+template <int GRP>
+__device__ __forceinline__ long long kp_before(const KpSeq& q, int i, int n_kv) {
+  return n_kv * (kp_sum(q.c + i - 1, GRP) - kp_sum(q.c - 1, GRP) + static_cast<long long>(i) * KP_FIXED);
+}
+
+struct KpPiece {
+  long long key;      // the unit's first slot
+  int s, g;
+  int row0, rows;     // rows of q and o
+  int pos0;           // position of row0 (may be negative)
+  int len;            // positions of the request
+  int nb, j0, j1;     // blocks of the unit, and those of this piece
+};
+
+// Walks the pieces of a CTA's slots; every warp keeps one.
+template <int GRP>
+struct KpWalk {
+  long long x, end, base;
+  int s;
+  KpSeq q;
+  __device__ __forceinline__ bool next(const Kv4AttnArgs& a, KpPiece& p) {
+    constexpr int R = KP_M / GRP;
+    while (x < end) {
+      const long long all = kp_before<GRP>(q, q.tiles, a.n_kv);
+      if (x >= base + all) {
+        base += all;
+        if (++s >= a.n_seq) return false;
+        q = kp_seq<GRP>(a, s);
+        continue;
+      }
+      int lo = 0, hi = q.tiles - 1;  // the last tile that starts at or before x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (base + kp_before<GRP>(q, mid, a.n_kv) <= x) lo = mid;
+        else hi = mid - 1;
+      }
+      const long long t0 = base + kp_before<GRP>(q, lo, a.n_kv);
+      p.nb = static_cast<int>(kp_blocks(q.c + lo, GRP));
+      const int per = p.nb + KP_FIXED;
+      p.g = static_cast<int>((x - t0) / per);
+      p.key = t0 + static_cast<long long>(p.g) * per;
+      p.s = s;
+      p.row0 = q.b0 + lo * R;
+      p.rows = min(R, q.rows - lo * R);
+      p.pos0 = q.len - q.rows + lo * R;
+      p.len = q.len;
+      const int off = static_cast<int>(x - p.key);
+      p.j0 = max(off - KP_FIXED, 0);
+      p.j1 = static_cast<int>(min(end - p.key, static_cast<long long>(per))) - KP_FIXED;
+      x = min(end, p.key + per);
+      if (p.j1 > p.j0) return true;
+    }
+    return false;
+  }
+};
+
+template <int GRP, int NCH>
+__global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const Kv4AttnArgs a) {
+  using Lay = KpLayout<NCH>;
+  constexpr int D = Lay::D;
+  constexpr uint32_t IDESC_S = kp_idesc(KP_M, KP_N, false);
+  constexpr uint32_t IDESC_PV = kp_idesc(KP_M, D, true);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t sbase = smem_u32(smem);
+  KpBars* bars = reinterpret_cast<KpBars*>(smem + Lay::BAR_OFF);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t tmo = a.timeout_ns;
+
+  // ---- the slots of every request: thread i sums the requests [i c, (i + 1) c)
+  KpWalk<GRP> walk;
+  long long quota;
+  {
+    const int c = (a.n_seq + KP_THREADS - 1) / KP_THREADS;
+    const int s0 = min(static_cast<long long>(a.n_seq), static_cast<long long>(tid) * c), s1 = min(a.n_seq, s0 + c);
+    long long sum = 0;
+    for (int s = s0; s < s1; ++s) {
+      const KpSeq q = kp_seq<GRP>(a, s);
+      sum += kp_before<GRP>(q, q.tiles, a.n_kv);
+    }
+    long long in = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += y;
+    }
+    if (lane == 31) bars->warp_sum[warp] = in;
+    __syncthreads();
+    long long at = in - sum, total = 0;
+    for (int w = 0; w < KP_WARPS; ++w) {
+      if (w < warp) at += bars->warp_sum[w];
+      total += bars->warp_sum[w];
+    }
+    quota = (total + gridDim.x - 1) / gridDim.x;
+    const long long x = blockIdx.x * quota;
+    if (x >= total) return;  // nothing for this CTA
+    if (at <= x && x < at + sum)
+      for (int s = s0; s < s1; ++s) {
+        const KpSeq q = kp_seq<GRP>(a, s);
+        const long long n = kp_before<GRP>(q, q.tiles, a.n_kv);
+        if (x < at + n) {
+          bars->base = at;
+          bars->seq = s;
+          break;
+        }
+        at += n;
+      }
+    walk.x = x;
+    walk.end = min(x + quota, total);
+  }
+
+  if (tid == 0) {
+    mbar_init(&bars->q_full, KP_SM_THREADS);
+    for (int i = 0; i < KP_KST; ++i) {
+      mbar_init(&bars->k_full[i], 64);
+      mbar_init(&bars->k_empty[i], 1);
+    }
+    for (int i = 0; i < KP_VST; ++i) {
+      mbar_init(&bars->v_full[i], 64);
+      mbar_init(&bars->v_empty[i], 1);
+      for (int k = 0; k < 4; ++k) bars->v_nan[i][k] = 0;
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_free[i], KP_SM_THREADS);
+    }
+    mbar_init(&bars->p_full, KP_SM_THREADS);
+    mbar_init(&bars->p_free, 1);
+    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->meet, KP_SM_THREADS);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == KP_MMA_WARP) {
+    tmem_alloc(&bars->tmem_base, KP_TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;  // columns [0, 256): S x 2; [256, 256 + d): O
+  walk.base = bars->base;
+  walk.s = bars->seq;
+  walk.q = kp_seq<GRP>(a, walk.s);
+  volatile int* abort_flag = &bars->abort;
+  auto give_up = [&]() {
+    raise_status(a.status, ST_TIMEOUT);
+    *abort_flag = 1;
+  };
+  KpPiece p;
+
+  if (warp < KP_DQ_WARPS) {
+    kp_regs_less<KP_DQ_REGS>();
+    // ------------------------------------------------------ operands from codes
+    // Warps 0, 1: K; 2, 3: V; each four of a block's eight pages.  Lane: half
+    // `hf` of page row `prow`; at d = 128 the second half's chunks go in the
+    // order 4 .. 7, 0 .. 3, so that eight lanes' stores hit all banks.
+    const bool is_k = warp < 2;
+    uint64_t* full = is_k ? bars->k_full : bars->v_full;
+    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+    const int nst = is_k ? KP_KST : KP_VST;
+    const uint32_t ring = sbase + (is_k ? Lay::K_OFF : Lay::V_OFF);
+    const int prow = lane >> 1, hf = lane & 1, page0 = (warp & 1) * 4;
+    constexpr int CW = D / 16;  // code words of a lane and page, one an 8-channel chunk
+    const int part = is_k ? 0 : 9 * D;
+    const int code_off = part + prow * (D / 2) + hf * (D / 4);
+    const int scale_off = part + 8 * D + prow * (D / 16) + hf * (D / 32);
+    uint32_t w[4][CW], sc[4];  // codes and scale bytes of four pages
+    uint32_t nan_bits = 0;     // V: pages whose row here holds a hidden-from-some NaN
+    auto load = [&](const KpPiece& u, int j) {  // block j of unit u
+      const int* bt = a.block_table + static_cast<size_t>(u.s) * a.max_pages;
+      const int npages = (u.len + KV4_P - 1) / KV4_P;
+      const int last = min(u.len, u.pos0 + u.rows) - 1;  // the tile's last visible position
+      int page = -1;
+      if (lane < 4 && j * 8 + page0 + lane < npages) {
+        page = bt[j * 8 + page0 + lane];
+        if (page < 0 || page >= a.num_pages) {  // never read outside the pool
+          raise_status(a.status, ST_BAD_PAGE);
+          page = 0;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int id = __shfl_sync(0xffffffffu, page, i);
+#pragma unroll
+        for (int k = 0; k < CW; ++k) w[i][k] = 0;
+        sc[i] = 0;
+        const int pos = j * KP_N + (page0 + i) * KV4_P + prow;
+        if (id >= 0 && pos <= last) {  // hidden positions hold zeros, whatever the cache has there
+          const uint8_t* src = a.pool + (static_cast<size_t>(id) * a.n_kv + u.g) * (18 * D);
+          const uint4 x = *reinterpret_cast<const uint4*>(src + code_off + (NCH == 2 ? hf * 16 : 0));
+          w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
+          if (NCH == 2) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src + code_off + (hf ^ 1) * 16);
+            w[i][4 % CW] = y.x; w[i][5 % CW] = y.y; w[i][6 % CW] = y.z; w[i][7 % CW] = y.w;
+            const uint32_t b = *reinterpret_cast<const uint32_t*>(src + scale_off);
+            sc[i] = hf ? (b >> 16) | (b << 16) : b;
+          } else {
+            sc[i] = *reinterpret_cast<const uint16_t*>(src + scale_off);
+          }
+          if (!is_k && u.pos0 < pos) {
+            // not every row of the tile sees this position: a NaN here must reach
+            // only those that do, through P (0 * NaN is NaN)
+            bool nan = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (((sc[i] >> (8 * k)) & 0x7Fu) == 0x7Fu) {
+                nan = true;
+                sc[i] &= ~(0xFFu << (8 * k));
+              }
+            if (nan) nan_bits |= 1u << i;
+          }
+        }
+      }
+    };
+    bool have = walk.next(a, p);
+    int j = have ? p.j0 : 0;
+    uint32_t n = 0;  // blocks made
+    if (have) load(p, j);
+    while (have) {
+      const uint32_t st = n % nst;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((n / nst) & 1) ^ 1, tmo, abort_flag))) {
+        if (!*abort_flag) give_up();
+        break;
+      }
+      const uint32_t dst = ring + st * Lay::KV_BYTES;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int pos = (page0 + i) * KV4_P + prow;
+        const uint32_t f01 = e4m3x2_to_f16x2(sc[i]), f23 = e4m3x2_to_f16x2(sc[i] >> 16);
+        const uint32_t f[4] = {__byte_perm(f01, f01, 0x1010), __byte_perm(f01, f01, 0x3232),
+                               __byte_perm(f23, f23, 0x1010), __byte_perm(f23, f23, 0x3232)};
+        const uint32_t row = dst + (pos >> 3) * Lay::KV_GROUP + (NCH == 2 ? hf * 1024 : 0) + (pos & 7) * 128;
+#pragma unroll
+        for (int k = 0; k < CW; ++k) {  // chunk of 8 channels: one word, two chunks a scale
+          const int ch = NCH == 2 ? k ^ (4 * hf) : 4 * hf + k;
+          const uint32_t s2 = f[k / 2];
+          kp_st16(row + ((ch ^ (pos & 7)) << 4),
+                  make_uint4(hmul2_u(e2m1_to_f16x2<0>(w[i][k]), s2), hmul2_u(e2m1_to_f16x2<1>(w[i][k]), s2),
+                             hmul2_u(e2m1_to_f16x2<2>(w[i][k]), s2), hmul2_u(e2m1_to_f16x2<3>(w[i][k]), s2)));
+        }
+      }
+      if (!is_k) {
+        // the block's NaN positions: this warp's two words (64 positions)
+        uint32_t bits[2] = {0, 0};
+        if (__any_sync(0xffffffffu, nan_bits != 0)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const unsigned rows = __ballot_sync(0xffffffffu, (nan_bits >> i) & 1);  // two lanes a row
+            uint32_t r16 = 0;
+            for (int r = 0; r < 16; ++r)
+              if ((rows >> (2 * r)) & 3) r16 |= 1u << r;
+            bits[i >> 1] |= r16 << (16 * (i & 1));
+          }
+        }
+        if (lane < 2) bars->v_nan[st][(page0 >> 1) + lane] = bits[lane];
+        nan_bits = 0;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&full[st]);
+      ++n;
+      if (++j >= p.j1) {
+        have = walk.next(a, p);
+        j = have ? p.j0 : 0;
+      }
+      if (have) load(p, j);
+    }
+  } else if (warp >= KP_MMA_WARP) {
+    kp_regs_less<KP_MMA_REGS>();
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t q_addr = sbase, p_addr = sbase + Lay::P_OFF, o_tmem = tmem + 256;
+    bool ok = true, any = false;
+    uint32_t n = 0, np = 0;  // blocks whose S was issued; pieces
+    auto pv = [&](uint32_t i, bool first) -> bool {
+      const uint32_t s = i % KP_VST;
+      if (!mbar_wait(&bars->v_full[s], (i / KP_VST) & 1, tmo, abort_flag)) return false;
+      if (!mbar_wait(&bars->p_full, i & 1, tmo, abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t v_addr = sbase + Lay::V_OFF + s * Lay::KV_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < KP_N / 16; ++kk) {
+        const uint64_t bdesc = desc_sw128_mnmajor(v_addr + kk * 2 * Lay::KV_GROUP, 1024, Lay::KV_GROUP);
+        const uint64_t adesc = desc_sw128_kmajor(p_addr + (kk >> 2) * KP_REGION) + 2 * (kk & 3);
+        tc_mma_bf16(o_tmem, adesc, bdesc, IDESC_PV, !first || kk > 0);
+      }
+      any = true;
+      tc_commit(&bars->p_free);
+      tc_commit(&bars->v_empty[s]);
+      return true;
+    };
+    while (warp == KP_MMA_WARP && ok && walk.next(a, p)) {
+      if (lane == 0) {
+        ok = mbar_wait(&bars->q_full, np & 1, tmo, abort_flag);
+        for (int j = p.j0; j < p.j1 && ok; ++j, ++n) {
+          const uint32_t s = n & 1, ks = n % KP_KST;
+          ok = mbar_wait(&bars->k_full[ks], (n / KP_KST) & 1, tmo, abort_flag) &&
+               mbar_wait(&bars->s_free[s], ((n >> 1) & 1) ^ 1, tmo, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_addr = sbase + Lay::K_OFF + ks * Lay::KV_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t adesc = desc_sw128_kmajor(q_addr + (kk >> 2) * KP_REGION) + 2 * (kk & 3);
+            const uint64_t bdesc = desc_sw128_kmajor_sbo(k_addr + (kk >> 2) * 1024, Lay::KV_GROUP) + 2 * (kk & 3);
+            tc_mma_bf16(tmem + s * KP_N, adesc, bdesc, IDESC_S, kk > 0);
+          }
+          any = true;
+          tc_commit(&bars->s_full[s]);
+          tc_commit(&bars->k_empty[ks]);
+          if (j > p.j0) ok = pv(n - 1, j - 1 == p.j0);
+        }
+        // the unit's last product before the next one's Q is waited for: its
+        // epilogue comes first
+        if (ok) ok = pv(n - 1, p.j1 - 1 == p.j0);
+        ++np;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (!ok && lane == 0) {
+      if (!*abort_flag) give_up();
+      if (any) {  // the products already issued finish before tensor memory goes away
+        tc_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0, tmo);
+      }
+    }
+  } else {
+    kp_regs_more<KP_SM_REGS>();
+    // --------------------------------------------------- softmax and epilogue
+    const int sw = warp - KP_DQ_WARPS;
+    const int quarter = warp & 3;      // tensor-memory lanes this warp may access
+    const int half = sw >> 2;          // which 64 keys of a block (and d/2 of O) it owns
+    const int r = quarter * 32 + lane; // the vector (lane) this thread owns
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    uint32_t n = 0, met = 0;           // blocks done; meetings
+    bool ok = true;
+    auto pv_done = [&](uint32_t i) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(&bars->p_free, i & 1, tmo, abort_flag));
+    };
+    auto meet = [&]() -> bool {  // a bounded barrier of the softmax threads
+      mbar_arrive(&bars->meet);
+      const bool good = __all_sync(0xffffffffu, mbar_wait(&bars->meet, met & 1, tmo, abort_flag));
+      ++met;
+      return good;
+    };
+    while (ok && walk.next(a, p)) {
+      const int ri = r / GRP;
+      const bool live = ri < p.rows;
+      const int qrow = p.row0 + (live ? ri : 0), qh = p.g * GRP + r % GRP;
+      const int qpos = live ? p.pos0 + ri : -1;  // sees positions 0 .. qpos
+      // Q: this half of the vector, scaled to fp16's range by its largest element
+      float scale;
+      {
+        const uint4* q4 = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(qrow) * a.n_q + qh) * D);
+        float top = 0.f;
+        uint4 own[D / 16];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 v = q4[c];
+          if (!live) v = make_uint4(0, 0, 0, 0);
+          top = fmaxf(top, kp_max3(kp_max3(fabsf(bf16lo(v.x)), fabsf(bf16hi(v.x)), fabsf(bf16lo(v.y))),
+                                   kp_max3(fabsf(bf16hi(v.y)), fabsf(bf16lo(v.z)), fabsf(bf16hi(v.z))),
+                                   fmaxf(fabsf(bf16lo(v.w)), fabsf(bf16hi(v.w)))));
+          if (c / (D / 16) == half) own[c % (D / 16)] = v;
+        }
+        const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        const int kq = top > 0.f ? max(-126, min(120, 14 - e)) : 0;
+        const float mul = exp2_int(kq);
+        scale = fmaxf(a.scale_log2 * exp2_int(-kq), 1.17549435e-38f);  // 0 times a hidden score's -inf is NaN
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int c = half * (D / 16) + i;
+          const uint4 v = own[i];
+          kp_st16(sbase + (c >> 3) * KP_REGION + kp_sw128(r, c & 7),
+                  make_uint4(kp_pack(bf16lo(v.x) * mul, bf16hi(v.x) * mul), kp_pack(bf16lo(v.y) * mul, bf16hi(v.y) * mul),
+                             kp_pack(bf16lo(v.z) * mul, bf16hi(v.z) * mul), kp_pack(bf16lo(v.w) * mul, bf16hi(v.w) * mul)));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q_full);
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = p.j0; j < p.j1; ++j, ++n) {
+        const uint32_t s = n & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[s], (n >> 1) & 1, tmo, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // this half's 64 scores, and the other half's for the row maximum
+        float x[KP_H];
+        float mx8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
+        const bool mixed = j * KP_N + KP_N - 1 > p.pos0;  // some row sees less than the block (uniform)
+        {
+          uint32_t w[32];
+          const int kb_own = j * KP_N + half * KP_H, kb_oth = j * KP_N + (half ^ 1) * KP_H;
+          const uint32_t own = tmem + lane_off + s * KP_N + half * KP_H, oth = tmem + lane_off + s * KP_N + (half ^ 1) * KP_H;
+          tc_ld_32x32b_x32(own, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+          tc_ld_32x32b_x32(own + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {  // the other half in two parts, for the maximum only
+            tc_ld_32x32b_x32(oth + 32 * c, w);
+            tc_wait_ld();
+            if (!mixed) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx8[i & 7] = kp_max3(mx8[i & 7], x[32 * c + i], __uint_as_float(w[i]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                if (kb_own + 32 * c + i > qpos) x[32 * c + i] = -INFINITY;
+                mx8[i & 7] = kp_max3(mx8[i & 7], x[32 * c + i], kb_oth + 32 * c + i > qpos ? -INFINITY : __uint_as_float(w[i]));
+              }
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&bars->s_free[s]);
+        }
+        const float mx = kp_max3(kp_max3(mx8[0], mx8[1], mx8[2]), kp_max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * scale;
+        float corr = 1.f;
+        if (mx > m_ref + KP_SLACK) {  // also from -inf, where O and l are still zero
+          corr = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mx);
+          m_ref = mx;
+          l *= corr;
+        }
+        // p = 2^(s scale - m + shift); m = -inf: nothing seen yet, all p are 0
+        const float nm = m_ref == -INFINITY ? KP_SHIFT : KP_SHIFT - m_ref;
+        if (__any_sync(0xffffffffu, fabsf(m_ref) > 3e7f && m_ref != -INFINITY)) {
+          // beyond fp32's whole numbers the fused step could pass the maximum's own
+          // rounding by more than the slack
+#pragma unroll
+          for (int i = 0; i < KP_H; ++i) x[i] = ex2_approx(__fadd_rn(__fmul_rn(x[i], scale), nm));
+        } else {
+          const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+#pragma unroll
+          for (int i = 0; i < KP_H / 2; ++i) {
+            const float2 t = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), sc2, nm2);
+            x[2 * i] = ex2_approx(t.x);
+            x[2 * i + 1] = ex2_approx(t.y);
+          }
+        }
+        if (mixed) {
+          // NaN of V at positions that not every row sees: to the rows that do
+          const uint32_t vs = n % KP_VST;
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (n / KP_VST) & 1, tmo, abort_flag))) {
+            ok = false;
+            break;
+          }
+          const uint32_t nan0 = bars->v_nan[vs][2 * half], nan1 = bars->v_nan[vs][2 * half + 1];
+          if (nan0 | nan1) {
+            const int kb = j * KP_N + half * KP_H;
+#pragma unroll
+            for (int i = 0; i < KP_H; ++i)
+              if ((((i < 32 ? nan0 : nan1) >> (i & 31)) & 1) && kb + i <= qpos) x[i] = __int_as_float(0x7FC00000);
+          }
+        }
+        {
+          float2 ls4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < KP_H / 2; ++i) ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(x[2 * i], x[2 * i + 1]));
+          const float2 a2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
+          l += a2.x + a2.y;
+        }
+        // a raised maximum rescales this half of the row of O, once the PV
+        // product of the previous block is done with it
+        if (j > p.j0 && __any_sync(0xffffffffu, corr != 1.f)) {
+          if (!pv_done(n - 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t u[32];
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            const uint32_t ta = tmem + lane_off + 256 + half * (D / 2) + c * 32;
+            tc_ld_32x32b_x32(ta, u);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * corr);
+            tc_st_32x32b_x32(ta, u);
+          }
+          tc_wait_st();
+        }
+        // P (free once the previous PV product is done), K-major in the 128-byte
+        // swizzle: this half's 64 keys fill one region
+        if (j > p.j0 && !pv_done(n - 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t p_reg = sbase + Lay::P_OFF + half * KP_REGION;
+#pragma unroll
+        for (int c = 0; c < KP_H / 8; ++c)
+          kp_st16(p_reg + kp_sw128(r, c), make_uint4(kp_pack(x[8 * c], x[8 * c + 1]), kp_pack(x[8 * c + 2], x[8 * c + 3]),
+                                                     kp_pack(x[8 * c + 4], x[8 * c + 5]), kp_pack(x[8 * c + 6], x[8 * c + 7])));
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full);
+      }
+      if (ok && !pv_done(n - 1)) ok = false;
+      if (!ok) break;
+      tc_fence_after();
+      bars->xch[half][r] = l;
+      if (!(ok = meet())) break;
+      const float L = bars->xch[0][r] + bars->xch[1][r];
+      uint4* dst = reinterpret_cast<uint4*>(a.o + (static_cast<size_t>(qrow) * a.n_q + qh) * D + half * (D / 2));
+      const bool whole = p.j0 == 0 && p.j1 == p.nb;
+      const int first = static_cast<int>((p.key + KP_FIXED) / quota);
+      const int last = static_cast<int>((p.key + KP_FIXED + p.nb - 1) / quota);
+      auto rec_of = [&](int cta) { return a.tiles + (static_cast<size_t>(cta) * 2 + (cta == first ? 1 : 0)) * Lay::REC; };
+      float* rec = rec_of(blockIdx.x);
+      const float inv = L == 0.f ? 0.f : a.v_scale / L;
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t u[32];
+        tc_ld_32x32b_x32(tmem + lane_off + 256 + half * (D / 2) + c * 32, u);
+        tc_wait_ld();
+        if (whole) {
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float* f = reinterpret_cast<const float*>(u) + 8 * i;
+              dst[c * 4 + i] = make_uint4(pack_bf16(f[0] * inv, f[1] * inv), pack_bf16(f[2] * inv, f[3] * inv),
+                                          pack_bf16(f[4] * inv, f[5] * inv), pack_bf16(f[6] * inv, f[7] * inv));
+            }
+          }
+        } else {  // four channels of all rows next to one another
+          float4* out = reinterpret_cast<float4*>(rec) + (half * (D / 8) + c * 8) * KP_M + r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float* f = reinterpret_cast<const float*>(u) + 4 * i;
+            out[i * KP_M] = make_float4(f[0], f[1], f[2], f[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (whole) {
+        if (!(ok = meet())) break;  // xch is free again
+        continue;
+      }
+      if (half == 0) {
+        rec[KP_M * D + r] = m_ref;
+        rec[KP_M * D + KP_M + r] = L;
+      }
+      __threadfence();
+      if (!(ok = meet())) break;
+      if (warp == KP_DQ_WARPS && lane == 0) {
+        const int before = atomicAdd(&a.tile_counters[first], 1);
+        bars->last = before == last - first;
+        if (before == last - first) a.tile_counters[first] = 0;  // as the next launch expects it
+      }
+      if (!(ok = meet())) break;
+      if (bars->last) {
+        __threadfence();
+        float M = -INFINITY, Ls = 0.f;
+        for (int b = first; b <= last; ++b) M = fmaxf(M, __ldcg(rec_of(b) + KP_M * D + r));
+        for (int b = first; b <= last; ++b) {
+          const float mb = __ldcg(rec_of(b) + KP_M * D + r);
+          Ls = fmaf(mb == -INFINITY ? 1.f : exp2f(mb - M), __ldcg(rec_of(b) + KP_M * D + KP_M + r), Ls);
+        }
+        const float iv = Ls == 0.f ? 0.f : a.v_scale / Ls;
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          float4 acc[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int b = first; b <= last; ++b) {
+            const float mb = __ldcg(rec_of(b) + KP_M * D + r);
+            const float wb = mb == -INFINITY ? 1.f : exp2f(mb - M);
+            const float4* in = reinterpret_cast<const float4*>(rec_of(b)) + (half * (D / 8) + c * 8) * KP_M + r;
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __ldcg(in + i * KP_M);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[i].x = fmaf(wb, v[i].x, acc[i].x);
+              acc[i].y = fmaf(wb, v[i].y, acc[i].y);
+              acc[i].z = fmaf(wb, v[i].z, acc[i].z);
+              acc[i].w = fmaf(wb, v[i].w, acc[i].w);
+            }
+          }
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 f = acc[2 * i], h = acc[2 * i + 1];
+              dst[c * 4 + i] = make_uint4(pack_bf16(f.x * iv, f.y * iv), pack_bf16(f.z * iv, f.w * iv),
+                                          pack_bf16(h.x * iv, h.y * iv), pack_bf16(h.z * iv, h.w * iv));
+            }
+          }
+        }
+      }
+    }
+    if (!ok && !*abort_flag) give_up();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == KP_MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, KP_TMEM_COLS);
+  }
+}
+
+template <int GRP, int NCH>
+cudaError_t launch_kp(const Kv4AttnArgs& a, cudaStream_t stream) {
+  const int smem = KpLayout<NCH>::SMEM;
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(attn_kv4_prefill_kernel<GRP, NCH>), smem);
+  if (e != cudaSuccess) return e;
+  attn_kv4_prefill_kernel<GRP, NCH><<<a.grid, KP_THREADS, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv4_tile_record_bytes(int head_dim) {
+  return (head_dim == 128 ? KpLayout<2>::REC : KpLayout<1>::REC) * sizeof(float);
+}
+
+cudaError_t launch_attention_kv4_prefill(const Kv4AttnArgs& a, cudaStream_t stream) {
+  const int grp = a.n_q / a.n_kv;
+#define NF_KP_CASE(G)                                          \
+  if (grp == G) return a.head_dim == 128 ? launch_kp<G, 2>(a, stream) : launch_kp<G, 1>(a, stream);
+  NF_KP_CASE(1) NF_KP_CASE(2) NF_KP_CASE(4) NF_KP_CASE(8)
+#undef NF_KP_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace nf

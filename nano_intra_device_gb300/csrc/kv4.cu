@@ -14,10 +14,11 @@
 struct nf_kv4_s {
   nf_model_shape shape{};
   int num_pages = 0, max_pages = 0, device = 0, num_sms = 0;
-  // one allocation: status word (256 bytes), arrival counters, split records
+  // one allocation: status word (256 bytes), arrival counters, split records of
+  // the two kernels
   uint32_t* status = nullptr;
-  int* counters = nullptr;
-  float* records = nullptr;
+  int *counters = nullptr, *tile_counters = nullptr;
+  float *records = nullptr, *tiles = nullptr;
 };
 
 namespace {
@@ -90,6 +91,10 @@ nf_status check_cache(const nf_kv_cache* c, bool fp4_only) {
   }
   return NF_OK;
 }
+
+// Requests of at most this many rows a step go to the kernel of few rows, which
+// reads the cache once for 8 / (n_q / n_kv) of them; longer ones to the tiles.
+constexpr int kSmallRows = 16;
 
 // Frequencies of (theta, head_dim), computed once for each pair in use: 64
 // powl calls cost more than the launch.
@@ -233,15 +238,19 @@ nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t 
   h->device = dev;
   h->num_sms = sms;
   const size_t cnt = ((size_t)sms * 4 + 255) / 256 * 256;
-  const size_t rec = (size_t)sms * 2 * nf::kv4_record_bytes(shape->head_dim);
-  if (cudaMalloc(&h->status, 256 + cnt + rec) != cudaSuccess ||
-      cudaMemset(h->status, 0, 256 + cnt) != cudaSuccess) {
+  const size_t rec = ((size_t)sms * 2 * nf::kv4_record_bytes(shape->head_dim) + 255) / 256 * 256;
+  const size_t tiles = (size_t)sms * 2 * nf::kv4_tile_record_bytes(shape->head_dim);
+  if (cudaMalloc(&h->status, 256 + 2 * cnt + rec + tiles) != cudaSuccess ||
+      cudaMemset(h->status, 0, 256 + 2 * cnt) != cudaSuccess) {
     cudaGetLastError();
     nf_kv4_destroy(h);
     return fail4(NF_ERR_OOM, "cudaMalloc of the workspace failed");
   }
-  h->counters = reinterpret_cast<int*>(reinterpret_cast<char*>(h->status) + 256);
-  h->records = reinterpret_cast<float*>(reinterpret_cast<char*>(h->status) + 256 + cnt);
+  char* at = reinterpret_cast<char*>(h->status) + 256;
+  h->counters = reinterpret_cast<int*>(at);
+  h->tile_counters = reinterpret_cast<int*>(at + cnt);
+  h->records = reinterpret_cast<float*>(at + 2 * cnt);
+  h->tiles = reinterpret_cast<float*>(at + 2 * cnt + rec);
   *out = h;
   return NF_OK;
 }
@@ -312,6 +321,11 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
   a.grid = h->num_sms;
   a.records = h->records;
   a.counters = h->counters;
+  a.tiles = h->tiles;
+  a.tile_counters = h->tile_counters;
+  a.small_rows = kSmallRows;
+  if (tok_begin && n_tok > kSmallRows)
+    NF_CUDA4(nf::launch_attention_kv4_prefill(a, static_cast<cudaStream_t>(stream)));
   NF_CUDA4(nf::launch_attention_kv4(a, static_cast<cudaStream_t>(stream)));
   return NF_OK;
 }

@@ -67,8 +67,14 @@ struct Kv4AttnArgs {
   int grid;              // CTAs, one an SM
   float* records;        // [grid][2] records of kv4_record_bytes
   int* counters;         // [grid], zero between launches
+  // requests of more rows than small_rows are the prefill kernel's
+  int small_rows;
+  float* tiles;          // [grid][2] records of kv4_tile_record_bytes
+  int* tile_counters;    // [grid], zero between launches
 };
 size_t kv4_record_bytes(int head_dim);
+size_t kv4_tile_record_bytes(int head_dim);
+cudaError_t launch_attention_kv4_prefill(const Kv4AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attention_kv4(const Kv4AttnArgs& a, cudaStream_t stream);
 
 }  // namespace nf
