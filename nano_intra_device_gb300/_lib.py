@@ -194,8 +194,11 @@ def ptr(t):
 
 def stream_handle(stream=None):
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return c_void_p(s.cuda_stream)
+    if stream is not None:
+        return c_void_p(stream.cuda_stream)
+    # the current stream's handle alone: a torch.cuda.Stream object around it takes
+    # 3 us, as long as a launch
+    return c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def make_shape(shape) -> nf_model_shape:

@@ -313,19 +313,41 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     const int part = is_k ? 0 : 9 * D;
     const int code_off = part + prow * (D / 2) + hf * (D / 4);
     const int scale_off = part + 8 * D + prow * (D / 16) + hf * (D / 32);
+    // Three blocks are under way: one in registers (w, sc) to be made, one whose
+    // page ids are here and whose codes are requested next, and one whose ids are
+    // requested.  Nothing waits for a load before it is used.
     uint32_t w[4][CW], sc[4];  // codes and scale bytes of four pages
-    uint32_t nan_bits = 0;     // V: pages whose row here holds a hidden-from-some NaN
-    auto load = [&](const KpPiece& u, int j) {  // block j of unit u
-      const int* bt = a.block_table + static_cast<size_t>(u.s) * a.max_pages;
-      const int npages = (u.len + KV4_P - 1) / KV4_P;
-      const int last = min(u.len, u.pos0 + u.rows) - 1;  // the tile's last visible position
-      int page = -1;
-      if (lane < 4 && j * 8 + page0 + lane < npages) {
-        page = bt[j * 8 + page0 + lane];
-        if (page < 0 || page >= a.num_pages) {  // never read outside the pool
-          raise_status(a.status, ST_BAD_PAGE);
-          page = 0;
-        }
+    struct Block {
+      int s, g, j, pos0, last, npages;
+      bool have;
+    } made, ahead;
+    made.have = ahead.have = false;
+    int page = -1;  // id of page `lane` of `ahead`
+    bool more = walk.next(a, p);
+    int j = more ? p.j0 : 0;
+    auto load_ids = [&]() {  // the walk's block becomes `ahead`
+      ahead.have = more;
+      page = -1;
+      if (!more) return;
+      ahead.s = p.s;
+      ahead.g = p.g;
+      ahead.j = j;
+      ahead.pos0 = p.pos0;
+      ahead.last = min(p.len, p.pos0 + p.rows) - 1;  // the tile's last visible position
+      ahead.npages = (p.len + KV4_P - 1) / KV4_P;
+      if (lane < 4 && j * 8 + page0 + lane < ahead.npages)
+        page = a.block_table[static_cast<size_t>(p.s) * a.max_pages + j * 8 + page0 + lane];
+      if (++j >= p.j1) {
+        more = walk.next(a, p);
+        j = more ? p.j0 : 0;
+      }
+    };
+    auto load_codes = [&]() {  // `ahead` becomes `made`
+      made = ahead;
+      if (!made.have) return;
+      if (lane < 4 && made.j * 8 + page0 + lane < made.npages && (page < 0 || page >= a.num_pages)) {
+        raise_status(a.status, ST_BAD_PAGE);  // never read outside the pool
+        page = 0;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -333,43 +355,44 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
 #pragma unroll
         for (int k = 0; k < CW; ++k) w[i][k] = 0;
         sc[i] = 0;
-        const int pos = j * KP_N + (page0 + i) * KV4_P + prow;
-        if (id >= 0 && pos <= last) {  // hidden positions hold zeros, whatever the cache has there
-          const uint8_t* src = a.pool + (static_cast<size_t>(id) * a.n_kv + u.g) * (18 * D);
+        if (id >= 0 && made.j * KP_N + (page0 + i) * KV4_P + prow <= made.last) {
+          // hidden positions hold zeros, whatever the cache has there
+          const uint8_t* src = a.pool + (static_cast<size_t>(id) * a.n_kv + made.g) * (18 * D);
           const uint4 x = *reinterpret_cast<const uint4*>(src + code_off + (NCH == 2 ? hf * 16 : 0));
           w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
           if (NCH == 2) {
             const uint4 y = *reinterpret_cast<const uint4*>(src + code_off + (hf ^ 1) * 16);
             w[i][4 % CW] = y.x; w[i][5 % CW] = y.y; w[i][6 % CW] = y.z; w[i][7 % CW] = y.w;
-            const uint32_t b = *reinterpret_cast<const uint32_t*>(src + scale_off);
-            sc[i] = hf ? (b >> 16) | (b << 16) : b;
+            sc[i] = *reinterpret_cast<const uint32_t*>(src + scale_off);
           } else {
             sc[i] = *reinterpret_cast<const uint16_t*>(src + scale_off);
-          }
-          if (!is_k && u.pos0 < pos) {
-            // not every row of the tile sees this position: a NaN here must reach
-            // only those that do, through P (0 * NaN is NaN)
-            bool nan = false;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (((sc[i] >> (8 * k)) & 0x7Fu) == 0x7Fu) {
-                nan = true;
-                sc[i] &= ~(0xFFu << (8 * k));
-              }
-            if (nan) nan_bits |= 1u << i;
           }
         }
       }
     };
-    bool have = walk.next(a, p);
-    int j = have ? p.j0 : 0;
+    load_ids();
+    load_codes();
+    load_ids();
     uint32_t n = 0;  // blocks made
-    if (have) load(p, j);
-    while (have) {
+    while (made.have) {
       const uint32_t st = n % nst;
       if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((n / nst) & 1) ^ 1, tmo, abort_flag))) {
         if (!*abort_flag) give_up();
         break;
+      }
+      uint32_t nan_bits = 0;  // V: pages whose row here holds a NaN that not every row of the tile sees
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!is_k && made.j * KP_N + (page0 + i) * KV4_P + prow > made.pos0) {
+          // it must reach only the rows that do, through P (0 * NaN is NaN)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (((sc[i] >> (8 * k)) & 0x7Fu) == 0x7Fu) {
+              nan_bits |= 1u << i;
+              sc[i] &= ~(0xFFu << (8 * k));
+            }
+        }
+        if (NCH == 2 && hf) sc[i] = __byte_perm(sc[i], 0, 0x1032);
       }
       const uint32_t dst = ring + st * Lay::KV_BYTES;
 #pragma unroll
@@ -401,17 +424,16 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
             bits[i >> 1] |= r16 << (16 * (i & 1));
           }
         }
-        if (lane < 2) bars->v_nan[st][(page0 >> 1) + lane] = bits[lane];
-        nan_bits = 0;
+        if (lane == 0) {
+          bars->v_nan[st][page0 >> 1] = bits[0];
+          bars->v_nan[st][(page0 >> 1) + 1] = bits[1];
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(&full[st]);
       ++n;
-      if (++j >= p.j1) {
-        have = walk.next(a, p);
-        j = have ? p.j0 : 0;
-      }
-      if (have) load(p, j);
+      load_codes();
+      load_ids();
     }
   } else if (warp >= KP_MMA_WARP) {
     kp_regs_less<KP_MMA_REGS>();
