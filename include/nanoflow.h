@@ -444,8 +444,8 @@ nf_status nf_gemm_wrows(const void* A, const void* B, void* C, const void* R, in
  * (position, KV head).  With E = k_exp for K and v_exp for V:
  *   a = max |x_i|;  s = e4m3(a / (6 * 2^E)), n_i = e2m1(x_i / (s * 2^E)), both
  *   rounded to nearest, ties to even, saturating at 448 and 6; n_i = 0 where
- *   s = 0; a NaN anywhere in the block makes s NaN; the block stands for
- *   n_i * s * 2^E.  Infinities saturate.
+ *   s = 0 (a zero is stored without sign); a NaN anywhere in the block makes s
+ *   NaN; the block stands for n_i * s * 2^E.  Infinities saturate.
  * These products have 6 significant bits, so they are exact in bf16.  The
  * decisions are those of the formulas in 64-bit arithmetic.
  * Pool: uint8 [num_pages, n_kv, 2 (K, V), 9 * head_dim]: the page's 16 rows of

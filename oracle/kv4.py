@@ -2,8 +2,8 @@
 
 A block is 16 channels of one (position, KV head) of K or V.  With the exponent
 E of K or V: a = max |x_i|, s = e4m3(a / (6 * 2^E)), n_i = e2m1(x_i / (s * 2^E)),
-nearest with ties to the even code, saturating; n_i = 0 where s = 0; a NaN makes
-s NaN; the block stands for n_i * s * 2^E.  A pool is uint8
+nearest with ties to the even code, saturating; n_i = 0 where s = 0, and a zero
+code has no sign; a NaN makes s NaN; the block stands for n_i * s * 2^E.  A pool is uint8
 [num_pages, n_kv, 2, 9 d]: 16 rows of d / 2 code bytes (channel 2i in the low
 half of byte i), then 16 rows of d / 16 scale bytes.
 
@@ -38,7 +38,8 @@ def quantise(x, exp):
     s = nearest(top, E4M3)
     with np.errstate(divide="ignore", invalid="ignore"):
         u = np.where(E4M3[s][..., None] > 0, np.minimum(a / E4M3[s][..., None], 1e9), 0.0)
-    n = nearest(u, E2M1) | (np.signbit(y) << 3)
+    n = nearest(u, E2M1)
+    n |= ((n > 0) & np.signbit(y)) << 3  # a zero has no sign
     n = np.where(bad[..., None] | (s == 0)[..., None], 0, n)
     return n.reshape(x.shape).astype(np.uint8), np.where(bad, 127, s).astype(np.uint8)
 

@@ -275,9 +275,13 @@ def test_append_nan_inf_and_zero_rows():
     h[2, 4:, 9] = float("inf")    # V saturates
     h[3, 4:, 40] = -float("inf")
     h[4, 4, :] = -0.0
+    h[6, 2, 11] = float("inf")    # a key's pair, and with it two blocks, to infinity or NaN
+    h[7, 3, 40] = -float("inf")
+    pos[7] = 0
     h[5, 5, :16] = float("nan")
-    check_append(shape_of(2, 2, 64), x, gains_of(r, 64), pos, slot, _lib.NF_KV_FP4, 3)
-    check_append(shape_of(2, 2, 64), x, [None, None], pos, slot, _lib.NF_KV_BF16, 3)
+    for fmt in (_lib.NF_KV_FP4, _lib.NF_KV_BF16):
+        for kind in ("both", "none"):
+            check_append(shape_of(2, 2, 64), x, gains_of(r, 64, kind), pos, slot, fmt, 3)
 
 
 def test_append_codes_are_those_of_64_bits():
