@@ -396,59 +396,73 @@ __device__ __forceinline__ uint32_t codes_near(const float2 (&x)[4], const float
   return below;
 }
 
-// Scale bytes and codes of a lane's two blocks (lo and hi channels).
-struct QkBytes {
-  uint32_t blo, bhi, wlo, whi;
-};
-// What fp32 left open, in pairs of floats: scales (slo, shi) and codes (nibbles of
-// olo, ohi).  Every lane of the warp calls (shuffles); arguments by value, so
-// that the callers' values stay in registers where nothing is open.
+// 1 / sqrt(mean + eps) of the head, in pairs of floats: the squares of 8 bits are
+// exact, the sums a tree.
 template <int D>
-__device__ __noinline__ QkBytes settle(QkLane q, const RopeFreq& f, float eps, float mul, bool slo, bool shi, uint32_t olo,
-                                       uint32_t ohi, QkBytes y) {
-  // both lanes of a block work out a scale that either left open, and all its codes
-  slo |= __shfl_xor_sync(0xffffffffu, slo, 1);
-  shi |= __shfl_xor_sync(0xffffffffu, shi, 1);
-  dd ss = {0.f, 0.f};
+__device__ __forceinline__ dd dd_norm(const QkLane& q, float eps) {
   const uint32_t raw[8] = {q.lo.x, q.lo.y, q.lo.z, q.lo.w, q.hi.x, q.hi.y, q.hi.z, q.hi.w};
+  dd t[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {  // squares of 8 bits are exact
-    ss = dd_add(ss, dd{bf16lo(raw[i]) * bf16lo(raw[i]), 0.f});
-    ss = dd_add(ss, dd{bf16hi(raw[i]) * bf16hi(raw[i]), 0.f});
-  }
+  for (int i = 0; i < 8; ++i) t[i] = dd_two_sum(bf16lo(raw[i]) * bf16lo(raw[i]), bf16hi(raw[i]) * bf16hi(raw[i]));
+#pragma unroll
+  for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) t[i] = dd_add(t[i], t[i + n]);
+  dd ss = t[0];
 #pragma unroll
   for (int o = 1; o < D / 16; o <<= 1)
     ss = dd_add(ss, dd{__shfl_xor_sync(0xffffffffu, ss.h, o), __shfl_xor_sync(0xffffffffu, ss.l, o)});
-  const dd r = dd_rsqrt(dd_add(dd{ss.h * (1.f / D), ss.l * (1.f / D)}, dd{eps, 0.f}));
-  dd mlo = {0.f, 0.f}, mhi = {0.f, 0.f};  // largest magnitudes of open blocks
+  return dd_rsqrt(dd_add(dd{ss.h * (1.f / D), ss.l * (1.f / D)}, dd{eps, 0.f}));
+}
+
+// What fp32 left open.  Every lane of the warp calls (shuffles); arguments by
+// value, so that the callers' values stay in registers where nothing is open.
+//
+// Scale bytes (lo in the low byte, hi in the next) from the values of the bits in
+// lo, hi, the only ones that may be their block's largest.
+template <int D>
+__device__ __noinline__ uint32_t settle_scales(QkLane q, const RopeFreq& f, float eps, float mul, uint32_t lo, uint32_t hi) {
+  const dd r = dd_norm<D>(q, eps);
   auto larger = [](dd a, dd b) { return dd_add(b, dd_neg(a)).h > 0.f ? b : a; };
   auto mag = [](dd a) { return a.h < 0.f ? dd_neg(a) : a; };
-  for (int i = 0; i < 8; ++i) {
-    if (!(slo || shi)) continue;
+  dd mlo = {0.f, 0.f}, mhi = {0.f, 0.f};
+  for (uint32_t any = lo | hi; any; any &= any - 1) {
+    const int i = __ffs(any) - 1;
     dd u, v;
     dd_pair(q, f, r, mul, i, &u, &v);
-    mlo = larger(mlo, mag(u));
-    mhi = larger(mhi, mag(v));
+    if ((lo >> i) & 1) mlo = larger(mlo, mag(u));
+    if ((hi >> i) & 1) mhi = larger(mhi, mag(v));
   }
+  __syncwarp();
   mlo = larger(mlo, dd{__shfl_xor_sync(0xffffffffu, mlo.h, 1), __shfl_xor_sync(0xffffffffu, mlo.l, 1)});
   mhi = larger(mhi, dd{__shfl_xor_sync(0xffffffffu, mhi.h, 1), __shfl_xor_sync(0xffffffffu, mhi.l, 1)});
-  if (slo) {
-    y.blo = dd_scale(mlo);
-    olo = ~0u;
-  }
-  if (shi) {
-    y.bhi = dd_scale(mhi);
-    ohi = ~0u;
-  }
-  for (int i = 0; i < 8; ++i) {
+  return dd_scale(mlo) | (dd_scale(mhi) << 8);
+}
+// The codes of the nibbles that lo, hi mark, under the scale bytes blo, bhi, in
+// the words wlo, whi.
+template <int D>
+__device__ __noinline__ uint2 settle_codes(QkLane q, const RopeFreq& f, float eps, float mul, uint32_t lo, uint32_t hi, uint32_t blo,
+                                           uint32_t bhi, uint32_t wlo, uint32_t whi) {
+  const dd r = dd_norm<D>(q, eps);
+  for (uint32_t any = lo | hi; any;) {
+    const int i = (__ffs(any) - 1) / 4;
     const uint32_t nib = 0xFu << (4 * i);
-    if (!((olo | ohi) & nib)) continue;
+    any &= ~nib;
     dd u, v;
     dd_pair(q, f, r, mul, i, &u, &v);
-    if (olo & nib) y.wlo = (y.wlo & ~nib) | (dd_code(u, y.blo) << (4 * i));
-    if (ohi & nib) y.whi = (y.whi & ~nib) | (dd_code(v, y.bhi) << (4 * i));
+    if (lo & nib) wlo = (wlo & ~nib) | (dd_code(u, blo) << (4 * i));
+    if (hi & nib) whi = (whi & ~nib) | (dd_code(v, bhi) << (4 * i));
   }
-  return y;
+  __syncwarp();
+  return make_uint2(wlo, whi);
+}
+// Bits of the values that may be the largest of a block whose largest is near t.
+__device__ __forceinline__ uint32_t near_largest(const float2 (&x)[4], float t) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m |= (fabsf(x[i].x) >= t ? 1u : 0u) << (2 * i) | (fabsf(x[i].y) >= t ? 2u : 0u) << (2 * i);
+  return m;
 }
 
 // Two values at a time.
@@ -606,11 +620,27 @@ __device__ __forceinline__ void kv_group(const QkNormRopeArgs& a, const RopeFreq
     q.gain_hi = LPH;
     q.pos = a.tok_pos[t];
     q.i0 = 8 * l;
-    const QkBytes y = settle<D>(q, f, a.eps, mul, slo, shi, olo, ohi, QkBytes{blo, bhi, wlo, whi});
-    blo = y.blo;
-    bhi = y.bhi;
-    wlo = y.wlo;
-    whi = y.whi;
+    if (__any_sync(0xffffffffu, slo || shi)) {
+      // both lanes of a block work out a scale that either left open
+      slo |= __shfl_xor_sync(0xffffffffu, slo, 1);
+      shi |= __shfl_xor_sync(0xffffffffu, shi, 1);
+      // what is smaller than the largest by more than their errors is not it
+      const uint32_t y = settle_scales<D>(q, f, a.eps, mul, slo ? near_largest(lo, (tlo - 4.f * e) / mul) : 0u,
+                                          shi ? near_largest(hi, (thi - 4.f * e) / mul) : 0u);
+      if (slo) {
+        blo = y & 0xFFu;
+        wlo = codes_near(lo, sum, mul * scale_inv(blo), &olo);
+      }
+      if (shi) {
+        bhi = (y >> 8) & 0xFFu;
+        whi = codes_near(hi, sum, mul * scale_inv(bhi), &ohi);
+      }
+    }
+    if (__any_sync(0xffffffffu, olo || ohi)) {
+      const uint2 y = settle_codes<D>(q, f, a.eps, mul, olo, ohi, blo, bhi, wlo, whi);
+      wlo = y.x;
+      whi = y.y;
+    }
   }
   if (store) {
     uint8_t* part = static_cast<uint8_t*>(a.k_pool) +
@@ -637,6 +667,7 @@ __global__ void __launch_bounds__(QK_THREADS, PART == PART_Q ? 4 : 2)
   constexpr int LPH = D / 16;         // lanes of a head
   constexpr int HPW = 32 / LPH;       // heads of a warp
   constexpr int HALF = D / 2, WARPS = QK_THREADS / 32;
+  if (PART == PART_KV) pdl_trigger();  // the queries' launch may fill the SMs that this one leaves free
   __shared__ __align__(16) float co[QK_MAX_TOK][HALF], si[QK_MAX_TOK][HALF];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hl = lane / LPH, l = lane % LPH;  // head of the warp, lane of the head
@@ -674,7 +705,10 @@ __global__ void __launch_bounds__(QK_THREADS, PART == PART_Q ? 4 : 2)
     si[k / HALF][i] = fmaf(c, d, s);
   }
   __syncthreads();
-  if (!busy) return;
+  if (!busy) {
+    if (PART == PART_Q) pdl_wait();
+    return;
+  }
   float2 c2[4], s2[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -706,6 +740,8 @@ __global__ void __launch_bounds__(QK_THREADS, PART == PART_Q ? 4 : 2)
     ulo = nlo;
     uhi = nhi;
   }
+  // what follows on the stream sees both launches complete
+  if (PART == PART_Q) pdl_wait();
 }
 
 // ------------------------------------------------------------ rows by slot
@@ -779,7 +815,16 @@ static cudaError_t launch_qk(const QkNormRopeArgs& a, const RopeFreq& f, int tok
   const int grid = (a.n_tok + tok - 1) / tok;
   if (split) {
     qk_norm_rope_kernel<D, FP4, PART_KV><<<grid, QK_THREADS, 0, stream>>>(a, f, tok);
-    qk_norm_rope_kernel<D, false, PART_Q><<<grid, QK_THREADS, 0, stream>>>(a, f, tok);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(QK_THREADS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<D, false, PART_Q>, a, f, tok);
   } else {
     qk_norm_rope_kernel<D, FP4, PART_ALL><<<grid, QK_THREADS, 0, stream>>>(a, f, tok);
   }
