@@ -500,7 +500,8 @@ nf_status nf_block_tables(const int32_t* held, const int32_t* seq_lens, int32_t 
  * qkv: device bf16 [n_tok, ld], each row the q heads, then the k heads, then
  *   the v heads; ld >= (n_q + 2 n_kv) * head_dim, a multiple of 8.
  * q_gain, k_gain: device bf16 [head_dim], or NULL: those heads are not normed.
- *   Normed heads become u * gain / sqrt(mean(u^2) + shape->rms_eps).
+ *   Normed heads become u * gain / sqrt(mean(u^2) + shape->rms_eps); the sum
+ *   of squares is held in fp32 and must not pass its range.
  * tok_pos, tok_slot: device int32 [n_tok].  Rotation as in nf_layer_step (pairs
  *   i and i + head_dim / 2, angle pos * rope_theta^(-2i / head_dim)), accurate
  *   at every 32-bit position.  A token whose slot is outside
@@ -525,6 +526,7 @@ nf_status nf_kv4_read(const nf_model_shape* shape, const nf_kv_cache* cache, con
 typedef struct nf_kv4_s* nf_kv4;
 nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t max_pages_per_seq,
                         nf_kv4* out);
+/* The caller sees to it that no call on the handle is still running. */
 void nf_kv4_destroy(nf_kv4 h);
 /* As nf_plan_poll, for the calls on this handle. */
 nf_status nf_kv4_poll(nf_kv4 h, int wait);
@@ -539,9 +541,13 @@ nf_status nf_kv4_poll(nf_kv4 h, int wait);
  * positions 0 ... its own; a row without any (a padding row of a request of
  * length 0) becomes zero.  Rows from tok_begin[n_seq] on stay as they are, so
  * a batch padded to n_tok rows is fine.
+ * What a row does not see cannot reach it, whatever it holds.  A NaN that it
+ * sees makes NaN of every channel (NaN in K) or of its block's channels at
+ * least (NaN in V).
  * A page id outside the pool reads page 0, a length outside
  * [0, 16 * max_pages_per_seq] counts as 0, rows outside [0, n_tok) are left
- * out; each sets the status that nf_kv4_poll reports.
+ * out, and rows that together would read 2^32 pages of a KV head or more are
+ * not computed; each sets the status that nf_kv4_poll reports.
  * NF_ERR_INVALID_ARG if another device than the handle's is current. */
 nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
                            const int32_t* block_table, const int32_t* seq_lens,

@@ -92,9 +92,16 @@ nf_status check_cache(const nf_kv_cache* c, bool fp4_only) {
   return NF_OK;
 }
 
-// Requests of at most this many rows a step go to the kernel of few rows, which
-// reads the cache once for 8 / (n_q / n_kv) of them; longer ones to the tiles.
-constexpr int kSmallRows = 16;
+// A request of at most this many query vectors a KV head (rows * n_q / n_kv) goes
+// to the kernel of few rows, which reads its cache once for 8 of them; a longer
+// one to the 128-vector tiles, whose time hardly depends on how full they are.
+// Measured, few rows against tiles, 32 query and 8 KV heads of 128, 16 requests
+// of 2000 positions: 45 / 64 us at 32 vectors, 70 / 64 at 64, 92 / 66 at 96; 128
+// requests of 500: 78 / 163, 129 / 164, 178 / 133.  With 8 query heads the two
+// meet at 64 vectors too (70 / 64), with 64 at 64 as well (68 / 64).  A single
+// request gains from the kernel of few rows for longer (25 / 43 at 96), which
+// cannot be told from the batch's sizes without its lengths.
+constexpr int kSmallVecs = 64;
 
 // Frequencies of (theta, head_dim), computed once for each pair in use: 64
 // powl calls cost more than the launch.
@@ -274,9 +281,10 @@ nf_status nf_kv4_poll(nf_kv4 h, int wait) {
   if (st) NF_CUDA4(cudaMemset(h->status, 0, 4));
   if (st & nf::ST_TIMEOUT) return fail4(NF_ERR_TIMEOUT, "a device wait timed out (status 0x%x)", st);
   if (st)
-    return fail4(NF_ERR_DEVICE, "device-side check failed (status 0x%x: %s%s)", st,
+    return fail4(NF_ERR_DEVICE, "device-side check failed (status 0x%x: %s%s%s)", st,
                  (st & nf::ST_BAD_PAGE) ? "page id out of range " : "",
-                 (st & nf::ST_BAD_LEN) ? "bad sequence length or rows" : "");
+                 (st & nf::ST_BAD_LEN) ? "bad sequence length or rows " : "",
+                 (st & nf::ST_OVERFLOW) ? "too many pages for a call" : "");
   return NF_OK;
 }
 
@@ -323,8 +331,8 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
   a.counters = h->counters;
   a.tiles = h->tiles;
   a.tile_counters = h->tile_counters;
-  a.small_rows = kSmallRows;
-  if (tok_begin && n_tok > kSmallRows)
+  a.small_rows = kSmallVecs / (a.n_q / a.n_kv);
+  if (tok_begin && n_tok > a.small_rows)
     NF_CUDA4(nf::launch_attention_kv4_prefill(a, static_cast<cudaStream_t>(stream)));
   NF_CUDA4(nf::launch_attention_kv4(a, static_cast<cudaStream_t>(stream)));
   return NF_OK;

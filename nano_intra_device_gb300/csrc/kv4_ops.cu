@@ -804,8 +804,8 @@ __global__ void __launch_bounds__(RD_THREADS)
 
 cudaError_t launch_block_tables(const BlockTableArgs& a, int num_sms, cudaStream_t stream) {
   // a CTA for every block of tokens the caller has room for, up to four an SM
-  int grid = (a.tok_cap + BT_TOKENS - 1) / BT_TOKENS;
-  grid = grid < 1 ? 1 : grid > 4 * num_sms ? 4 * num_sms : grid;
+  const long long want = (static_cast<long long>(a.tok_cap) + BT_TOKENS - 1) / BT_TOKENS;
+  const int grid = static_cast<int>(want < 1 ? 1 : want > 4 * num_sms ? 4 * num_sms : want);
   block_tables_kernel<<<grid, BT_THREADS, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -86,6 +86,18 @@ def test_block_tables(n, width, kind, seed):
     assert want["state_out"][3] == 0 and want["state_out"][2] == tok
 
 
+def test_block_tables_of_a_large_batch():
+    """Tens of thousands of requests and tokens, some prompts of thousands."""
+    r = np.random.default_rng(21)
+    n, width = 20000, 300
+    held = r.integers(0, 200, n)
+    lens = np.where(r.random(n) < 0.9, held + 1, r.integers(0, 200, n))
+    lens[r.integers(0, n, 40)] = 4800
+    num = int((-(-np.maximum(held, lens) // 16)).sum()) + 3
+    table, ring, free, rows = make_tables(r, n, width, num, held, num - 5, int(np.clip(lens - held, 0, None).sum()))
+    run_tables(held, lens, table, ring, (num - 5, free), rows)
+
+
 def test_block_tables_short_ring_changes_nothing():
     r = np.random.default_rng(5)
     held, lens = np.array([5, 16, 40, 30]), np.array([6, 33, 0, 200])
@@ -224,6 +236,51 @@ def test_append_many_tokens(n_tok):
     r = np.random.default_rng(n_tok)
     x, pos, slot = append_case(r, n_tok, 2, 1, 64, n_tok // 16 + 1, 5000)
     check_append(shape_of(2, 1, 64), x, gains_of(r, 64), pos, slot, _lib.NF_KV_FP4, n_tok // 16 + 1)
+
+
+@pytest.mark.parametrize("fmt", [_lib.NF_KV_FP4, _lib.NF_KV_BF16])
+@pytest.mark.parametrize("n_tok,n_q,n_kv,d", [(3700, 8, 8, 64), (5001, 8, 2, 128), (4000, 16, 4, 64)])
+def test_append_of_thousands(fmt, n_tok, n_q, n_kv, d):
+    r = np.random.default_rng(n_tok)
+    x, pos, slot = append_case(r, n_tok, n_q, n_kv, d, n_tok // 16 + 2, 5000)
+    slot[5::97] = -1
+    check_append(shape_of(n_q, n_kv, d), x, gains_of(r, d), pos, slot, fmt, n_tok // 16 + 2, (-1, 2))
+
+
+@pytest.mark.parametrize("n_tok", [40, 4500])
+def test_append_in_a_graph_and_on_another_stream(n_tok):
+    r = np.random.default_rng(n_tok)
+    n_q, n_kv, d, num = 8, 4, 128, n_tok // 16 + 2
+    shape = shape_of(n_q, n_kv, d)
+    x, pos, slot = append_case(r, n_tok, n_q, n_kv, d, num, 5000)
+    g = [t.to(DEV) for t in gains_of(r, d)]
+    xd, pd, sd = x.to(DEV), dev32(pos), dev32(slot)
+    side = torch.cuda.Stream()
+    outs = []
+    for way in ("plain", "graph", "stream"):
+        pool = torch.zeros(num, n_kv, 2, 9 * d, dtype=torch.uint8, device=DEV)
+        q, k, v = (torch.zeros(n_tok, h, d, dtype=torch.bfloat16, device=DEV) for h in (n_q, n_kv, n_kv))
+        cache = _lib.KvCache(shape, num, _lib.NF_KV_FP4, pool)
+
+        def run(stream=None):
+            _lib.qk_norm_rope(shape, xd, g[0], g[1], pd, sd, q, cache, stream=stream)
+            _lib.kv4_read(shape, cache, sd, k, v, stream=stream)  # behind the append, whatever it launches
+        torch.cuda.synchronize()
+        if way == "graph":
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                run()
+            for _ in range(3):
+                pool.zero_()
+                q.zero_()
+                graph.replay()
+        else:
+            run(side if way == "stream" else None)
+        torch.cuda.synchronize()
+        outs.append([pool, q, k, v])
+    for o in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+    assert outs[0][2].any() and outs[0][3].any()
 
 
 @pytest.mark.parametrize("kind", ["none", "q", "k"])
@@ -540,6 +597,166 @@ def test_attention_repeats_bit_for_bit_in_a_graph_and_on_another_stream():
     h.poll()
     for o in outs + [last]:
         assert torch.equal(o, first)
+
+
+def poison(r, pool, bt, n, lo, d):
+    """NaN scales in a few K and V blocks at positions [lo, n) of request 0's first and last KV head."""
+    n_kv = pool.shape[1]
+    for part in (0, 1, 1):
+        p, g = int(r.integers(lo, n)), int(r.choice([0, n_kv - 1]))
+        at = 8 * d + p % 16 * (d // 16) + int(r.integers(0, d // 16))
+        pool[bt[0, p // 16], g, part, at] = r.choice([0x7F, 0xFF])
+
+
+@pytest.mark.parametrize("n_q,n_kv,d", [(1, 1, 64), (4, 2, 128), (8, 2, 64), (8, 1, 128)])
+@pytest.mark.parametrize("lens,q_lens", [([40], [12]), ([9], [9]), ([300, 5], [200, 1]), ([1000, 33], [70, 17]), ([17, 200], [17, 8])])
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_attention_nan_reaches_the_rows_that_see_it(n_q, n_kv, d, lens, q_lens, seed):
+    """A NaN of K or V at a position of the chunk: rows before it keep their values."""
+    r = np.random.default_rng(100 * seed + lens[0])
+    shape = shape_of(n_q, n_kv, d)
+    pool, bt, q = attention_case(r, n_q, n_kv, d, lens, q_lens)
+    poison(r, pool, bt, lens[0], lens[0] - q_lens[0], d)
+    got = run_attention(shape, pool, bt, q, lens, q_lens)
+    q64 = q.double().numpy()
+    want, mag = orc.attention(q64, pool, (0, 0), bt, lens, q_lens)
+    hit = np.isnan(want)
+    assert hit.any() and np.isnan(got[hit]).all()
+    clean = ~hit.any(-1)  # (row, head) pairs that see no NaN
+    top, vtop = (np.nan_to_num(np.abs(orc.take(pool, range(pool.shape[0] * 16), i, 0))).max() for i in (0, 1))
+    mass = np.abs(q64).sum(-1, keepdims=True) * top / np.sqrt(d)
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * d * 2.0 ** -24 * mass) * mag + max(lens) * 2.0 ** -32 * vtop
+    assert (np.abs(got - want)[clean] <= bound[clean]).all()
+
+
+@pytest.mark.parametrize("q_len", [1, 9, 60])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_attention_a_bad_query_spoils_its_own_row(q_len, bad):
+    r = np.random.default_rng(q_len)
+    lens, q_lens = [200, 70], [q_len, q_len]
+    pool, bt, q = attention_case(r, 4, 2, 64, lens, q_lens)
+    shape = shape_of(4, 2, 64)
+    good = run_attention(shape, pool, bt, q, lens, q_lens)
+    q[0, 1, 5] = bad
+    got = run_attention(shape, pool, bt, q, lens, q_lens)
+    assert not np.isfinite(got[0, 1]).all()
+    got[0, 1] = good[0, 1]
+    assert np.array_equal(got, good)
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,lens,q_lens", [
+    (8, 1, 128, [6000], [130]), (4, 4, 64, [5000, 3, 900, 64], [77, 3, 65, 64]), (8, 2, 128, [2500, 60, 16, 18, 200], [900, 17, 16, 18, 1]), (2, 1, 64, [333, 32, 5000], [33, 32, 31]),
+    (2, 2, 128, [1500], [1500]), (16, 2, 64, [40, 0, 10, 700, 8], [40, 30, 40, 128, 9])])
+def test_attention_long_chunks(n_q, n_kv, d, lens, q_lens):
+    """Tiles cut between CTAs, chunks on both sides of what one kernel takes, tiles without a position."""
+    r = np.random.default_rng(lens[0])
+    check_attention(shape_of(n_q, n_kv, d), *attention_case(r, n_q, n_kv, d, lens, q_lens), lens, q_lens, pad_rows=3)
+
+
+@pytest.mark.parametrize("n_q,n_kv", [(2, 2), (8, 1)])
+def test_attention_many_chunks(n_q, n_kv):
+    """More requests than threads, every third of them with rows for the tiles."""
+    r = np.random.default_rng(n_q)
+    q_lens = np.where(np.arange(700) % 3 == 0, 64 * n_kv // n_q - 1 + np.arange(700) % 5, np.arange(700) % 4)
+    lens = np.maximum(q_lens + r.integers(-2, 60, 700), 0)
+    check_attention(shape_of(n_q, n_kv, 64), *attention_case(r, n_q, n_kv, 64, lens, q_lens), lens, q_lens)
+
+
+def test_attention_two_handles_at_once():
+    r = np.random.default_rng(18)
+    shape = shape_of(8, 2, 128)
+    jobs = []
+    for lens, q_lens in (([3000, 40], [300, 1]), ([2000, 500, 7], [1, 200, 7])):
+        pool, bt, q = attention_case(r, 8, 2, 128, lens, q_lens)
+        h = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
+        cache = _lib.KvCache(shape, pool.shape[0], _lib.NF_KV_FP4, torch.from_numpy(pool).to(DEV))
+        args = (h, q.to(DEV), cache, dev32(bt), dev32(lens))
+        begin = dev32(np.concatenate([[0], np.cumsum(q_lens)]))
+        alone = torch.empty(q.shape, dtype=torch.bfloat16, device=DEV)
+        _lib.attention_kv4(*args, alone, begin)
+        jobs.append((args, begin, alone, [torch.empty_like(alone) for _ in range(8)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(8):
+        for args, begin, _, outs, stream in jobs:
+            _lib.attention_kv4(*args, outs[i], begin, stream=stream)
+    torch.cuda.synchronize()
+    for args, _, alone, outs, _ in jobs:
+        args[0].poll()
+        assert all(torch.equal(o, alone) for o in outs)
+
+
+def test_attention_too_many_pages_for_a_call_is_reported():
+    """43 requests of 100,000 pages and 1024 KV heads: past 2^32 (page, head) pairs nothing is written."""
+    shape = shape_of(1024, 1024, 64)
+    pages, n = 100_000, 43
+    h = _lib.Kv4(shape, 1, pages)
+    cache = _lib.KvCache(shape, 1, _lib.NF_KV_FP4, torch.zeros(1, 1024, 2, 576, dtype=torch.uint8, device=DEV))
+    o = torch.full((n, 1024, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    _lib.attention_kv4(h, torch.zeros_like(o), cache, dev32(np.zeros((n, pages))), dev32([16 * pages] * n), o)
+    with pytest.raises(_lib.NanoflowError) as e:
+        h.poll()
+    assert e.value.code == _lib.NF_ERR_DEVICE and "too many" in str(e.value)
+    assert (o == 5.0).all()
+
+
+# ------------------------------------------------------------------ sizes past 32 bits
+
+def test_a_pool_past_32_bits():
+    """A cache of more than 2^32 bytes: append, rows by slot and attention at its far end."""
+    n_q, n_kv, d, num = 32, 8, 128, 240_000
+    shape = shape_of(n_q, n_kv, d)
+    r = np.random.default_rng(19)
+    n = 100
+    x, pos, _ = append_case(r, n, n_q, n_kv, d, num, 1000)
+    slot = num * 16 - 1 - r.permutation(7 * 16)[:n]
+    outs = []
+    for pages, shift in ((num, 0), (7, (num - 7) * 16)):  # the same slots in a pool of the last pages alone
+        pool = torch.full((pages, n_kv, 2, 9 * d), 0x7F, dtype=torch.uint8, device=DEV)
+        cache = _lib.KvCache(shape, pages, _lib.NF_KV_FP4, pool)
+        q = torch.empty(n, n_q, d, dtype=torch.bfloat16, device=DEV)
+        _lib.qk_norm_rope(shape, x.to(DEV), None, None, dev32(pos), dev32(slot - shift), q, cache)
+        k, v = (torch.empty(n, n_kv, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        _lib.kv4_read(shape, cache, dev32(slot - shift), k, v)
+        pool[-7:, :, :, 8 * d:][pool[-7:, :, :, 8 * d:] == 0x7F] = 0x30
+        o = torch.empty(40, n_q, d, dtype=torch.bfloat16, device=DEV)
+        h = _lib.Kv4(shape, pages, 3)
+        bt = dev32([[num - 1, num - 4, num - 2], [num - 7, num - 3, num - 6]]) - shift // 16
+        _lib.attention_kv4(h, q[:40], cache, bt, dev32([45, 48]), o, dev32([0, 5, 40]))
+        h.poll()
+        outs.append([pool[-7:].clone(), q, k, v, o])
+        del pool, cache
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert np.array_equal(host(outs[0][2].float())[0].astype(float), orc.take(host(outs[1][0]), [int(slot[0]) - (num - 7) * 16], 0, 0)[0])
+
+
+def test_rows_past_32_bits():
+    """Rows whose offsets in qkv, q and the read-out pass 2^32 bytes give what they give in a small call."""
+    shape = shape_of(32, 8, 128)
+    n, tail = 400_000, 50
+    g = torch.Generator(device=DEV).manual_seed(20)
+    x = torch.zeros(n, 48 * 128, dtype=torch.bfloat16, device=DEV)
+    x[-tail:] = torch.randn(tail, 48 * 128, generator=g, device=DEV).to(torch.bfloat16)
+    slot = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    slot[-tail:] = torch.arange(tail, dtype=torch.int32, device=DEV)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    outs = []
+    for m in (n, tail):
+        pool = torch.zeros(4, 8, 2, 9 * 128, dtype=torch.uint8, device=DEV)
+        q = torch.empty(m, 32, 128, dtype=torch.bfloat16, device=DEV)
+        _lib.qk_norm_rope(shape, x[-m:], None, None, pos[-m:].contiguous(), slot[-m:].contiguous(), q, _lib.KvCache(shape, 4, _lib.NF_KV_FP4, pool))
+        outs.append([pool, q[-tail:].clone()])
+        del q
+    del x
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    n = 2_200_000
+    k, v = (torch.empty(n, 8, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    slots = torch.arange(n, dtype=torch.int32, device=DEV) % 64
+    cache = _lib.KvCache(shape, 4, _lib.NF_KV_FP4, outs[0][0])
+    _lib.kv4_read(shape, cache, slots, k, v)
+    ks, vs = (torch.empty(64, 8, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    _lib.kv4_read(shape, cache, slots[:64].contiguous(), ks, vs)
+    assert ks.any() and all(torch.equal(a[-64:], b.roll(-(n % 64), 0)) for a, b in ((k, ks), (v, vs)))
 
 
 # ------------------------------------------------------------------ together
