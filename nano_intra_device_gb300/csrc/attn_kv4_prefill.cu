@@ -63,10 +63,12 @@ struct KpBars {
   uint64_t p_free;                           // a PV product finished
   uint64_t drain;
   uint64_t meet;                             // KP_SM_THREADS arrivals: the softmax threads
+  uint64_t pair[4];                          // 64 arrivals: both warps of 32 rows have a block's maxima
   uint32_t tmem_base;
   int abort, last;
   uint32_t v_nan[KP_VST][4];                 // positions whose V holds a NaN that not every row sees
   float xch[2][KP_M];                        // the two halves of a row exchange their sums
+  float top[2][2][KP_M];                     // and, by the block's parity, their maxima
   long long warp_sum[KP_WARPS];
   long long base;                            // where this CTA starts: a request's first slot
   int seq;                                   // and the request
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     mbar_init(&bars->p_full, KP_SM_THREADS);
     mbar_init(&bars->p_free, 1);
     mbar_init(&bars->drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->pair[i], 64);
     mbar_init(&bars->meet, KP_SM_THREADS);
     bars->abort = 0;
     fence_mbar_init();
@@ -555,37 +558,45 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           break;
         }
         tc_fence_after();
-        // this half's 64 scores, and the other half's for the row maximum
+        // this half's 64 scores; the row maximum by way of shared memory
         float x[KP_H];
-        float mx8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
         const bool mixed = j * KP_N + KP_N - 1 > p.pos0;  // some row sees less than the block (uniform)
         {
-          uint32_t w[32];
-          const int kb_own = j * KP_N + half * KP_H, kb_oth = j * KP_N + (half ^ 1) * KP_H;
-          const uint32_t own = tmem + lane_off + s * KP_N + half * KP_H, oth = tmem + lane_off + s * KP_N + (half ^ 1) * KP_H;
+          const uint32_t own = tmem + lane_off + s * KP_N + half * KP_H;
           tc_ld_32x32b_x32(own, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
           tc_ld_32x32b_x32(own + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {  // the other half in two parts, for the maximum only
-            tc_ld_32x32b_x32(oth + 32 * c, w);
-            tc_wait_ld();
-            if (!mixed) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) mx8[i & 7] = kp_max3(mx8[i & 7], x[32 * c + i], __uint_as_float(w[i]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (kb_own + 32 * c + i > qpos) x[32 * c + i] = -INFINITY;
-                mx8[i & 7] = kp_max3(mx8[i & 7], x[32 * c + i], kb_oth + 32 * c + i > qpos ? -INFINITY : __uint_as_float(w[i]));
-              }
-            }
-          }
+          tc_wait_ld();
           tc_fence_before();
           mbar_arrive(&bars->s_free[s]);
         }
-        const float mx = kp_max3(kp_max3(mx8[0], mx8[1], mx8[2]), kp_max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * scale;
+        if (mixed) {
+          const int kb = j * KP_N + half * KP_H;
+#pragma unroll
+          for (int i = 0; i < KP_H; ++i)
+            if (kb + i > qpos) x[i] = -INFINITY;
+        }
+        float mx;
+        {
+          float mx8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx8[i] = kp_max3(x[i], x[8 + i], x[16 + i]);
+#pragma unroll
+          for (int i = 24; i < KP_H - 8; i += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx8[k] = kp_max3(mx8[k], x[i + k], x[i + 8 + k]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], x[KP_H - 8 + k]);
+          mx = kp_max3(kp_max3(mx8[0], mx8[1], mx8[2]), kp_max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+          // a slot is written again only after the other half has read it: its next
+          // arrival, which this thread waits for in between, follows its read
+          bars->top[s][half][r] = mx;
+          mbar_arrive(&bars->pair[quarter]);
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->pair[quarter], n & 1, tmo, abort_flag))) {
+            ok = false;
+            break;
+          }
+          mx = fmaxf(mx, bars->top[s][half ^ 1][r]) * scale;
+        }
         float corr = 1.f;
         if (mx > m_ref + KP_SLACK) {  // also from -inf, where O and l are still zero
           corr = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mx);
