@@ -233,13 +233,17 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
     }
     if (all > 0xFFF00000ll) {  // 10 TB of pages: not a call that ends
       if (blockIdx.x == 0 && tid == 0) raise_status(a.status, ST_OVERFLOW);
+      pdl_wait();
       return;
     }
     total = static_cast<uint32_t>(all);
     const uint32_t n_warps = gridDim.x * KA_WARPS;
     quota = max((total + n_warps - 1) / n_warps, KA_MIN_QUOTA);
     const uint32_t cta0 = blockIdx.x * KA_WARPS * quota;
-    if (cta0 >= total) return;  // nothing for this CTA
+    if (cta0 >= total) {  // nothing for this CTA
+      pdl_wait();
+      return;
+    }
     // the thread whose requests hold a warp's first slot says where it starts
     uint32_t at = static_cast<uint32_t>(before);
     if (sum > 0 && at < cta0 + KA_WARPS * quota && at + static_cast<uint32_t>(sum) > cta0) {
@@ -701,7 +705,10 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
   // ---- units cut between CTAs: at most the first and the last run
   __threadfence();
   __syncthreads();
-  if (starts == 0) return;
+  if (starts == 0) {
+    pdl_wait();
+    return;
+  }
   const int e_first = __ffs(starts) - 1, e_last = 31 - __clz(starts);
   for (int k = 0; k < 2; ++k) {
     if (k == 1 && e_last == e_first) break;
@@ -762,15 +769,28 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
     }
     __syncthreads();
   }
+  pdl_wait();
 }
 
+// Behind the tiles' launch the CTAs start on the SMs that it leaves: the two
+// touch no common data, so only the end waits (pdl_wait at every exit; a no-op
+// otherwise), which makes the stream's next launch wait for both.
 template <int GRP, int D>
-cudaError_t launch_t(const Kv4AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_t(const Kv4AttnArgs& a, bool behind, cudaStream_t stream) {
   const int smem = KaLayout<D>::SMEM;
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(attn_kv4_kernel<GRP, D>), smem);
   if (e != cudaSuccess) return e;
-  attn_kv4_kernel<GRP, D><<<a.grid, KA_THREADS, smem, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.grid), 1, 1);
+  cfg.blockDim = dim3(KA_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<GRP, D>, a);
 }
 
 }  // namespace
@@ -779,10 +799,10 @@ size_t kv4_record_bytes(int head_dim) {
   return (head_dim == 128 ? KaLayout<128>::REC : KaLayout<64>::REC) * sizeof(float);
 }
 
-cudaError_t launch_attention_kv4(const Kv4AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_attention_kv4(const Kv4AttnArgs& a, bool behind, cudaStream_t stream) {
   const int grp = a.n_q / a.n_kv;
 #define NF_KV4_CASE(G)                                          \
-  if (grp == G) return a.head_dim == 128 ? launch_t<G, 128>(a, stream) : launch_t<G, 64>(a, stream);
+  if (grp == G) return a.head_dim == 128 ? launch_t<G, 128>(a, behind, stream) : launch_t<G, 64>(a, behind, stream);
   NF_KV4_CASE(1) NF_KV4_CASE(2) NF_KV4_CASE(4) NF_KV4_CASE(8)
 #undef NF_KV4_CASE
   return cudaErrorInvalidValue;

@@ -43,7 +43,6 @@ constexpr int KP_THREADS = KP_WARPS * 32;
 // 512 = 4 x 128 registers a thread at launch, dealt again by role
 constexpr int KP_DQ_REGS = 112, KP_SM_REGS = 160, KP_MMA_REGS = 80;
 static_assert(KP_DQ_REGS + 2 * KP_SM_REGS + KP_MMA_REGS == 512, "the shares of the launch's registers");
-constexpr int KP_SM_THREADS = KP_SM_WARPS * 32;
 constexpr int KP_M = 128;            // query vectors of a tile (tensor-memory lanes)
 constexpr int KP_N = 128;            // positions of a key block
 constexpr int KP_H = KP_N / 2;       // positions of a block one softmax thread owns
@@ -55,15 +54,15 @@ constexpr uint32_t KP_TMEM_COLS = 512;
 constexpr int KP_KST = 2, KP_VST = 2;  // ring stages of K and V
 
 struct KpBars {
-  uint64_t q_full;                           // KP_SM_THREADS arrivals: Q of a piece written
-  uint64_t k_full[KP_KST], k_empty[KP_KST];  // full: 64 arrivals (two warps)
+  uint64_t q_full;                           // every softmax warp: Q of a piece written
+  uint64_t k_full[KP_KST], k_empty[KP_KST];  // full: two warps
   uint64_t v_full[KP_VST], v_empty[KP_VST];
-  uint64_t s_full[2], s_free[2];             // S accumulators (free: KP_SM_THREADS arrivals)
-  uint64_t p_full;                           // KP_SM_THREADS arrivals: P written (and O rescaled)
+  uint64_t s_full[2], s_free[2];             // S accumulators (free: every softmax warp)
+  uint64_t p_full;                           // every softmax warp: P written (and O rescaled)
   uint64_t p_free;                           // a PV product finished
   uint64_t drain;
-  uint64_t meet;                             // KP_SM_THREADS arrivals: the softmax threads
-  uint64_t pair[4];                          // 64 arrivals: both warps of 32 rows have a block's maxima
+  uint64_t meet;                             // the softmax warps
+  uint64_t pair[4];                          // both warps of 32 rows have a block's maxima
   uint32_t tmem_base;
   int abort, last;
   uint32_t v_nan[KP_VST][4];                 // positions whose V holds a NaN that not every row sees
@@ -217,6 +216,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t tmo = a.timeout_ns;
 
+  pdl_trigger();  // the launch of few rows takes the SMs that this one leaves
+
   // ---- the slots of every request: thread i sums the requests [i c, (i + 1) c)
   KpWalk<GRP> walk;
   long long quota;
@@ -260,25 +261,25 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
   }
 
   if (tid == 0) {
-    mbar_init(&bars->q_full, KP_SM_THREADS);
+    mbar_init(&bars->q_full, KP_SM_WARPS);
     for (int i = 0; i < KP_KST; ++i) {
-      mbar_init(&bars->k_full[i], 64);
+      mbar_init(&bars->k_full[i], 2);
       mbar_init(&bars->k_empty[i], 1);
     }
     for (int i = 0; i < KP_VST; ++i) {
-      mbar_init(&bars->v_full[i], 64);
+      mbar_init(&bars->v_full[i], 2);
       mbar_init(&bars->v_empty[i], 1);
       for (int k = 0; k < 4; ++k) bars->v_nan[i][k] = 0;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->s_free[i], KP_SM_THREADS);
+      mbar_init(&bars->s_free[i], KP_SM_WARPS);
     }
-    mbar_init(&bars->p_full, KP_SM_THREADS);
+    mbar_init(&bars->p_full, KP_SM_WARPS);
     mbar_init(&bars->p_free, 1);
     mbar_init(&bars->drain, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&bars->pair[i], 64);
-    mbar_init(&bars->meet, KP_SM_THREADS);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->pair[i], 2);
+    mbar_init(&bars->meet, KP_SM_WARPS);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -297,6 +298,15 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
   auto give_up = [&]() {
     raise_status(a.status, ST_TIMEOUT);
     *abort_flag = 1;
+  };
+  // One arrival and one poll a warp: the arrivals of 32 lanes go one after the
+  // other.  What a lane wrote before is ordered by the warp's barrier.
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
   };
   KpPiece p;
 
@@ -379,7 +389,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     uint32_t n = 0;  // blocks made
     while (made.have) {
       const uint32_t st = n % nst;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((n / nst) & 1) ^ 1, tmo, abort_flag))) {
+      if (!wait(&empty[st], ((n / nst) & 1) ^ 1)) {
         if (!*abort_flag) give_up();
         break;
       }
@@ -433,7 +443,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&full[st]);
+      arrive(&full[st]);
       ++n;
       load_codes();
       load_ids();
@@ -507,11 +517,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     uint32_t n = 0, met = 0;           // blocks done; meetings
     bool ok = true;
     auto pv_done = [&](uint32_t i) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(&bars->p_free, i & 1, tmo, abort_flag));
+      return wait(&bars->p_free, i & 1);
     };
     auto meet = [&]() -> bool {  // a bounded barrier of the softmax threads
-      mbar_arrive(&bars->meet);
-      const bool good = __all_sync(0xffffffffu, mbar_wait(&bars->meet, met & 1, tmo, abort_flag));
+      arrive(&bars->meet);
+      const bool good = wait(&bars->meet, met & 1);
       ++met;
       return good;
     };
@@ -548,12 +558,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
                              kp_pack(bf16lo(v.z) * mul, bf16hi(v.z) * mul), kp_pack(bf16lo(v.w) * mul, bf16hi(v.w) * mul)));
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bars->q_full);
+        arrive(&bars->q_full);
       }
       float m_ref = -INFINITY, l = 0.f;
       for (int j = p.j0; j < p.j1; ++j, ++n) {
         const uint32_t s = n & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[s], (n >> 1) & 1, tmo, abort_flag))) {
+        if (!wait(&bars->s_full[s], (n >> 1) & 1)) {
           ok = false;
           break;
         }
@@ -567,7 +577,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           tc_ld_32x32b_x32(own + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
           tc_wait_ld();
           tc_fence_before();
-          mbar_arrive(&bars->s_free[s]);
+          arrive(&bars->s_free[s]);
         }
         if (mixed) {
           const int kb = j * KP_N + half * KP_H;
@@ -590,8 +600,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           // a slot is written again only after the other half has read it: its next
           // arrival, which this thread waits for in between, follows its read
           bars->top[s][half][r] = mx;
-          mbar_arrive(&bars->pair[quarter]);
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars->pair[quarter], n & 1, tmo, abort_flag))) {
+          arrive(&bars->pair[quarter]);
+          if (!wait(&bars->pair[quarter], n & 1)) {
             ok = false;
             break;
           }
@@ -622,7 +632,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         if (mixed) {
           // NaN of V at positions that not every row sees: to the rows that do
           const uint32_t vs = n % KP_VST;
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (n / KP_VST) & 1, tmo, abort_flag))) {
+          if (!wait(&bars->v_full[vs], (n / KP_VST) & 1)) {
             ok = false;
             break;
           }
@@ -633,15 +643,6 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
             for (int i = 0; i < KP_H; ++i)
               if ((((i < 32 ? nan0 : nan1) >> (i & 31)) & 1) && kb + i <= qpos) x[i] = __int_as_float(0x7FC00000);
           }
-        }
-        {
-          float2 ls4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < KP_H / 2; ++i) ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(x[2 * i], x[2 * i + 1]));
-          const float2 a2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
-          l += a2.x + a2.y;
         }
         // a raised maximum rescales this half of the row of O, once the PV
         // product of the previous block is done with it
@@ -676,7 +677,16 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
                                                      kp_pack(x[8 * c + 4], x[8 * c + 5]), kp_pack(x[8 * c + 6], x[8 * c + 7])));
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&bars->p_full);
+        arrive(&bars->p_full);
+        {
+          float2 ls4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < KP_H / 2; ++i) ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(x[2 * i], x[2 * i + 1]));
+          const float2 a2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
+          l += a2.x + a2.y;
+        }
       }
       if (ok && !pv_done(n - 1)) ok = false;
       if (!ok) break;

@@ -332,8 +332,8 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
   a.tiles = h->tiles;
   a.tile_counters = h->tile_counters;
   a.small_rows = kSmallVecs / (a.n_q / a.n_kv);
-  if (tok_begin && n_tok > a.small_rows)
-    NF_CUDA4(nf::launch_attention_kv4_prefill(a, static_cast<cudaStream_t>(stream)));
-  NF_CUDA4(nf::launch_attention_kv4(a, static_cast<cudaStream_t>(stream)));
+  const bool tiles = tok_begin && n_tok > a.small_rows;
+  if (tiles) NF_CUDA4(nf::launch_attention_kv4_prefill(a, static_cast<cudaStream_t>(stream)));
+  NF_CUDA4(nf::launch_attention_kv4(a, tiles, static_cast<cudaStream_t>(stream)));
   return NF_OK;
 }

@@ -75,6 +75,7 @@ struct Kv4AttnArgs {
 size_t kv4_record_bytes(int head_dim);
 size_t kv4_tile_record_bytes(int head_dim);
 cudaError_t launch_attention_kv4_prefill(const Kv4AttnArgs& a, cudaStream_t stream);
-cudaError_t launch_attention_kv4(const Kv4AttnArgs& a, cudaStream_t stream);
+// behind: the stream's last launch is this call's tiles
+cudaError_t launch_attention_kv4(const Kv4AttnArgs& a, bool behind, cudaStream_t stream);
 
 }  // namespace nf
