@@ -51,7 +51,7 @@ constexpr int KP_FIXED = 1;          // blocks' worth of a unit's fixed cost
 constexpr float KP_SLACK = 8.f;
 constexpr float KP_SHIFT = 7.f;
 constexpr uint32_t KP_TMEM_COLS = 512;
-constexpr int KP_KST = 2, KP_VST = 2;  // ring stages of K and V
+constexpr int KP_KST = 2, KP_VST = 1;  // ring stages of K and V
 
 struct KpBars {
   uint64_t q_full;                           // every softmax warp: Q of a piece written
@@ -66,7 +66,7 @@ struct KpBars {
   uint32_t tmem_base;
   int abort, last;
   uint32_t v_nan[KP_VST][4];                 // positions whose V holds a NaN that not every row sees
-  float xch[2][KP_M];                        // the two halves of a row exchange their sums
+  float xch[2][2][KP_M];                      // the two halves of a row exchange their sums
   float top[2][2][KP_M];                     // and, by the block's parity, their maxima
   long long warp_sum[KP_WARPS];
   long long base;                            // where this CTA starts: a request's first slot
@@ -80,12 +80,13 @@ struct KpLayout {
   static constexpr int KV_BYTES = NCH * KP_REGION;  // 16 groups of 8 positions, each [d/64][8][128 B]
   static constexpr int KV_GROUP = NCH * 1024;
   static constexpr int P_BYTES = 2 * KP_REGION;     // [keys/64][128 vectors][128 B]
-  static constexpr int K_OFF = Q_BYTES;
+  static constexpr int K_OFF = 2 * Q_BYTES;
   static constexpr int V_OFF = K_OFF + KP_KST * KV_BYTES;
   static constexpr int P_OFF = V_OFF + KP_VST * KV_BYTES;
   static constexpr int BAR_OFF = P_OFF + P_BYTES;
   static constexpr int SMEM = 1024 + BAR_OFF + static_cast<int>(sizeof(KpBars));
-  static constexpr int REC = KP_M * D + 2 * KP_M;   // floats of a record: O, m, l
+  static constexpr int TREC = KP_M * D + 2 * KP_M;  // floats of a tile's record: O, m, l
+  static constexpr int REC = 2 * TREC;
 };
 
 __device__ __forceinline__ uint32_t kp_sw128(int r, int c) {
@@ -118,37 +119,51 @@ constexpr uint32_t kp_idesc(int M, int N, bool b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24) | (b_mn ? 1u << 16 : 0u);
 }
 
-// Blocks of the tile whose last row's limit is k steps of R = 128 / g positions
-// (at least one), and their sum over 1 .. m (m <= 0: minus one a step).
-__device__ __forceinline__ long long kp_blocks(long long k, int g) { return k <= 0 ? 1 : (k + g - 1) / g; }
-__device__ __forceinline__ long long kp_sum(long long m, int g) {
+// A unit is R = 256 / GRP rows.  Its last row's limit lies k steps of R positions
+// past a multiple of R: ceil(k / h) blocks, h = 128 / R, at least one; kp_sum is
+// their sum over 1 .. m (m <= 0: minus one a step).  At GRP = 1 the step is a
+// block, two a unit.
+__device__ __forceinline__ long long kp_sum(long long m, int h) {
   if (m <= 0) return m;
-  const long long q = m / g, r = m % g;
-  return g * q * (q + 1) / 2 + r * (q + 1);
+  const long long q = m / h, r = m % h;
+  return h * q * (q + 1) / 2 + r * (q + 1);
 }
 
 struct KpSeq {
-  int b0, rows, len, tiles;
-  long long c;  // steps of R up to the last row of tile 0
+  int b0, rows, len, units;
+  long long c;  // steps up to the first row
 };
 template <int GRP>
 __device__ __forceinline__ KpSeq kp_seq(const Kv4AttnArgs& a, int s) {
-  constexpr int R = KP_M / GRP;
+  constexpr int R = 2 * KP_M / GRP, U = R < KP_N ? R : KP_N;
   KpSeq q;
   const int b0 = a.tok_begin[s], b1 = a.tok_begin[s + 1];
   q.b0 = b0;
   q.rows = b0 < 0 || b1 < b0 || b1 > a.n_tok ? 0 : b1 - b0;
   q.len = a.seq_lens[s];
   if (q.len < 0 || q.len > static_cast<long long>(a.max_pages) * KV4_P) q.len = 0;
-  q.tiles = q.rows > a.small_rows ? (q.rows + R - 1) / R : 0;
+  q.units = q.rows > a.small_rows ? (q.rows + R - 1) / R : 0;
   const int first = q.len - q.rows;  // position of the first row
-  q.c = (first >= 0 ? (first + R - 1) / R : -(-first / R)) + 1;
+  q.c = first >= 0 ? (first + U - 1) / U : -(-first / U);
   return q;
 }
-// Slots before tile i of a request.
+template <int GRP>
+__device__ __forceinline__ long long kp_blocks(const KpSeq& q, int i) {
+  const long long k = GRP == 1 ? q.c + 2 * (i + 1LL) : q.c + i + 1;
+  constexpr int h = GRP == 1 ? 1 : GRP / 2;
+  return k <= 0 ? 1 : (k + h - 1) / h;
+}
+// Slots before unit i of a request.
 template <int GRP>
 __device__ __forceinline__ long long kp_before(const KpSeq& q, int i, int n_kv) {
-  return n_kv * (kp_sum(q.c + i - 1, GRP) - kp_sum(q.c - 1, GRP) + static_cast<long long>(i) * KP_FIXED);
+  long long blocks;
+  if (GRP == 1) {
+    const long long one = min(static_cast<long long>(i), q.c < 0 ? -q.c / 2 : 0);  // units of one block
+    blocks = one + (i - one) * q.c + i * (i + 1LL) - one * (one + 1);
+  } else {
+    blocks = kp_sum(q.c + i, GRP / 2) - kp_sum(q.c, GRP / 2);
+  }
+  return n_kv * (blocks + static_cast<long long>(i) * KP_FIXED);
 }
 
 struct KpPiece {
@@ -158,6 +173,7 @@ struct KpPiece {
   int pos0;           // position of row0 (may be negative)
   int len;            // positions of the request
   int nb, j0, j1;     // blocks of the unit, and those of this piece
+  int nt;             // tiles of the unit: 1 or 2
 };
 
 // Walks the pieces of a CTA's slots; every warp keeps one.
@@ -167,29 +183,30 @@ struct KpWalk {
   int s;
   KpSeq q;
   __device__ __forceinline__ bool next(const Kv4AttnArgs& a, KpPiece& p) {
-    constexpr int R = KP_M / GRP;
+    constexpr int R = 2 * KP_M / GRP;
     while (x < end) {
-      const long long all = kp_before<GRP>(q, q.tiles, a.n_kv);
+      const long long all = kp_before<GRP>(q, q.units, a.n_kv);
       if (x >= base + all) {
         base += all;
         if (++s >= a.n_seq) return false;
         q = kp_seq<GRP>(a, s);
         continue;
       }
-      int lo = 0, hi = q.tiles - 1;  // the last tile that starts at or before x
+      int lo = 0, hi = q.units - 1;  // the last unit that starts at or before x
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (base + kp_before<GRP>(q, mid, a.n_kv) <= x) lo = mid;
         else hi = mid - 1;
       }
       const long long t0 = base + kp_before<GRP>(q, lo, a.n_kv);
-      p.nb = static_cast<int>(kp_blocks(q.c + lo, GRP));
+      p.nb = static_cast<int>(kp_blocks<GRP>(q, lo));
       const int per = p.nb + KP_FIXED;
       p.g = static_cast<int>((x - t0) / per);
       p.key = t0 + static_cast<long long>(p.g) * per;
       p.s = s;
       p.row0 = q.b0 + lo * R;
       p.rows = min(R, q.rows - lo * R);
+      p.nt = p.rows > R / 2 ? 2 : 1;
       p.pos0 = q.len - q.rows + lo * R;
       p.len = q.len;
       const int off = static_cast<int>(x - p.key);
@@ -227,7 +244,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     long long sum = 0;
     for (int s = s0; s < s1; ++s) {
       const KpSeq q = kp_seq<GRP>(a, s);
-      sum += kp_before<GRP>(q, q.tiles, a.n_kv);
+      sum += kp_before<GRP>(q, q.units, a.n_kv);
     }
     long long in = sum;
 #pragma unroll
@@ -248,7 +265,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     if (at <= x && x < at + sum)
       for (int s = s0; s < s1; ++s) {
         const KpSeq q = kp_seq<GRP>(a, s);
-        const long long n = kp_before<GRP>(q, q.tiles, a.n_kv);
+        const long long n = kp_before<GRP>(q, q.units, a.n_kv);
         if (x < at + n) {
           bars->base = at;
           bars->seq = s;
@@ -453,48 +470,60 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     // ------------------------------------------------------------ MMA issuer
     const uint32_t q_addr = sbase, p_addr = sbase + Lay::P_OFF, o_tmem = tmem + 256;
     bool ok = true, any = false;
-    uint32_t n = 0, np = 0;  // blocks whose S was issued; pieces
-    auto pv = [&](uint32_t i, bool first) -> bool {
-      const uint32_t s = i % KP_VST;
-      if (!mbar_wait(&bars->v_full[s], (i / KP_VST) & 1, tmo, abort_flag)) return false;
-      if (!mbar_wait(&bars->p_full, i & 1, tmo, abort_flag)) return false;
+    uint32_t i = 0, n = 0, np = 0;  // S products issued, blocks begun and ended; pieces
+    // the PV product that follows the S product of the next step
+    uint32_t vt = 0, vn = 0;        // its tile and block
+    bool vfirst = false;            // the first of its piece
+    auto pv = [&](uint32_t step, int nt) -> bool {
+      const uint32_t s = vn % KP_VST;
+      if (vt == 0 && !mbar_wait(&bars->v_full[s], (vn / KP_VST) & 1, tmo, abort_flag)) return false;
+      if (!mbar_wait(&bars->p_full, step & 1, tmo, abort_flag)) return false;
       tc_fence_after();
       const uint32_t v_addr = sbase + Lay::V_OFF + s * Lay::KV_BYTES;
 #pragma unroll
       for (int kk = 0; kk < KP_N / 16; ++kk) {
         const uint64_t bdesc = desc_sw128_mnmajor(v_addr + kk * 2 * Lay::KV_GROUP, 1024, Lay::KV_GROUP);
         const uint64_t adesc = desc_sw128_kmajor(p_addr + (kk >> 2) * KP_REGION) + 2 * (kk & 3);
-        tc_mma_bf16(o_tmem, adesc, bdesc, IDESC_PV, !first || kk > 0);
+        tc_mma_bf16(o_tmem + vt * D, adesc, bdesc, IDESC_PV, !vfirst || kk > 0);
       }
       any = true;
       tc_commit(&bars->p_free);
-      tc_commit(&bars->v_empty[s]);
+      if (static_cast<int>(vt) == nt - 1) tc_commit(&bars->v_empty[s]);
       return true;
     };
     while (warp == KP_MMA_WARP && ok && walk.next(a, p)) {
       if (lane == 0) {
         ok = mbar_wait(&bars->q_full, np & 1, tmo, abort_flag);
         for (int j = p.j0; j < p.j1 && ok; ++j, ++n) {
-          const uint32_t s = n & 1, ks = n % KP_KST;
-          ok = mbar_wait(&bars->k_full[ks], (n / KP_KST) & 1, tmo, abort_flag) &&
-               mbar_wait(&bars->s_free[s], ((n >> 1) & 1) ^ 1, tmo, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t k_addr = sbase + Lay::K_OFF + ks * Lay::KV_BYTES;
+          const uint32_t ks = n % KP_KST;
+          for (int t = 0; t < p.nt; ++t, ++i) {
+            const uint32_t s = i & 1;
+            ok = (t > 0 || mbar_wait(&bars->k_full[ks], (n / KP_KST) & 1, tmo, abort_flag)) &&
+                 mbar_wait(&bars->s_free[s], ((i >> 1) & 1) ^ 1, tmo, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t k_addr = sbase + Lay::K_OFF + ks * Lay::KV_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t adesc = desc_sw128_kmajor(q_addr + (kk >> 2) * KP_REGION) + 2 * (kk & 3);
-            const uint64_t bdesc = desc_sw128_kmajor_sbo(k_addr + (kk >> 2) * 1024, Lay::KV_GROUP) + 2 * (kk & 3);
-            tc_mma_bf16(tmem + s * KP_N, adesc, bdesc, IDESC_S, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t adesc = desc_sw128_kmajor(q_addr + t * Lay::Q_BYTES + (kk >> 2) * KP_REGION) + 2 * (kk & 3);
+              const uint64_t bdesc = desc_sw128_kmajor_sbo(k_addr + (kk >> 2) * 1024, Lay::KV_GROUP) + 2 * (kk & 3);
+              tc_mma_bf16(tmem + s * KP_N, adesc, bdesc, IDESC_S, kk > 0);
+            }
+            any = true;
+            tc_commit(&bars->s_full[s]);
+            if (t == p.nt - 1) tc_commit(&bars->k_empty[ks]);
+            if (j > p.j0 || t > 0) {
+              ok = pv(i - 1, p.nt);
+              if (!ok) break;
+            }
+            vt = t;
+            vn = n;
+            vfirst = j == p.j0;
           }
-          any = true;
-          tc_commit(&bars->s_full[s]);
-          tc_commit(&bars->k_empty[ks]);
-          if (j > p.j0) ok = pv(n - 1, j - 1 == p.j0);
         }
         // the unit's last product before the next one's Q is waited for: its
         // epilogue comes first
-        if (ok) ok = pv(n - 1, p.j1 - 1 == p.j0);
+        if (ok) ok = pv(i - 1, p.nt);
         ++np;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -514,7 +543,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     const int half = sw >> 2;          // which 64 keys of a block (and d/2 of O) it owns
     const int r = quarter * 32 + lane; // the vector (lane) this thread owns
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    uint32_t n = 0, met = 0;           // blocks done; meetings
+    uint32_t n = 0, blk = 0, met = 0;  // steps done; blocks done; meetings
     bool ok = true;
     auto pv_done = [&](uint32_t i) -> bool {
       return wait(&bars->p_free, i & 1);
@@ -526,14 +555,27 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
       return good;
     };
     while (ok && walk.next(a, p)) {
-      const int ri = r / GRP;
-      const bool live = ri < p.rows;
-      const int qrow = p.row0 + (live ? ri : 0), qh = p.g * GRP + r % GRP;
-      const int qpos = live ? p.pos0 + ri : -1;  // sees positions 0 .. qpos
-      // Q: this half of the vector, scaled to fp16's range by its largest element
-      float scale;
-      {
-        const uint4* q4 = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(qrow) * a.n_q + qh) * D);
+      constexpr int RT = KP_M / GRP;  // rows of a tile
+      // the state of the tile at hand, and of the other one
+      float scale = 0.f, scale_b = 0.f, m_ref = -INFINITY, m_b = -INFINITY, l = 0.f, l_b = 0.f;
+      int qpos = -1, qpos_b = -1;  // the row sees positions 0 .. qpos
+      auto other = [&]() {
+        float f = scale; scale = scale_b; scale_b = f;
+        f = m_ref; m_ref = m_b; m_b = f;
+        f = l; l = l_b; l_b = f;
+        const int i = qpos; qpos = qpos_b; qpos_b = i;
+      };
+      auto row_of = [&](int t) { return t * RT + r / GRP; };
+      auto row_at = [&](int t) {  // of q and o; a row that is not there: the unit's first
+        return (static_cast<size_t>(p.row0 + (row_of(t) < p.rows ? row_of(t) : 0)) * a.n_q + p.g * GRP + r % GRP) * D;
+      };
+      // Q: this half of the vectors, scaled to fp16's range by their largest element
+#pragma unroll 1
+      for (int t = 0; t < p.nt; ++t) {
+        const bool live = row_of(t) < p.rows;
+        if (t > 0) other();
+        qpos = live ? p.pos0 + row_of(t) : -1;
+        const uint4* q4 = reinterpret_cast<const uint4*>(a.q + row_at(t));
         float top = 0.f;
         uint4 own[D / 16];
 #pragma unroll
@@ -553,15 +595,16 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         for (int i = 0; i < D / 16; ++i) {
           const int c = half * (D / 16) + i;
           const uint4 v = own[i];
-          kp_st16(sbase + (c >> 3) * KP_REGION + kp_sw128(r, c & 7),
+          kp_st16(sbase + t * Lay::Q_BYTES + (c >> 3) * KP_REGION + kp_sw128(r, c & 7),
                   make_uint4(kp_pack(bf16lo(v.x) * mul, bf16hi(v.x) * mul), kp_pack(bf16lo(v.y) * mul, bf16hi(v.y) * mul),
                              kp_pack(bf16lo(v.z) * mul, bf16hi(v.z) * mul), kp_pack(bf16lo(v.w) * mul, bf16hi(v.w) * mul)));
         }
-        fence_proxy_async_smem();
-        arrive(&bars->q_full);
       }
-      float m_ref = -INFINITY, l = 0.f;
-      for (int j = p.j0; j < p.j1; ++j, ++n) {
+      if (p.nt == 2) other();
+      fence_proxy_async_smem();
+      arrive(&bars->q_full);
+      int j = p.j0, t = 0;
+      while (j < p.j1) {
         const uint32_t s = n & 1;
         if (!wait(&bars->s_full[s], (n >> 1) & 1)) {
           ok = false;
@@ -631,8 +674,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         }
         if (mixed) {
           // NaN of V at positions that not every row sees: to the rows that do
-          const uint32_t vs = n % KP_VST;
-          if (!wait(&bars->v_full[vs], (n / KP_VST) & 1)) {
+          const uint32_t vs = blk % KP_VST;
+          if (!wait(&bars->v_full[vs], (blk / KP_VST) & 1)) {
             ok = false;
             break;
           }
@@ -655,7 +698,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           uint32_t u[32];
 #pragma unroll 1
           for (int c = 0; c < D / 64; ++c) {
-            const uint32_t ta = tmem + lane_off + 256 + half * (D / 2) + c * 32;
+            const uint32_t ta = tmem + lane_off + 256 + t * D + half * (D / 2) + c * 32;
             tc_ld_32x32b_x32(ta, u);
             tc_wait_ld();
 #pragma unroll
@@ -666,7 +709,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         }
         // P (free once the previous PV product is done), K-major in the 128-byte
         // swizzle: this half's 64 keys fill one region
-        if (j > p.j0 && !pv_done(n - 1)) {
+        if ((j > p.j0 || t > 0) && !pv_done(n - 1)) {
           ok = false;
           break;
         }
@@ -687,51 +730,65 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           const float2 a2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
           l += a2.x + a2.y;
         }
+        ++n;
+        if (p.nt == 2) other();
+        if (++t == p.nt) {
+          t = 0;
+          ++j;
+          ++blk;
+        }
       }
       if (ok && !pv_done(n - 1)) ok = false;
       if (!ok) break;
       tc_fence_after();
-      bars->xch[half][r] = l;
+      bars->xch[0][half][r] = l;
+      bars->xch[1][half][r] = l_b;
       if (!(ok = meet())) break;
-      const float L = bars->xch[0][r] + bars->xch[1][r];
-      uint4* dst = reinterpret_cast<uint4*>(a.o + (static_cast<size_t>(qrow) * a.n_q + qh) * D + half * (D / 2));
       const bool whole = p.j0 == 0 && p.j1 == p.nb;
       const int first = static_cast<int>((p.key + KP_FIXED) / quota);
       const int last = static_cast<int>((p.key + KP_FIXED + p.nb - 1) / quota);
       auto rec_of = [&](int cta) { return a.tiles + (static_cast<size_t>(cta) * 2 + (cta == first ? 1 : 0)) * Lay::REC; };
       float* rec = rec_of(blockIdx.x);
-      const float inv = L == 0.f ? 0.f : a.v_scale / L;
 #pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t u[32];
-        tc_ld_32x32b_x32(tmem + lane_off + 256 + half * (D / 2) + c * 32, u);
-        tc_wait_ld();
-        if (whole) {
-          if (live) {
+      for (int t2 = 0; t2 < p.nt; ++t2) {
+        const bool live = row_of(t2) < p.rows;
+        uint4* dst = reinterpret_cast<uint4*>(a.o + row_at(t2) + half * (D / 2));
+        const float L = bars->xch[t2][0][r] + bars->xch[t2][1][r];
+        const float inv = L == 0.f ? 0.f : a.v_scale / L;
+        float* tile = rec + t2 * Lay::TREC;
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t u[32];
+          tc_ld_32x32b_x32(tmem + lane_off + 256 + t2 * D + half * (D / 2) + c * 32, u);
+          tc_wait_ld();
+          if (whole) {
+            if (live) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* f = reinterpret_cast<const float*>(u) + 8 * i;
-              dst[c * 4 + i] = make_uint4(pack_bf16(f[0] * inv, f[1] * inv), pack_bf16(f[2] * inv, f[3] * inv),
-                                          pack_bf16(f[4] * inv, f[5] * inv), pack_bf16(f[6] * inv, f[7] * inv));
+              for (int i = 0; i < 4; ++i) {
+                const float* f = reinterpret_cast<const float*>(u) + 8 * i;
+                dst[c * 4 + i] = make_uint4(pack_bf16(f[0] * inv, f[1] * inv), pack_bf16(f[2] * inv, f[3] * inv),
+                                            pack_bf16(f[4] * inv, f[5] * inv), pack_bf16(f[6] * inv, f[7] * inv));
+              }
+            }
+          } else {  // four channels of all rows next to one another
+            float4* out = reinterpret_cast<float4*>(tile) + (half * (D / 8) + c * 8) * KP_M + r;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float* f = reinterpret_cast<const float*>(u) + 4 * i;
+              out[i * KP_M] = make_float4(f[0], f[1], f[2], f[3]);
             }
           }
-        } else {  // four channels of all rows next to one another
-          float4* out = reinterpret_cast<float4*>(rec) + (half * (D / 8) + c * 8) * KP_M + r;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float* f = reinterpret_cast<const float*>(u) + 4 * i;
-            out[i * KP_M] = make_float4(f[0], f[1], f[2], f[3]);
-          }
         }
+        if (!whole && half == 0) {
+          tile[KP_M * D + r] = m_ref;
+          tile[KP_M * D + KP_M + r] = L;
+        }
+        if (p.nt == 2) other();
       }
       tc_fence_before();
       if (whole) {
         if (!(ok = meet())) break;  // xch is free again
         continue;
-      }
-      if (half == 0) {
-        rec[KP_M * D + r] = m_ref;
-        rec[KP_M * D + KP_M + r] = L;
       }
       __threadfence();
       if (!(ok = meet())) break;
@@ -743,39 +800,44 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
       if (!(ok = meet())) break;
       if (bars->last) {
         __threadfence();
-        float M = -INFINITY, Ls = 0.f;
-        for (int b = first; b <= last; ++b) M = fmaxf(M, __ldcg(rec_of(b) + KP_M * D + r));
-        for (int b = first; b <= last; ++b) {
-          const float mb = __ldcg(rec_of(b) + KP_M * D + r);
-          Ls = fmaf(mb == -INFINITY ? 1.f : exp2f(mb - M), __ldcg(rec_of(b) + KP_M * D + KP_M + r), Ls);
-        }
-        const float iv = Ls == 0.f ? 0.f : a.v_scale / Ls;
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          float4 acc[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int t2 = 0; t2 < p.nt; ++t2) {
+          auto tile_of = [&](int cta) { return rec_of(cta) + t2 * Lay::TREC; };
+          float M = -INFINITY, Ls = 0.f;
+          for (int b = first; b <= last; ++b) M = fmaxf(M, __ldcg(tile_of(b) + KP_M * D + r));
           for (int b = first; b <= last; ++b) {
-            const float mb = __ldcg(rec_of(b) + KP_M * D + r);
-            const float wb = mb == -INFINITY ? 1.f : exp2f(mb - M);
-            const float4* in = reinterpret_cast<const float4*>(rec_of(b)) + (half * (D / 8) + c * 8) * KP_M + r;
-            float4 v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __ldcg(in + i * KP_M);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[i].x = fmaf(wb, v[i].x, acc[i].x);
-              acc[i].y = fmaf(wb, v[i].y, acc[i].y);
-              acc[i].z = fmaf(wb, v[i].z, acc[i].z);
-              acc[i].w = fmaf(wb, v[i].w, acc[i].w);
-            }
+            const float mb = __ldcg(tile_of(b) + KP_M * D + r);
+            Ls = fmaf(mb == -INFINITY ? 1.f : exp2f(mb - M), __ldcg(tile_of(b) + KP_M * D + KP_M + r), Ls);
           }
-          if (live) {
+          const float iv = Ls == 0.f ? 0.f : a.v_scale / Ls;
+          uint4* dst = reinterpret_cast<uint4*>(a.o + row_at(t2) + half * (D / 2));
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            float4 acc[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = acc[2 * i], h = acc[2 * i + 1];
-              dst[c * 4 + i] = make_uint4(pack_bf16(f.x * iv, f.y * iv), pack_bf16(f.z * iv, f.w * iv),
-                                          pack_bf16(h.x * iv, h.y * iv), pack_bf16(h.z * iv, h.w * iv));
+            for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int b = first; b <= last; ++b) {
+              const float mb = __ldcg(tile_of(b) + KP_M * D + r);
+              const float wb = mb == -INFINITY ? 1.f : exp2f(mb - M);
+              const float4* in = reinterpret_cast<const float4*>(tile_of(b)) + (half * (D / 8) + c * 8) * KP_M + r;
+              float4 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = __ldcg(in + i * KP_M);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                acc[i].x = fmaf(wb, v[i].x, acc[i].x);
+                acc[i].y = fmaf(wb, v[i].y, acc[i].y);
+                acc[i].z = fmaf(wb, v[i].z, acc[i].z);
+                acc[i].w = fmaf(wb, v[i].w, acc[i].w);
+              }
+            }
+            if (row_of(t2) < p.rows) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 f = acc[2 * i], h = acc[2 * i + 1];
+                dst[c * 4 + i] = make_uint4(pack_bf16(f.x * iv, f.y * iv), pack_bf16(f.z * iv, f.w * iv),
+                                            pack_bf16(h.x * iv, h.y * iv), pack_bf16(h.z * iv, h.w * iv));
+              }
             }
           }
         }
