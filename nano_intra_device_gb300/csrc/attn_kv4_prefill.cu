@@ -35,39 +35,35 @@ namespace nf {
 namespace {
 
 constexpr int KP_DQ_WARPS = 4;       // warps that make operands: two for K, two for V
-constexpr int KP_SM_WARPS = 8;       // softmax warps: two per tensor-memory lane quarter
+constexpr int KP_SM_WARPS = 8;       // softmax warps: four a tile, one a tensor-memory lane quarter
 constexpr int KP_MMA_WARP = KP_DQ_WARPS + KP_SM_WARPS;
 constexpr int KP_WARPS = 16;         // registers are dealt by warpgroups of four: the last holds the
                                      // MMA warp and three that only take part in the prologue
 constexpr int KP_THREADS = KP_WARPS * 32;
 // 512 = 4 x 128 registers a thread at launch, dealt again by role
-constexpr int KP_DQ_REGS = 112, KP_SM_REGS = 160, KP_MMA_REGS = 80;
+constexpr int KP_DQ_REGS = 104, KP_SM_REGS = 176, KP_MMA_REGS = 56;
 static_assert(KP_DQ_REGS + 2 * KP_SM_REGS + KP_MMA_REGS == 512, "the shares of the launch's registers");
 constexpr int KP_M = 128;            // query vectors of a tile (tensor-memory lanes)
 constexpr int KP_N = 128;            // positions of a key block
-constexpr int KP_H = KP_N / 2;       // positions of a block one softmax thread owns
 constexpr int KP_REGION = 128 * 128; // 128 rows x 128 bytes: 64 fp16 columns of 128 rows
 constexpr int KP_FIXED = 1;          // blocks' worth of a unit's fixed cost
 constexpr float KP_SLACK = 8.f;
 constexpr float KP_SHIFT = 7.f;
 constexpr uint32_t KP_TMEM_COLS = 512;
-constexpr int KP_KST = 2, KP_VST = 1;  // ring stages of K and V
+constexpr int KP_KST = 2, KP_VST = 2;  // ring stages of K and V
 
 struct KpBars {
-  uint64_t q_full;                           // every softmax warp: Q of a piece written
+  uint64_t q_full[2];                        // by tile: its softmax warps have written Q
   uint64_t k_full[KP_KST], k_empty[KP_KST];  // full: two warps
   uint64_t v_full[KP_VST], v_empty[KP_VST];
-  uint64_t s_full[2], s_free[2];             // S accumulators (free: every softmax warp)
-  uint64_t p_full;                           // every softmax warp: P written (and O rescaled)
-  uint64_t p_free;                           // a PV product finished
+  uint64_t s_full[2];                        // by tile: S of a block, and all products before it
+  uint64_t p_full[2];                        // its softmax warps: P written (and O rescaled)
+  uint64_t o_full[2];                        // the last product of a piece
+  uint64_t meet[2];                          // a bounded barrier of a tile's softmax warps
   uint64_t drain;
-  uint64_t meet;                             // the softmax warps
-  uint64_t pair[4];                          // both warps of 32 rows have a block's maxima
   uint32_t tmem_base;
-  int abort, last;
+  int abort, last[2];
   uint32_t v_nan[KP_VST][4];                 // positions whose V holds a NaN that not every row sees
-  float xch[2][2][KP_M];                      // the two halves of a row exchange their sums
-  float top[2][2][KP_M];                     // and, by the block's parity, their maxima
   long long warp_sum[KP_WARPS];
   long long base;                            // where this CTA starts: a request's first slot
   int seq;                                   // and the request
@@ -79,11 +75,9 @@ struct KpLayout {
   static constexpr int Q_BYTES = NCH * KP_REGION;   // [d/64][128 vectors][128 B]
   static constexpr int KV_BYTES = NCH * KP_REGION;  // 16 groups of 8 positions, each [d/64][8][128 B]
   static constexpr int KV_GROUP = NCH * 1024;
-  static constexpr int P_BYTES = 2 * KP_REGION;     // [keys/64][128 vectors][128 B]
   static constexpr int K_OFF = 2 * Q_BYTES;
   static constexpr int V_OFF = K_OFF + KP_KST * KV_BYTES;
-  static constexpr int P_OFF = V_OFF + KP_VST * KV_BYTES;
-  static constexpr int BAR_OFF = P_OFF + P_BYTES;
+  static constexpr int BAR_OFF = V_OFF + KP_VST * KV_BYTES;
   static constexpr int SMEM = 1024 + BAR_OFF + static_cast<int>(sizeof(KpBars));
   static constexpr int TREC = KP_M * D + 2 * KP_M;  // floats of a tile's record: O, m, l
   static constexpr int REC = 2 * TREC;
@@ -113,6 +107,29 @@ __device__ __forceinline__ float kp_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+// 32 lanes x 16 columns, as the 32-column forms.
+__device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// tcgen05.mma with A in tensor memory: a column holds two neighbours along K.
+__device__ __forceinline__ void kp_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 // Instruction descriptor, kind::f16: fp16 A and B, fp32 D; B K-major or MN-major.
 constexpr uint32_t kp_idesc(int M, int N, bool b_mn) {
@@ -278,7 +295,6 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
   }
 
   if (tid == 0) {
-    mbar_init(&bars->q_full, KP_SM_WARPS);
     for (int i = 0; i < KP_KST; ++i) {
       mbar_init(&bars->k_full[i], 2);
       mbar_init(&bars->k_empty[i], 1);
@@ -289,14 +305,13 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
       for (int k = 0; k < 4; ++k) bars->v_nan[i][k] = 0;
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], KP_SM_WARPS / 2);
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->s_free[i], KP_SM_WARPS);
+      mbar_init(&bars->p_full[i], KP_SM_WARPS / 2);
+      mbar_init(&bars->o_full[i], 1);
+      mbar_init(&bars->meet[i], KP_SM_WARPS / 2);
     }
-    mbar_init(&bars->p_full, KP_SM_WARPS);
-    mbar_init(&bars->p_free, 1);
     mbar_init(&bars->drain, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&bars->pair[i], 2);
-    mbar_init(&bars->meet, KP_SM_WARPS);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -307,7 +322,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;  // columns [0, 256): S x 2; [256, 256 + d): O
+  const uint32_t tmem = bars->tmem_base;  // columns [0, 256): S of the two tiles, P over it; [256, 256 + 2 d): O
   walk.base = bars->base;
   walk.s = bars->seq;
   walk.q = kp_seq<GRP>(a, walk.s);
@@ -468,63 +483,61 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
   } else if (warp >= KP_MMA_WARP) {
     kp_regs_less<KP_MMA_REGS>();
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t q_addr = sbase, p_addr = sbase + Lay::P_OFF, o_tmem = tmem + 256;
     bool ok = true, any = false;
-    uint32_t i = 0, n = 0, np = 0;  // S products issued, blocks begun and ended; pieces
-    // the PV product that follows the S product of the next step
-    uint32_t vt = 0, vn = 0;        // its tile and block
-    bool vfirst = false;            // the first of its piece
-    auto pv = [&](uint32_t step, int nt) -> bool {
-      const uint32_t s = vn % KP_VST;
-      if (vt == 0 && !mbar_wait(&bars->v_full[s], (vn / KP_VST) & 1, tmo, abort_flag)) return false;
-      if (!mbar_wait(&bars->p_full, step & 1, tmo, abort_flag)) return false;
-      tc_fence_after();
-      const uint32_t v_addr = sbase + Lay::V_OFF + s * Lay::KV_BYTES;
+    uint32_t n = 0;                  // blocks
+    uint32_t np0 = 0, np1 = 0;       // pieces and steps of either tile
+    uint32_t st0 = 0, st1 = 0;
+    auto s_product = [&](int t, uint32_t block) {
+      const uint32_t k_addr = sbase + Lay::K_OFF + (block % KP_KST) * Lay::KV_BYTES;
 #pragma unroll
-      for (int kk = 0; kk < KP_N / 16; ++kk) {
-        const uint64_t bdesc = desc_sw128_mnmajor(v_addr + kk * 2 * Lay::KV_GROUP, 1024, Lay::KV_GROUP);
-        const uint64_t adesc = desc_sw128_kmajor(p_addr + (kk >> 2) * KP_REGION) + 2 * (kk & 3);
-        tc_mma_bf16(o_tmem + vt * D, adesc, bdesc, IDESC_PV, !vfirst || kk > 0);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t adesc = desc_sw128_kmajor(sbase + t * Lay::Q_BYTES + (kk >> 2) * KP_REGION) + 2 * (kk & 3);
+        const uint64_t bdesc = desc_sw128_kmajor_sbo(k_addr + (kk >> 2) * 1024, Lay::KV_GROUP) + 2 * (kk & 3);
+        tc_mma_bf16(tmem + t * KP_N, adesc, bdesc, IDESC_S, kk > 0);
       }
       any = true;
-      tc_commit(&bars->p_free);
-      if (static_cast<int>(vt) == nt - 1) tc_commit(&bars->v_empty[s]);
-      return true;
+      tc_commit(&bars->s_full[t]);
+    };
+    auto k_wait = [&](uint32_t block) -> bool {
+      const bool good = mbar_wait(&bars->k_full[block % KP_KST], (block / KP_KST) & 1, tmo, abort_flag);
+      tc_fence_after();
+      return good;
     };
     while (warp == KP_MMA_WARP && ok && walk.next(a, p)) {
       if (lane == 0) {
-        ok = mbar_wait(&bars->q_full, np & 1, tmo, abort_flag);
+        ok = mbar_wait(&bars->q_full[0], np0++ & 1, tmo, abort_flag) &&
+             (p.nt == 1 || mbar_wait(&bars->q_full[1], np1++ & 1, tmo, abort_flag)) && k_wait(n);
+        if (ok) {
+          for (int t = 0; t < p.nt; ++t) s_product(t, n);
+          tc_commit(&bars->k_empty[n % KP_KST]);
+        }
         for (int j = p.j0; j < p.j1 && ok; ++j, ++n) {
-          const uint32_t ks = n % KP_KST;
-          for (int t = 0; t < p.nt; ++t, ++i) {
-            const uint32_t s = i & 1;
-            ok = (t > 0 || mbar_wait(&bars->k_full[ks], (n / KP_KST) & 1, tmo, abort_flag)) &&
-                 mbar_wait(&bars->s_free[s], ((i >> 1) & 1) ^ 1, tmo, abort_flag);
+          const uint32_t vs = n % KP_VST;
+          const bool more = j + 1 < p.j1;
+          ok = mbar_wait(&bars->v_full[vs], (n / KP_VST) & 1, tmo, abort_flag);
+          for (int t = 0; t < p.nt && ok; ++t) {
+            // P over S, then the next S over P: the products run in their order
+            ok = mbar_wait(&bars->p_full[t], (t ? st1++ : st0++) & 1, tmo, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t k_addr = sbase + Lay::K_OFF + ks * Lay::KV_BYTES;
+            const uint32_t v_addr = sbase + Lay::V_OFF + vs * Lay::KV_BYTES;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t adesc = desc_sw128_kmajor(q_addr + t * Lay::Q_BYTES + (kk >> 2) * KP_REGION) + 2 * (kk & 3);
-              const uint64_t bdesc = desc_sw128_kmajor_sbo(k_addr + (kk >> 2) * 1024, Lay::KV_GROUP) + 2 * (kk & 3);
-              tc_mma_bf16(tmem + s * KP_N, adesc, bdesc, IDESC_S, kk > 0);
+            for (int kk = 0; kk < KP_N / 16; ++kk) {
+              const uint64_t bdesc = desc_sw128_mnmajor(v_addr + kk * 2 * Lay::KV_GROUP, 1024, Lay::KV_GROUP);
+              kp_mma_ts(tmem + 256 + t * D, tmem + t * KP_N + kk * 8, bdesc, IDESC_PV, j > p.j0 || kk > 0);
             }
             any = true;
-            tc_commit(&bars->s_full[s]);
-            if (t == p.nt - 1) tc_commit(&bars->k_empty[ks]);
-            if (j > p.j0 || t > 0) {
-              ok = pv(i - 1, p.nt);
+            if (t == p.nt - 1) tc_commit(&bars->v_empty[vs]);
+            if (more) {
+              if (t == 0) ok = k_wait(n + 1);
               if (!ok) break;
+              s_product(t, n + 1);
+              if (t == p.nt - 1) tc_commit(&bars->k_empty[(n + 1) % KP_KST]);
+            } else {
+              tc_commit(&bars->o_full[t]);
             }
-            vt = t;
-            vn = n;
-            vfirst = j == p.j0;
           }
         }
-        // the unit's last product before the next one's Q is waited for: its
-        // epilogue comes first
-        if (ok) ok = pv(i - 1, p.nt);
-        ++np;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
@@ -539,45 +552,37 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     kp_regs_more<KP_SM_REGS>();
     // --------------------------------------------------- softmax and epilogue
     const int sw = warp - KP_DQ_WARPS;
+    const int t = sw >> 2;             // the tile
     const int quarter = warp & 3;      // tensor-memory lanes this warp may access
-    const int half = sw >> 2;          // which 64 keys of a block (and d/2 of O) it owns
     const int r = quarter * 32 + lane; // the vector (lane) this thread owns
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    uint32_t n = 0, blk = 0, met = 0;  // steps done; blocks done; meetings
+    const uint32_t s_tmem = tmem + lane_off + t * KP_N, o_tmem = tmem + lane_off + 256 + t * D;
+    constexpr int RT = KP_M / GRP;     // rows of a tile
+    uint32_t n = 0, np = 0, met = 0;   // blocks, pieces and meetings of this tile
+    uint32_t blk = 0;                  // blocks of the CTA
     bool ok = true;
-    auto pv_done = [&](uint32_t i) -> bool {
-      return wait(&bars->p_free, i & 1);
-    };
-    auto meet = [&]() -> bool {  // a bounded barrier of the softmax threads
-      arrive(&bars->meet);
-      const bool good = wait(&bars->meet, met & 1);
+    auto meet = [&]() -> bool {
+      arrive(&bars->meet[t]);
+      const bool good = wait(&bars->meet[t], met & 1);
       ++met;
       return good;
     };
     while (ok && walk.next(a, p)) {
-      constexpr int RT = KP_M / GRP;  // rows of a tile
-      // the state of the tile at hand, and of the other one
-      float scale = 0.f, scale_b = 0.f, m_ref = -INFINITY, m_b = -INFINITY, l = 0.f, l_b = 0.f;
-      int qpos = -1, qpos_b = -1;  // the row sees positions 0 .. qpos
-      auto other = [&]() {
-        float f = scale; scale = scale_b; scale_b = f;
-        f = m_ref; m_ref = m_b; m_b = f;
-        f = l; l = l_b; l_b = f;
-        const int i = qpos; qpos = qpos_b; qpos_b = i;
-      };
-      auto row_of = [&](int t) { return t * RT + r / GRP; };
-      auto row_at = [&](int t) {  // of q and o; a row that is not there: the unit's first
-        return (static_cast<size_t>(p.row0 + (row_of(t) < p.rows ? row_of(t) : 0)) * a.n_q + p.g * GRP + r % GRP) * D;
-      };
-      // Q: this half of the vectors, scaled to fp16's range by their largest element
-#pragma unroll 1
-      for (int t = 0; t < p.nt; ++t) {
-        const bool live = row_of(t) < p.rows;
-        if (t > 0) other();
-        qpos = live ? p.pos0 + row_of(t) : -1;
-        const uint4* q4 = reinterpret_cast<const uint4*>(a.q + row_at(t));
+      if (t >= p.nt) {
+        blk += p.j1 - p.j0;
+        continue;
+      }
+      const int row = t * RT + r / GRP;
+      const bool live = row < p.rows;
+      const int qpos = live ? p.pos0 + row : -1;  // sees positions 0 .. qpos
+      // of q and o; a row that is not there: the unit's first
+      const size_t at = (static_cast<size_t>(p.row0 + (live ? row : 0)) * a.n_q + p.g * GRP + r % GRP) * D;
+      // Q, scaled to fp16's range by the vector's largest element
+      float scale;
+      {
+        const uint4* q4 = reinterpret_cast<const uint4*>(a.q + at);
         float top = 0.f;
-        uint4 own[D / 16];
+        uint4 own[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           uint4 v = q4[c];
@@ -585,48 +590,39 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           top = fmaxf(top, kp_max3(kp_max3(fabsf(bf16lo(v.x)), fabsf(bf16hi(v.x)), fabsf(bf16lo(v.y))),
                                    kp_max3(fabsf(bf16hi(v.y)), fabsf(bf16lo(v.z)), fabsf(bf16hi(v.z))),
                                    fmaxf(fabsf(bf16lo(v.w)), fabsf(bf16hi(v.w)))));
-          if (c / (D / 16) == half) own[c % (D / 16)] = v;
+          own[c] = v;
         }
         const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
         const int kq = top > 0.f ? max(-126, min(120, 14 - e)) : 0;
         const float mul = exp2_int(kq);
         scale = fmaxf(a.scale_log2 * exp2_int(-kq), 1.17549435e-38f);  // 0 times a hidden score's -inf is NaN
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int c = half * (D / 16) + i;
-          const uint4 v = own[i];
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = own[c];
           kp_st16(sbase + t * Lay::Q_BYTES + (c >> 3) * KP_REGION + kp_sw128(r, c & 7),
                   make_uint4(kp_pack(bf16lo(v.x) * mul, bf16hi(v.x) * mul), kp_pack(bf16lo(v.y) * mul, bf16hi(v.y) * mul),
                              kp_pack(bf16lo(v.z) * mul, bf16hi(v.z) * mul), kp_pack(bf16lo(v.w) * mul, bf16hi(v.w) * mul)));
         }
+        fence_proxy_async_smem();
+        arrive(&bars->q_full[t]);
       }
-      if (p.nt == 2) other();
-      fence_proxy_async_smem();
-      arrive(&bars->q_full);
-      int j = p.j0, t = 0;
-      while (j < p.j1) {
-        const uint32_t s = n & 1;
-        if (!wait(&bars->s_full[s], (n >> 1) & 1)) {
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = p.j0; j < p.j1; ++j, ++n, ++blk) {
+        if (!wait(&bars->s_full[t], n & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // this half's 64 scores; the row maximum by way of shared memory
-        float x[KP_H];
-        const bool mixed = j * KP_N + KP_N - 1 > p.pos0;  // some row sees less than the block (uniform)
-        {
-          const uint32_t own = tmem + lane_off + s * KP_N + half * KP_H;
-          tc_ld_32x32b_x32(own, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-          tc_ld_32x32b_x32(own + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-          tc_wait_ld();
-          tc_fence_before();
-          arrive(&bars->s_free[s]);
-        }
-        if (mixed) {
-          const int kb = j * KP_N + half * KP_H;
+        float x[KP_N];
 #pragma unroll
-          for (int i = 0; i < KP_H; ++i)
-            if (kb + i > qpos) x[i] = -INFINITY;
+        for (int c = 0; c < KP_N / 32; ++c) tc_ld_32x32b_x32(s_tmem + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
+        tc_wait_ld();
+        const bool mixed = j * KP_N + KP_N - 1 > p.pos0;  // some row of the unit sees less than the block
+        if (mixed) {
+          const int see = qpos - j * KP_N;
+#pragma unroll
+          for (int i = 0; i < KP_N; ++i)
+            if (i > see) x[i] = -INFINITY;
         }
         float mx;
         {
@@ -634,21 +630,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
 #pragma unroll
           for (int i = 0; i < 8; ++i) mx8[i] = kp_max3(x[i], x[8 + i], x[16 + i]);
 #pragma unroll
-          for (int i = 24; i < KP_H - 8; i += 16)
+          for (int i = 24; i < KP_N - 8; i += 16)
 #pragma unroll
             for (int k = 0; k < 8; ++k) mx8[k] = kp_max3(mx8[k], x[i + k], x[i + 8 + k]);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], x[KP_H - 8 + k]);
-          mx = kp_max3(kp_max3(mx8[0], mx8[1], mx8[2]), kp_max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-          // a slot is written again only after the other half has read it: its next
-          // arrival, which this thread waits for in between, follows its read
-          bars->top[s][half][r] = mx;
-          arrive(&bars->pair[quarter]);
-          if (!wait(&bars->pair[quarter], n & 1)) {
-            ok = false;
-            break;
-          }
-          mx = fmaxf(mx, bars->top[s][half ^ 1][r]) * scale;
+          for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], x[KP_N - 8 + k]);
+          mx = kp_max3(kp_max3(mx8[0], mx8[1], mx8[2]), kp_max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * scale;
         }
         float corr = 1.f;
         if (mx > m_ref + KP_SLACK) {  // also from -inf, where O and l are still zero
@@ -656,20 +643,33 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           m_ref = mx;
           l *= corr;
         }
+        // a raised maximum rescales the row of O; the product of the block before is
+        // done, as it was issued before this S
+        if (j > p.j0 && __any_sync(0xffffffffu, corr != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t u[16];
+            tc_ld_32x32b_x16(o_tmem + c * 16, u);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * corr);
+            tc_st_32x32b_x16(o_tmem + c * 16, u);
+          }
+        }
         // p = 2^(s scale - m + shift); m = -inf: nothing seen yet, all p are 0
         const float nm = m_ref == -INFINITY ? KP_SHIFT : KP_SHIFT - m_ref;
         if (__any_sync(0xffffffffu, fabsf(m_ref) > 3e7f && m_ref != -INFINITY)) {
           // beyond fp32's whole numbers the fused step could pass the maximum's own
           // rounding by more than the slack
 #pragma unroll
-          for (int i = 0; i < KP_H; ++i) x[i] = ex2_approx(__fadd_rn(__fmul_rn(x[i], scale), nm));
+          for (int i = 0; i < KP_N; ++i) x[i] = ex2_approx(__fadd_rn(__fmul_rn(x[i], scale), nm));
         } else {
           const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
 #pragma unroll
-          for (int i = 0; i < KP_H / 2; ++i) {
-            const float2 t = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), sc2, nm2);
-            x[2 * i] = ex2_approx(t.x);
-            x[2 * i + 1] = ex2_approx(t.y);
+          for (int i = 0; i < KP_N / 2; ++i) {
+            const float2 f = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), sc2, nm2);
+            x[2 * i] = ex2_approx(f.x);
+            x[2 * i + 1] = ex2_approx(f.y);
           }
         }
         if (mixed) {
@@ -679,165 +679,122 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
             ok = false;
             break;
           }
-          const uint32_t nan0 = bars->v_nan[vs][2 * half], nan1 = bars->v_nan[vs][2 * half + 1];
-          if (nan0 | nan1) {
-            const int kb = j * KP_N + half * KP_H;
+          const int see = qpos - j * KP_N;
 #pragma unroll
-            for (int i = 0; i < KP_H; ++i)
-              if ((((i < 32 ? nan0 : nan1) >> (i & 31)) & 1) && kb + i <= qpos) x[i] = __int_as_float(0x7FC00000);
+          for (int k = 0; k < KP_N / 32; ++k) {
+            const uint32_t nan = bars->v_nan[vs][k];
+            if (nan) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (((nan >> i) & 1) && 32 * k + i <= see) x[32 * k + i] = __int_as_float(0x7FC00000);
+            }
           }
         }
-        // a raised maximum rescales this half of the row of O, once the PV
-        // product of the previous block is done with it
-        if (j > p.j0 && __any_sync(0xffffffffu, corr != 1.f)) {
-          if (!pv_done(n - 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          uint32_t u[32];
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            const uint32_t ta = tmem + lane_off + 256 + t * D + half * (D / 2) + c * 32;
-            tc_ld_32x32b_x32(ta, u);
-            tc_wait_ld();
+        // P as fp16 pairs over the first half of S
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * corr);
-            tc_st_32x32b_x32(ta, u);
-          }
-          tc_wait_st();
-        }
-        // P (free once the previous PV product is done), K-major in the 128-byte
-        // swizzle: this half's 64 keys fill one region
-        if ((j > p.j0 || t > 0) && !pv_done(n - 1)) {
-          ok = false;
-          break;
-        }
-        const uint32_t p_reg = sbase + Lay::P_OFF + half * KP_REGION;
+        for (int c = 0; c < KP_N / 64; ++c) {
+          uint32_t w[32];
 #pragma unroll
-        for (int c = 0; c < KP_H / 8; ++c)
-          kp_st16(p_reg + kp_sw128(r, c), make_uint4(kp_pack(x[8 * c], x[8 * c + 1]), kp_pack(x[8 * c + 2], x[8 * c + 3]),
-                                                     kp_pack(x[8 * c + 4], x[8 * c + 5]), kp_pack(x[8 * c + 6], x[8 * c + 7])));
-        fence_proxy_async_smem();
+          for (int i = 0; i < 32; ++i) w[i] = kp_pack(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]);
+          tc_st_32x32b_x32(s_tmem + 32 * c, w);
+        }
+        tc_wait_st();
         tc_fence_before();
-        arrive(&bars->p_full);
+        arrive(&bars->p_full[t]);
         {
           float2 ls4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < KP_H / 2; ++i) ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(x[2 * i], x[2 * i + 1]));
+          for (int i = 0; i < KP_N / 2; ++i) ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(x[2 * i], x[2 * i + 1]));
           const float2 a2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
           l += a2.x + a2.y;
         }
-        ++n;
-        if (p.nt == 2) other();
-        if (++t == p.nt) {
-          t = 0;
-          ++j;
-          ++blk;
-        }
       }
-      if (ok && !pv_done(n - 1)) ok = false;
+      if (ok && !wait(&bars->o_full[t], np & 1)) ok = false;
       if (!ok) break;
+      ++np;
       tc_fence_after();
-      bars->xch[0][half][r] = l;
-      bars->xch[1][half][r] = l_b;
-      if (!(ok = meet())) break;
       const bool whole = p.j0 == 0 && p.j1 == p.nb;
       const int first = static_cast<int>((p.key + KP_FIXED) / quota);
       const int last = static_cast<int>((p.key + KP_FIXED + p.nb - 1) / quota);
-      auto rec_of = [&](int cta) { return a.tiles + (static_cast<size_t>(cta) * 2 + (cta == first ? 1 : 0)) * Lay::REC; };
+      auto rec_of = [&](int cta) {
+        return a.tiles + (static_cast<size_t>(cta) * 2 + (cta == first ? 1 : 0)) * Lay::REC + t * Lay::TREC;
+      };
       float* rec = rec_of(blockIdx.x);
+      uint4* dst = reinterpret_cast<uint4*>(a.o + at);
+      const float inv = l == 0.f ? 0.f : a.v_scale / l;
 #pragma unroll 1
-      for (int t2 = 0; t2 < p.nt; ++t2) {
-        const bool live = row_of(t2) < p.rows;
-        uint4* dst = reinterpret_cast<uint4*>(a.o + row_at(t2) + half * (D / 2));
-        const float L = bars->xch[t2][0][r] + bars->xch[t2][1][r];
-        const float inv = L == 0.f ? 0.f : a.v_scale / L;
-        float* tile = rec + t2 * Lay::TREC;
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t u[32];
-          tc_ld_32x32b_x32(tmem + lane_off + 256 + t2 * D + half * (D / 2) + c * 32, u);
-          tc_wait_ld();
-          if (whole) {
-            if (live) {
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t u[32];
+        tc_ld_32x32b_x32(o_tmem + c * 32, u);
+        tc_wait_ld();
+        if (whole) {
+          if (live) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float* f = reinterpret_cast<const float*>(u) + 8 * i;
-                dst[c * 4 + i] = make_uint4(pack_bf16(f[0] * inv, f[1] * inv), pack_bf16(f[2] * inv, f[3] * inv),
-                                            pack_bf16(f[4] * inv, f[5] * inv), pack_bf16(f[6] * inv, f[7] * inv));
-              }
-            }
-          } else {  // four channels of all rows next to one another
-            float4* out = reinterpret_cast<float4*>(tile) + (half * (D / 8) + c * 8) * KP_M + r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float* f = reinterpret_cast<const float*>(u) + 4 * i;
-              out[i * KP_M] = make_float4(f[0], f[1], f[2], f[3]);
+            for (int i = 0; i < 4; ++i) {
+              const float* f = reinterpret_cast<const float*>(u) + 8 * i;
+              dst[c * 4 + i] = make_uint4(pack_bf16(f[0] * inv, f[1] * inv), pack_bf16(f[2] * inv, f[3] * inv),
+                                          pack_bf16(f[4] * inv, f[5] * inv), pack_bf16(f[6] * inv, f[7] * inv));
             }
           }
+        } else {  // four channels of all rows next to one another
+          float4* out = reinterpret_cast<float4*>(rec) + c * 8 * KP_M + r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float* f = reinterpret_cast<const float*>(u) + 4 * i;
+            out[i * KP_M] = make_float4(f[0], f[1], f[2], f[3]);
+          }
         }
-        if (!whole && half == 0) {
-          tile[KP_M * D + r] = m_ref;
-          tile[KP_M * D + KP_M + r] = L;
-        }
-        if (p.nt == 2) other();
       }
       tc_fence_before();
-      if (whole) {
-        if (!(ok = meet())) break;  // xch is free again
-        continue;
-      }
+      if (whole) continue;
+      rec[KP_M * D + r] = m_ref;
+      rec[KP_M * D + KP_M + r] = l;
       __threadfence();
       if (!(ok = meet())) break;
-      if (warp == KP_DQ_WARPS && lane == 0) {
-        const int before = atomicAdd(&a.tile_counters[first], 1);
-        bars->last = before == last - first;
-        if (before == last - first) a.tile_counters[first] = 0;  // as the next launch expects it
+      if (quarter == 0 && lane == 0) {
+        int* counter = a.tile_counters + 2 * first + t;
+        const int before = atomicAdd(counter, 1);
+        bars->last[t] = before == last - first;
+        if (before == last - first) *counter = 0;  // as the next launch expects it
       }
       if (!(ok = meet())) break;
-      if (bars->last) {
+      if (bars->last[t]) {
         __threadfence();
+        float M = -INFINITY, Ls = 0.f;
+        for (int b = first; b <= last; ++b) M = fmaxf(M, __ldcg(rec_of(b) + KP_M * D + r));
+        for (int b = first; b <= last; ++b) {
+          const float mb = __ldcg(rec_of(b) + KP_M * D + r);
+          Ls = fmaf(mb == -INFINITY ? 1.f : exp2f(mb - M), __ldcg(rec_of(b) + KP_M * D + KP_M + r), Ls);
+        }
+        const float iv = Ls == 0.f ? 0.f : a.v_scale / Ls;
 #pragma unroll 1
-        for (int t2 = 0; t2 < p.nt; ++t2) {
-          auto tile_of = [&](int cta) { return rec_of(cta) + t2 * Lay::TREC; };
-          float M = -INFINITY, Ls = 0.f;
-          for (int b = first; b <= last; ++b) M = fmaxf(M, __ldcg(tile_of(b) + KP_M * D + r));
+        for (int c = 0; c < D / 32; ++c) {
+          float4 acc[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int b = first; b <= last; ++b) {
-            const float mb = __ldcg(tile_of(b) + KP_M * D + r);
-            Ls = fmaf(mb == -INFINITY ? 1.f : exp2f(mb - M), __ldcg(tile_of(b) + KP_M * D + KP_M + r), Ls);
-          }
-          const float iv = Ls == 0.f ? 0.f : a.v_scale / Ls;
-          uint4* dst = reinterpret_cast<uint4*>(a.o + row_at(t2) + half * (D / 2));
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            float4 acc[8];
+            const float mb = __ldcg(rec_of(b) + KP_M * D + r);
+            const float wb = mb == -INFINITY ? 1.f : exp2f(mb - M);
+            const float4* in = reinterpret_cast<const float4*>(rec_of(b)) + c * 8 * KP_M + r;
+            float4 v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int b = first; b <= last; ++b) {
-              const float mb = __ldcg(tile_of(b) + KP_M * D + r);
-              const float wb = mb == -INFINITY ? 1.f : exp2f(mb - M);
-              const float4* in = reinterpret_cast<const float4*>(tile_of(b)) + (half * (D / 8) + c * 8) * KP_M + r;
-              float4 v[8];
+            for (int i = 0; i < 8; ++i) v[i] = __ldcg(in + i * KP_M);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = __ldcg(in + i * KP_M);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                acc[i].x = fmaf(wb, v[i].x, acc[i].x);
-                acc[i].y = fmaf(wb, v[i].y, acc[i].y);
-                acc[i].z = fmaf(wb, v[i].z, acc[i].z);
-                acc[i].w = fmaf(wb, v[i].w, acc[i].w);
-              }
+            for (int i = 0; i < 8; ++i) {
+              acc[i].x = fmaf(wb, v[i].x, acc[i].x);
+              acc[i].y = fmaf(wb, v[i].y, acc[i].y);
+              acc[i].z = fmaf(wb, v[i].z, acc[i].z);
+              acc[i].w = fmaf(wb, v[i].w, acc[i].w);
             }
-            if (row_of(t2) < p.rows) {
+          }
+          if (live) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 f = acc[2 * i], h = acc[2 * i + 1];
-                dst[c * 4 + i] = make_uint4(pack_bf16(f.x * iv, f.y * iv), pack_bf16(f.z * iv, f.w * iv),
-                                            pack_bf16(h.x * iv, h.y * iv), pack_bf16(h.z * iv, h.w * iv));
-              }
+            for (int i = 0; i < 4; ++i) {
+              const float4 f = acc[2 * i], h = acc[2 * i + 1];
+              dst[c * 4 + i] = make_uint4(pack_bf16(f.x * iv, f.y * iv), pack_bf16(f.z * iv, f.w * iv),
+                                          pack_bf16(h.x * iv, h.y * iv), pack_bf16(h.z * iv, h.w * iv));
             }
           }
         }

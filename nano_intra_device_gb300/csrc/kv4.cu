@@ -244,7 +244,7 @@ nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t 
   h->max_pages = max_pages_per_seq;
   h->device = dev;
   h->num_sms = sms;
-  const size_t cnt = ((size_t)sms * 4 + 255) / 256 * 256;
+  const size_t cnt = ((size_t)sms * 8 + 255) / 256 * 256;
   const size_t rec = ((size_t)sms * 2 * nf::kv4_record_bytes(shape->head_dim) + 255) / 256 * 256;
   const size_t tiles = (size_t)sms * 2 * nf::kv4_tile_record_bytes(shape->head_dim);
   if (cudaMalloc(&h->status, 256 + 2 * cnt + rec + tiles) != cudaSuccess ||

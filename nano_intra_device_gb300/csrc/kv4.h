@@ -70,7 +70,7 @@ struct Kv4AttnArgs {
   // requests of more rows than small_rows are the prefill kernel's
   int small_rows;
   float* tiles;          // [grid][2] records of kv4_tile_record_bytes
-  int* tile_counters;    // [grid], zero between launches
+  int* tile_counters;    // [grid][2], zero between launches
 };
 size_t kv4_record_bytes(int head_dim);
 size_t kv4_tile_record_bytes(int head_dim);
