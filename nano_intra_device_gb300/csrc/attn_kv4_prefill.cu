@@ -41,7 +41,7 @@ constexpr int KP_WARPS = 16;         // registers are dealt by warpgroups of fou
                                      // MMA warp and three that only take part in the prologue
 constexpr int KP_THREADS = KP_WARPS * 32;
 // 512 = 4 x 128 registers a thread at launch, dealt again by role
-constexpr int KP_DQ_REGS = 104, KP_SM_REGS = 176, KP_MMA_REGS = 56;
+constexpr int KP_DQ_REGS = 96, KP_SM_REGS = 184, KP_MMA_REGS = 48;
 static_assert(KP_DQ_REGS + 2 * KP_SM_REGS + KP_MMA_REGS == 512, "the shares of the launch's registers");
 constexpr int KP_M = 128;            // query vectors of a tile (tensor-memory lanes)
 constexpr int KP_N = 128;            // positions of a key block
