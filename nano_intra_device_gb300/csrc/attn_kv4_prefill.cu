@@ -690,10 +690,15 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
             }
           }
         }
-        // P as fp16 pairs over the first half of S
+        // P as fp16 pairs over the first half of S, and the row's sum
+        float2 ls4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < KP_N / 64; ++c) {
           uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]));
 #pragma unroll
           for (int i = 0; i < 32; ++i) w[i] = kp_pack(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]);
           tc_st_32x32b_x32(s_tmem + 32 * c, w);
@@ -701,15 +706,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         tc_wait_st();
         tc_fence_before();
         arrive(&bars->p_full[t]);
-        {
-          float2 ls4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < KP_N / 2; ++i) ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(x[2 * i], x[2 * i + 1]));
-          const float2 a2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
-          l += a2.x + a2.y;
-        }
+        const float2 a2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
+        l += a2.x + a2.y;
       }
       if (ok && !wait(&bars->o_full[t], np & 1)) ok = false;
       if (!ok) break;
