@@ -2,27 +2,44 @@
 // 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
 //
 // A tile is 128 query vectors: 128 / GRP consecutive rows of one request and the
-// GRP query heads of one KV head.  Per key block of 128 positions
+// GRP query heads of one KV head; a unit is two neighbouring tiles.  Per key
+// block of 128 positions and tile
 //   S = Q K^T   (M 128, N 128, K d),   O += P V   (M 128, N d, K 128),
 // both with fp16 operands and fp32 accumulators.
 //  * Four warps turn codes into fp16 operands: a lane loads half a row of a page
 //    (a scale for every 16 channels), converts a byte an instruction, multiplies
 //    by the scale (exact, see attn_kv4.cu) and stores 16-byte chunks in the
 //    128-byte swizzle the products read; K has a ring of its own, V another.
-//    The next block's codes are in registers while the ring is full.
-//  * One thread issues the products.  S of the next block runs while the softmax
-//    of this one does.
-//  * Eight warps own half a vector each: online softmax with a lazily raised
-//    maximum (base 2), P written as fp16 of 2^7 times its share of the running
-//    maximum, denominators summed in fp32.
+//    The next block's codes are in registers while the ring is full.  Both tiles
+//    use a block's operands: with one tile a CTA these four warps took issue
+//    slots and shared memory from the softmax of every block (299 us against 290
+//    in the case below).
+//  * One thread issues the products, tile by tile: P V of one tile and its next S
+//    run while the other tile's softmax does.  S of a tile stands in 128 columns
+//    of tensor memory, P over their first half: products run in their order, so
+//    the S that follows needs no barrier but P's.
+//  * Four softmax warps a tile, a thread a row: no exchange between threads.
+//    Online softmax with a lazily raised maximum (base 2), P as fp16 of 2^7 times
+//    its share of the running maximum, denominators summed in fp32.
 // Q is scaled by a power of two a vector so that fp16 holds all of bf16's bits.
 //
-// Work split: the key blocks of all (tile, KV head) units are laid end to end
-// (closed-form sums, as a tile's blocks grow with its position) and every CTA
+// Work split: the key blocks of all (unit, KV head) pairs are laid end to end
+// (closed-form sums, as a unit's blocks grow with its position) and every CTA
 // takes the same number.  A unit cut between CTAs is joined by the CTA that
 // arrives last, from fp32 records in the handle's workspace, in the order of the
 // pieces.  So a short chunk over a long prefix fills the GPU like a long prompt.
 // The rings run on over the ends of units.
+//
+// Measured (1985 rows over 4099 positions, 32 query and 8 KV heads of 128, 166
+// GFLOP, beside 63 decode rows): 213 us for this kernel, 232 for the call, 38 %
+// of the cuBLAS bf16 rate.  What bounds it: the softmax warps, two on each of an
+// SM's four schedulers, which issue in 37 % of the cycles; they wait for scores
+// and for their own chains, and a sixth of the waits is for instructions (four
+// roles' unrolled loops).  Tried and slower: two threads a row with the tiles one
+// after the other (290; three quarters of the scores' reads and an exchange of
+// maxima a block), four threads a row (354: 80 registers, spills), exponentials
+// by the old maximum before the new one is known (327), P through shared memory
+// (no difference), one lane polling for its warp (387 against 309).
 //
 // Every wait is bounded; on expiry the kernel flags ST_TIMEOUT, every role
 // leaves its loop, and the products issued finish before tensor memory is freed.
@@ -40,7 +57,8 @@ constexpr int KP_MMA_WARP = KP_DQ_WARPS + KP_SM_WARPS;
 constexpr int KP_WARPS = 16;         // registers are dealt by warpgroups of four: the last holds the
                                      // MMA warp and three that only take part in the prologue
 constexpr int KP_THREADS = KP_WARPS * 32;
-// 512 = 4 x 128 registers a thread at launch, dealt again by role
+// 512 = 4 x 128 registers a thread at launch, dealt again by role (104 / 176 / 56:
+// 237 us against 232, 112 / 168 / 64: 247)
 constexpr int KP_DQ_REGS = 96, KP_SM_REGS = 184, KP_MMA_REGS = 48;
 static_assert(KP_DQ_REGS + 2 * KP_SM_REGS + KP_MMA_REGS == 512, "the shares of the launch's registers");
 constexpr int KP_M = 128;            // query vectors of a tile (tensor-memory lanes)
@@ -331,8 +349,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     raise_status(a.status, ST_TIMEOUT);
     *abort_flag = 1;
   };
-  // One arrival and one poll a warp: the arrivals of 32 lanes go one after the
-  // other.  What a lane wrote before is ordered by the warp's barrier.
+  // One arrival a warp; what its lanes wrote before is ordered by the warp's
+  // barrier.  All lanes poll: one lane's poll costs more than 32 at once.
   auto arrive = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);

@@ -94,13 +94,13 @@ nf_status check_cache(const nf_kv_cache* c, bool fp4_only) {
 
 // A request of at most this many query vectors a KV head (rows * n_q / n_kv) goes
 // to the kernel of few rows, which reads its cache once for 8 of them; a longer
-// one to the 128-vector tiles, whose time hardly depends on how full they are.
+// one to the tiles of 128, whose time hardly depends on how full they are.
 // Measured, few rows against tiles, 32 query and 8 KV heads of 128, 16 requests
-// of 2000 positions: 45 / 64 us at 32 vectors, 70 / 64 at 64, 92 / 66 at 96; 128
-// requests of 500: 78 / 163, 129 / 164, 178 / 133.  With 8 query heads the two
-// meet at 64 vectors too (70 / 64), with 64 at 64 as well (68 / 64).  A single
-// request gains from the kernel of few rows for longer (25 / 43 at 96), which
-// cannot be told from the batch's sizes without its lengths.
+// of 2000 positions: 45 / 66 us at 32 vectors, 70 / 64 at 64, 92 / 64 at 96; 128
+// requests of 500: 78 / 177, 129 / 182, 178 / 184.  With 8 query heads 70 / 66 at
+// 64, with 64 heads 68 / 64 at 64 and 93 / 62 at 96.  A single request gains from
+// the kernel of few rows for longer (25 / 43 at 96), which cannot be told from
+// the batch's sizes without its lengths.
 constexpr int kSmallVecs = 64;
 
 // Frequencies of (theta, head_dim), computed once for each pair in use: 64
