@@ -25,6 +25,11 @@
 //    values.  The maximum is raised only when a score passes it by 2^8, so p
 //    stays below 2^15.
 //
+// The pages come by 16-byte asynchronous copies into a ring of two stages a warp,
+// which runs on over the ends of units; nothing but the warp itself waits for
+// them.  12 warps of 168 registers and two stages; 8 and 16 warps, rings of three
+// and four stages and loads straight to registers were all slower.
+//
 // Work split: every warp gets the same number of pages.  The pages of all
 // (request, column group, KV head) units are laid end to end, each unit behind
 // a few slots that stand for its fixed cost, and warp w takes the slots
@@ -34,6 +39,16 @@
 // CTA, one cut between CTAs through a record in the handle's workspace by the
 // CTA that arrives last, in the order of the pieces either way: the result does
 // not depend on timing.  The arrival counters are zero between launches.
+//
+// Measured, heads of 128:
+//   1000 rows of 600 positions (median), 64 query and 8 KV heads, 917 MB: 167 us,
+//     5.5 TB/s, 0.81 of the copy rate;
+//   64 rows of 600, 32 and 8 heads, 70 MB: 31 us; one row of 65,543: 28 us.
+// The first is bound by issue: about 105 clocks a page and KV head where the copy
+// rate gives 98, with 60 % of the issue slots and 54 % of the arithmetic pipe
+// (conversions, integer work) in use and the rest lost to fixed latencies.  The
+// other two are bound by latency: 3 us of launch, 3 to find the slots, 5 to 7 for
+// the last CTA's joins, whose code runs once and comes from memory.
 #include <type_traits>
 
 #include "common.cuh"
@@ -51,8 +66,11 @@ constexpr int KA_STAGES = 2;       // ring stages of a warp
 constexpr int KA_GROUP = 4608;     // bytes of a stage: 2 pages at d = 128, 4 at d = 64
 constexpr int KA_QUEUE = 8;        // pieces from what is worked on to what is fetched: at most one
                                    // a stage, the batch in use and the one after it
-constexpr uint32_t KA_FIXED = 3;   // slots a unit costs beside its pages
-constexpr uint32_t KA_MIN_QUOTA = 4;  // fewest slots of a warp
+// Slots a unit costs beside its pages (query, epilogue, joins).  1000 rows of the
+// table below at 1, 3, 5, 8, 12: 182, 171, 167, 170, 176 us; one long row 31, 30,
+// 28, 30, 29; 64 rows 31, 30, 31, 31, 31.
+constexpr uint32_t KA_FIXED = 5;
+constexpr uint32_t KA_MIN_QUOTA = 8;  // fewest slots of a warp (1, 4, 8: the same)
 constexpr float KA_LAZY = 8.f;
 constexpr float KA_SHIFT = 7.f;
 

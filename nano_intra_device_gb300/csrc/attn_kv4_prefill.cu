@@ -64,7 +64,7 @@ static_assert(KP_DQ_REGS + 2 * KP_SM_REGS + KP_MMA_REGS == 512, "the shares of t
 constexpr int KP_M = 128;            // query vectors of a tile (tensor-memory lanes)
 constexpr int KP_N = 128;            // positions of a key block
 constexpr int KP_REGION = 128 * 128; // 128 rows x 128 bytes: 64 fp16 columns of 128 rows
-constexpr int KP_FIXED = 1;          // blocks' worth of a unit's fixed cost
+constexpr int KP_FIXED = 1;          // blocks' worth of a unit's fixed cost (2, 4: 235, 232 us)
 constexpr float KP_SLACK = 8.f;
 constexpr float KP_SHIFT = 7.f;
 constexpr uint32_t KP_TMEM_COLS = 512;

@@ -19,6 +19,10 @@ namespace {
 // threads), then maps its own share of the tokens and of the requests.  No CTA
 // reads what another one writes: the page of a token past the held ones comes
 // from the ring, whose free part the call leaves alone, not from the table.
+// Measured: 64 requests of one token 5.3 us, 1801 requests 10.3, 4096 with 1024
+// prompts of 1000 tokens 27.8 (9.8 MB: 1.4 us of copy rate).  What bounds it is
+// latency: the sums over the requests, then one round of table reads a block of
+// tokens; in the last case the warps that move a prompt's pages.
 constexpr int BT_THREADS = 512;
 constexpr int BT_WARPS = BT_THREADS / 32;
 
@@ -35,7 +39,10 @@ __device__ __forceinline__ BtSeq bt_seq(const BlockTableArgs& a, int s) {
   return r;
 }
 
-constexpr int BT_FEW = 4;                        // pages a lane moves by itself
+// Pages a lane moves by itself; more take a warp.  0 (a warp for every request),
+// 4, no limit: 12.3, 10.3, 20.5 us for 1801 requests with two prompts; 28.7, 27.8,
+// 47.0 for 4096 with 1024.
+constexpr int BT_FEW = 4;
 constexpr int BT_PER = 2;                        // tokens of a thread and block
 constexpr int BT_TOKENS = BT_THREADS * BT_PER;
 
@@ -247,6 +254,11 @@ __global__ void __launch_bounds__(BT_THREADS) block_tables_kernel(const BlockTab
 // two scales), about one head in two hundred, the lane computes it again in
 // pairs of floats (dd.cuh).  V comes in bf16, where the comparison is exact: 8
 // bits against borders of at most 7.
+//
+// Measured: 64 tokens of 32 + 8 + 8 heads of 128 into 4 bits 6 us, into bf16 2048
+// tokens 16.4 us (50 MB: 7.4 at the copy rate).  8191 tokens of 64 + 8 + 8 heads
+// into 4 bits: 28 us for keys and values, which are bound by issue (the codes'
+// and borders' arithmetic), then 46 us for the queries at 64 % of the DRAM rate.
 constexpr int QK_THREADS = 256;
 constexpr int QK_MAX_TOK = 8;      // tokens a CTA handles at once: 1, 2, 4 or 8, a power of two
 // Bound of the error of a rotated value relative to |a| + |b| of its pair, in
@@ -748,6 +760,8 @@ __global__ void __launch_bounds__(QK_THREADS, PART == PART_Q ? 4 : 2)
 //
 // HBM-bound: a lane makes 8 channels of K and the same of V, so that a warp's
 // stores are whole 512-byte runs; it has RD_ITEMS tokens' loads in flight.
+// Measured: 30,000 tokens of 8 heads of 128 (158 MB) 31 us, 5.1 TB/s, 0.75 of the
+// copy rate; 333 tokens of 2 heads of 64 5.8 us, a launch.
 constexpr int RD_THREADS = 256;
 constexpr int RD_ITEMS = 4;
 
@@ -834,7 +848,10 @@ static cudaError_t launch_qk(const QkNormRopeArgs& a, const RopeFreq& f, int tok
 cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& a, const RopeFreq& f, bool fp4, int num_sms,
                                 cudaStream_t stream) {
   // one token a CTA until that fills the GPU three times, then up to 8, a warp
-  // each: fewer warps then load a token's angles and gains
+  // each: fewer warps then load a token's angles and gains.  8191 tokens of 80
+  // heads into 4 bits and back at 1, 2, 4, 8 tokens: 120, 96, 88 (in two launches),
+  // 84 us, and 93 for 8 in one launch; 2048 tokens of 48 heads into bf16: 21 at 1,
+  // 15 to 17 at 2 to 8.
   int tok = 1;
   while (tok < QK_MAX_TOK && a.n_tok >= 2 * tok * 3 * num_sms) tok *= 2;
   const int hpw = a.head_dim == 128 ? 4 : 8;  // heads of a group
