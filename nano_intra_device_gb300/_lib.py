@@ -454,6 +454,13 @@ def _dense(name, t, dtype, *shape):
                          f"got {t.dtype} {list(t.shape)}")
 
 
+def _arg(name, t, dtype, n):
+    """The address of a call's tensor, which has to hold n contiguous elements of dtype."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: need {n} contiguous elements of {dtype}, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
 class KvCache:
     """The nf_kv_cache of one layer, and the tensors it points to.
 
@@ -469,6 +476,8 @@ class KvCache:
             for n, t in (("K pool", k), ("V pool", v)):
                 _dense(n, t, torch.bfloat16, num_pages, s.n_kv_heads, s.page_size, s.head_dim)
         self.k, self.v = k, v
+        self.heads = (s.n_kv_heads, s.head_dim)
+        self.types = (torch.bfloat16, torch.int32)
         self.c = nf_kv_cache(fmt, num_pages, k.data_ptr(), None if v is None else v.data_ptr(), k_exp, v_exp)
 
 
@@ -515,20 +524,31 @@ def block_tables(args: BlockTables, stream=None):
 def qk_norm_rope(shape, qkv, q_gain, k_gain, tok_pos, tok_slot, q, cache: KvCache, stream=None):
     """nf_qk_norm_rope: per-head norm (gains None: none) and rotation of q and k, k and v appended
     to the cache.  qkv [n_tok, >= (n_q + 2 n_kv) d], rows may be strided."""
-    if qkv.stride(-1) != 1:
-        raise ValueError("qkv: the rows must be contiguous")
+    (bf16, i32), n = cache.types, qkv.shape[0]
+    if qkv.dtype is not bf16 or qkv.dim() != 2 or qkv.stride(1) != 1:
+        raise ValueError("qkv: need bf16 [n_tok, width] with contiguous rows")
     s = make_shape(shape)
-    if qkv.shape[1] < (s.n_q_heads + 2 * s.n_kv_heads) * s.head_dim:
+    d = s.head_dim
+    if cache.heads != (s.n_kv_heads, d):
+        raise ValueError("the cache was made for another shape")
+    if qkv.shape[1] < (s.n_q_heads + 2 * s.n_kv_heads) * d:
         raise ValueError("qkv: rows too short for the shape")
-    check(lib().nf_qk_norm_rope(ctypes.byref(s), ptr(qkv), qkv.stride(0), ptr(q_gain), ptr(k_gain), ptr(tok_pos),
-                                ptr(tok_slot), qkv.shape[0], ptr(q), ctypes.byref(cache.c), stream_handle(stream)))
+    check(lib().nf_qk_norm_rope(ctypes.byref(s), qkv.data_ptr(), qkv.stride(0),
+                                None if q_gain is None else _arg("q_gain", q_gain, bf16, d),
+                                None if k_gain is None else _arg("k_gain", k_gain, bf16, d),
+                                _arg("tok_pos", tok_pos, i32, n), _arg("tok_slot", tok_slot, i32, n), n,
+                                _arg("q", q, bf16, n * s.n_q_heads * d), ctypes.byref(cache.c),
+                                stream_handle(stream)))
 
 
 def kv4_read(shape, cache: KvCache, slots, k, v, stream=None):
     """nf_kv4_read: rows of the 4-bit cache by slot, as bf16 k, v [n, n_kv, d]."""
-    s = make_shape(shape)
-    check(lib().nf_kv4_read(ctypes.byref(s), ctypes.byref(cache.c), ptr(slots), slots.numel(), ptr(k), ptr(v),
-                            stream_handle(stream)))
+    s, (bf16, i32), n = make_shape(shape), cache.types, slots.numel()
+    if cache.heads != (s.n_kv_heads, s.head_dim):
+        raise ValueError("the cache was made for another shape")
+    size = n * s.n_kv_heads * s.head_dim
+    check(lib().nf_kv4_read(ctypes.byref(s), ctypes.byref(cache.c), _arg("slots", slots, i32, n), n,
+                            _arg("k", k, bf16, size), _arg("v", v, bf16, size), stream_handle(stream)))
 
 
 class Kv4:
@@ -538,6 +558,8 @@ class Kv4:
         self.h = c_void_p()
         self.max_pages = max_pages
         s = make_shape(shape)
+        self.heads = (s.n_kv_heads, s.head_dim)
+        self.row = s.n_q_heads * s.head_dim
         check(lib().nf_kv4_create(ctypes.byref(s), num_pages, max_pages, ctypes.byref(self.h)))
 
     def poll(self, wait=True):
@@ -558,10 +580,18 @@ class Kv4:
 def attention_kv4(handle: Kv4, q, cache: KvCache, block_table, seq_lens, o, tok_begin=None, stream=None):
     """nf_attention_kv4: attention of a step's tokens over the 4-bit cache (tok_begin None: one row
     per request)."""
+    (bf16, i32), n, rows = cache.types, seq_lens.numel(), q.shape[0]
     if block_table.shape[1] != handle.max_pages:
         raise ValueError(f"block_table: need rows of {handle.max_pages} entries, got {block_table.shape[1]}")
-    check(lib().nf_attention_kv4(handle.h, ptr(q), ctypes.byref(cache.c), ptr(block_table), ptr(seq_lens),
-                                 ptr(tok_begin), seq_lens.numel(), q.shape[0], ptr(o), stream_handle(stream)))
+    if cache.heads != handle.heads:
+        raise ValueError("the cache was made for another shape than the handle")
+    if o.dtype is not bf16 or o.numel() < rows * handle.row or not o.is_contiguous():
+        raise ValueError("o: need contiguous bf16 rows, as many as q's at least")
+    check(lib().nf_attention_kv4(handle.h, _arg("q", q, bf16, rows * handle.row), ctypes.byref(cache.c),
+                                 _arg("block_table", block_table, i32, n * handle.max_pages),
+                                 _arg("seq_lens", seq_lens, i32, n),
+                                 None if tok_begin is None else _arg("tok_begin", tok_begin, i32, n + 1), n, rows,
+                                 o.data_ptr(), stream_handle(stream)))
 
 
 def plan_search(shape, batch, profile_json=None, num_sms=152, n_layers=1):

@@ -2,6 +2,7 @@
 refusals of its entry points (nothing is launched)."""
 import ctypes
 import os
+import types
 
 import numpy as np
 import pytest
@@ -218,3 +219,28 @@ def test_binding_checks_tensors():
     for at, t in ((0, z(3).long()), (1, z(4)), (2, z(2, 4)), (2, z(3, 8)[:, ::2]), (4, z(3)), (5, z(2)), (6, z(3)), (8, z(8))):
         with pytest.raises(ValueError):
             _lib.BlockTables(*[t if k == at else x for k, x in enumerate(good)])
+
+
+def test_binding_checks_a_calls_tensors():
+    """Types, sizes and strides that the addresses alone do not show, and a cache of another shape."""
+    i, b = torch.int32, torch.bfloat16
+    cache = _lib.KvCache(SHAPE, 8, _lib.NF_KV_FP4, torch.zeros(8, 2, 2, 576, dtype=torch.uint8))
+    other = _lib.KvCache(wl.Shape(hidden=256, n_q=4, n_kv=4, head_dim=64, ffn=16), 8, _lib.NF_KV_FP4, torch.zeros(8, 4, 2, 576, dtype=torch.uint8))
+    n, row = 3, SHAPE.n_q * 64
+    z = lambda *n, t=i: torch.zeros(n, dtype=t)  # noqa: E731
+    good = dict(qkv=z(n, 512, t=b), q_gain=z(64, t=b), k_gain=None, tok_pos=z(n), tok_slot=z(n), q=z(n, row, t=b), cache=cache)
+    for bad in (dict(qkv=z(n, 512)), dict(qkv=z(512, n, t=b).T), dict(qkv=z(n, 504, t=b)), dict(q_gain=z(64)), dict(k_gain=z(32, t=b)),
+                dict(tok_pos=z(n + 1)), dict(tok_slot=z(n).long()), dict(q=z(n, row)), dict(q=z(n + 1, row, t=b)), dict(q=z(row, n, t=b).T),
+                dict(cache=other)):
+        with pytest.raises(ValueError):
+            _lib.qk_norm_rope(SHAPE, **(good | bad))
+    good = dict(cache=cache, slots=z(n), k=z(n, 128, t=b), v=z(n, 128, t=b))
+    for bad in (dict(slots=z(n).long()), dict(slots=z(2 * n)[::2]), dict(k=z(n, 128)), dict(v=z(n, 64, t=b)), dict(cache=other)):
+        with pytest.raises(ValueError):
+            _lib.kv4_read(SHAPE, **(good | bad))
+    handle = types.SimpleNamespace(h=None, max_pages=5, heads=(2, 64), row=row)
+    good = dict(q=z(n, row, t=b), cache=cache, block_table=z(2, 5), seq_lens=z(2), o=z(n, row, t=b), tok_begin=z(3))
+    for bad in (dict(q=z(n, row)), dict(q=z(n, row // 2, t=b)), dict(block_table=z(2, 4)), dict(block_table=z(3, 5)), dict(block_table=z(2, 10)[:, ::2]),
+                dict(seq_lens=z(2).long()), dict(o=z(n - 1, row, t=b)), dict(o=z(n, row)), dict(o=z(row, n, t=b).T), dict(tok_begin=z(2)), dict(cache=other)):
+        with pytest.raises(ValueError):
+            _lib.attention_kv4(handle, **(good | bad))
