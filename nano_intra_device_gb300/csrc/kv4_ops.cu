@@ -150,12 +150,14 @@ __global__ void __launch_bounds__(BT_THREADS) block_tables_kernel(const BlockTab
     at.take += grow;
     at.back += back;
   }
-  // Requests that move more, a warp each: the warps look through 32 at a time.
-  for (long long w0 = (static_cast<long long>(blockIdx.x) * BT_WARPS + warp) * 32; w0 < a.n_seq;
-       w0 += static_cast<long long>(gridDim.x) * BT_THREADS) {
+  // Requests that move more, a warp each: a warp looks through its share, up to 32
+  // at a time.
+  const long long warps = static_cast<long long>(gridDim.x) * BT_WARPS;
+  const int share = static_cast<int>(min((a.n_seq + warps - 1) / warps, 32ll));
+  for (long long w0 = (static_cast<long long>(blockIdx.x) * BT_WARPS + warp) * share; w0 < a.n_seq; w0 += warps * share) {
     const int mine = static_cast<int>(min(w0 + lane, static_cast<long long>(a.n_seq - 1)));
     const BtSeq m = bt_seq(a, mine);
-    unsigned many = __ballot_sync(0xffffffffu, w0 + lane < a.n_seq && max(m.pl - m.ph, m.ph - m.pl) > BT_FEW);
+    unsigned many = __ballot_sync(0xffffffffu, lane < share && w0 + lane < a.n_seq && max(m.pl - m.ph, m.ph - m.pl) > BT_FEW);
     while (many) {
       const int src = __ffs(many) - 1;
       many &= many - 1;
