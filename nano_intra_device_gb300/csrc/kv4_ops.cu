@@ -19,10 +19,10 @@ namespace {
 // threads), then maps its own share of the tokens and of the requests.  No CTA
 // reads what another one writes: the page of a token past the held ones comes
 // from the ring, whose free part the call leaves alone, not from the table.
-// Measured: 64 requests of one token 5.3 us, 1801 requests 10.3, 4096 with 1024
-// prompts of 1000 tokens 27.8 (9.8 MB: 1.4 us of copy rate).  What bounds it is
+// Measured: 64 requests of one token 6.0 us, 1801 requests 8.2, 4096 with 1024
+// prompts of 1000 tokens 16.4 (9.8 MB: 1.4 us of copy rate).  What bounds it is
 // latency: the sums over the requests, then one round of table reads a block of
-// tokens; in the last case the warps that move a prompt's pages.
+// tokens, while the same warps move the prompts' pages.
 constexpr int BT_THREADS = 512;
 constexpr int BT_WARPS = BT_THREADS / 32;
 
@@ -39,12 +39,13 @@ __device__ __forceinline__ BtSeq bt_seq(const BlockTableArgs& a, int s) {
   return r;
 }
 
-// Pages a lane moves by itself; more take a warp.  0 (a warp for every request),
-// 4, no limit: 12.3, 10.3, 20.5 us for 1801 requests with two prompts; 28.7, 27.8,
-// 47.0 for 4096 with 1024.
+// Pages a lane moves by itself; more take a warp.  With three CTAs for 1801
+// requests and four an SM for 4096, at 0 (a warp for every request), 4 and no limit:
+// 12.3, 10.3, 20.5 us for 1801 with two prompts; 28.7, 27.8, 47.0 for 4096 with 1024.
 constexpr int BT_FEW = 4;
-constexpr int BT_PER = 2;                        // tokens of a thread and block
+constexpr int BT_PER = 4;                        // tokens of a thread and block
 constexpr int BT_TOKENS = BT_THREADS * BT_PER;
+constexpr int BT_REQS = 32;                      // requests for each of which a launch has a CTA at least
 
 // What the tokens of a request in a block of tokens need: the request, the
 // position of its first token there, the pages it held, those taken before it.
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(QK_THREADS, PART == PART_Q ? 4 : 2)
 // HBM-bound: a lane makes 8 channels of K and the same of V, so that a warp's
 // stores are whole 512-byte runs; it has RD_ITEMS tokens' loads in flight.
 // Measured: 30,000 tokens of 8 heads of 128 (158 MB) 31 us, 5.1 TB/s, 0.75 of the
-// copy rate; 333 tokens of 2 heads of 64 5.8 us, a launch.
+// copy rate; 333 tokens of 2 heads of 64 3.3 us in a graph, a launch.
 constexpr int RD_THREADS = 256;
 constexpr int RD_ITEMS = 4;
 
@@ -819,9 +820,13 @@ __global__ void __launch_bounds__(RD_THREADS)
 }  // namespace
 
 cudaError_t launch_block_tables(const BlockTableArgs& a, int num_sms, cudaStream_t stream) {
-  // a CTA for every block of tokens the caller has room for, up to four an SM
-  const long long want = (static_cast<long long>(a.tok_cap) + BT_TOKENS - 1) / BT_TOKENS;
-  const int grid = static_cast<int>(want < 1 ? 1 : want > 4 * num_sms ? 4 * num_sms : want);
+  // a CTA for every block of tokens the caller has room for and for every BT_REQS
+  // requests, up to two an SM.  1801 requests / 4096 with half a million tokens:
+  // 8.2 / 16.4 us; without the second 12.3 / 16.4; blocks of half the tokens 9.0 /
+  // 18.4; up to four CTAs an SM 20.4, one 20.5 (with the smaller blocks) for the latter
+  const long long blocks = (static_cast<long long>(a.tok_cap) + BT_TOKENS - 1) / BT_TOKENS;
+  const long long want = max(blocks, (static_cast<long long>(a.n_seq) + BT_REQS - 1) / BT_REQS);
+  const int grid = static_cast<int>(min(want, 2ll * num_sms));
   block_tables_kernel<<<grid, BT_THREADS, 0, stream>>>(a);
   return cudaGetLastError();
 }
