@@ -501,7 +501,8 @@ nf_status nf_block_tables(const int32_t* held, const int32_t* seq_lens, int32_t 
  *   the v heads; ld >= (n_q + 2 n_kv) * head_dim, a multiple of 8.
  * q_gain, k_gain: device bf16 [head_dim], or NULL: those heads are not normed.
  *   Normed heads become u * gain / sqrt(mean(u^2) + shape->rms_eps); the sum
- *   of squares is held in fp32 and must not pass its range.
+ *   of squares is held in fp32 and must not pass its range (nor, with
+ *   rms_eps = 0, the squares fall below its normal numbers).
  * tok_pos, tok_slot: device int32 [n_tok].  Rotation as in nf_layer_step (pairs
  *   i and i + head_dim / 2, angle pos * rope_theta^(-2i / head_dim)), accurate
  *   at every 32-bit position.  A token whose slot is outside
@@ -521,7 +522,8 @@ nf_status nf_kv4_read(const nf_model_shape* shape, const nf_kv_cache* cache, con
 
 /* Attention over an NF_KV_FP4 cache.  The handle owns the device workspace and
  * the status word, made on the current device; like a plan it serves one stream
- * at a time, and two captured graphs that use it must not run at once.
+ * at a time, and two captured graphs that use it must not run at once.  The
+ * workspace is about 43 MB at head_dim 128, half of that at 64.
  * Shapes as nf_model_shape allows; 1 <= max_pages_per_seq. */
 typedef struct nf_kv4_s* nf_kv4;
 nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t max_pages_per_seq,
@@ -533,7 +535,7 @@ nf_status nf_kv4_poll(nf_kv4 h, int wait);
 
 /* Causal GQA attention of a step's tokens over the cache, which must already
  * hold the step's K and V.
- * q, o: device bf16 [n_tok, n_q, head_dim].  block_table: device int32
+ * q, o: device bf16 [n_tok, n_q, head_dim], not overlapping.  block_table: device int32
  *   [n_seq, max_pages_per_seq].  seq_lens: device int32 [n_seq], lengths after
  *   the step.  tok_begin: device int32 [n_seq + 1], request s owns the rows
  *   [tok_begin[s], tok_begin[s + 1]), or NULL: one row each (n_tok = n_seq).
