@@ -19,6 +19,7 @@ struct nf_kv4_s {
   uint32_t* status = nullptr;
   int *counters = nullptr, *tile_counters = nullptr;
   float *records = nullptr, *tiles = nullptr;
+  size_t zeroed = 0;  // bytes from status on that a launch expects to be zero
 };
 
 namespace {
@@ -247,8 +248,9 @@ nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t 
   const size_t cnt = ((size_t)sms * 8 + 255) / 256 * 256;
   const size_t rec = ((size_t)sms * 2 * nf::kv4_record_bytes(shape->head_dim) + 255) / 256 * 256;
   const size_t tiles = (size_t)sms * 2 * nf::kv4_tile_record_bytes(shape->head_dim);
-  if (cudaMalloc(&h->status, 256 + 2 * cnt + rec + tiles) != cudaSuccess ||
-      cudaMemset(h->status, 0, 256 + 2 * cnt) != cudaSuccess) {
+  h->zeroed = 256 + 2 * cnt;
+  if (cudaMalloc(&h->status, h->zeroed + rec + tiles) != cudaSuccess ||
+      cudaMemset(h->status, 0, h->zeroed) != cudaSuccess) {
     cudaGetLastError();
     nf_kv4_destroy(h);
     return fail4(NF_ERR_OOM, "cudaMalloc of the workspace failed");
@@ -279,7 +281,12 @@ nf_status nf_kv4_poll(nf_kv4 h, int wait) {
   uint32_t st = 0;
   NF_CUDA4(cudaMemcpy(&st, h->status, 4, cudaMemcpyDeviceToHost));
   if (st) NF_CUDA4(cudaMemset(h->status, 0, 4));
-  if (st & nf::ST_TIMEOUT) return fail4(NF_ERR_TIMEOUT, "a device wait timed out (status 0x%x)", st);
+  if (st & nf::ST_TIMEOUT) {
+    // pieces that were given up never arrived: the counters start over
+    NF_CUDA4(cudaDeviceSynchronize());
+    NF_CUDA4(cudaMemset(h->status, 0, h->zeroed));
+    return fail4(NF_ERR_TIMEOUT, "a device wait timed out (status 0x%x)", st);
+  }
   if (st)
     return fail4(NF_ERR_DEVICE, "device-side check failed (status 0x%x: %s%s%s)", st,
                  (st & nf::ST_BAD_PAGE) ? "page id out of range " : "",
