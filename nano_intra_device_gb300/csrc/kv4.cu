@@ -99,10 +99,14 @@ nf_status check_cache(const nf_kv_cache* c, bool fp4_only) {
 // Measured, few rows against tiles, 32 query and 8 KV heads of 128, 16 requests
 // of 2000 positions: 45 / 66 us at 32 vectors, 70 / 64 at 64, 92 / 64 at 96; 128
 // requests of 500: 78 / 177, 129 / 182, 178 / 184.  With 8 query heads 70 / 66 at
-// 64, with 64 heads 68 / 64 at 64 and 93 / 62 at 96.  A single request gains from
-// the kernel of few rows for longer (25 / 43 at 96), which cannot be told from
-// the batch's sizes without its lengths.
+// 64, with 64 heads 68 / 64 at 64 and 93 / 62 at 96.
 constexpr int kSmallVecs = 64;
+// A launch of tiles takes 35 to 40 us however little there is to do (its roles'
+// code comes from memory once).  So where the kernel of few rows can at most visit
+// this many (page, KV head, 8 vectors) an SM, by the longest request that the
+// handle allows, every request goes there: 128 vectors of one request of 2000
+// positions (105 an SM) 25 / 43 us, of 8000 (421) 43 / 51, of 32,000 (1684) 113 / 68.
+constexpr int kFewVisits = 500;
 
 // Frequencies of (theta, head_dim), computed once for each pair in use: 64
 // powl calls cost more than the launch.
@@ -338,7 +342,8 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
   a.counters = h->counters;
   a.tiles = h->tiles;
   a.tile_counters = h->tile_counters;
-  a.small_rows = kSmallVecs / (a.n_q / a.n_kv);
+  const double visits = (double)n_tok * a.n_q / 8 * a.max_pages;
+  a.small_rows = visits <= (double)kFewVisits * h->num_sms ? n_tok : kSmallVecs / (a.n_q / a.n_kv);
   const bool tiles = tok_begin && n_tok > a.small_rows;
   if (tiles) NF_CUDA4(nf::launch_attention_kv4_prefill(a, static_cast<cudaStream_t>(stream)));
   NF_CUDA4(nf::launch_attention_kv4(a, tiles, static_cast<cudaStream_t>(stream)));

@@ -456,34 +456,40 @@ def test_attention_many_rows(n):
     check_attention(shape_of(4, 2, 64), *attention_case(r, 4, 2, 64, lens, [1] * n), lens, [1] * n)
 
 
+WIDE = 40000  # pages a request may have: chunks of a few rows on go to the tiles, with None to the kernel of few rows
+
+
+@pytest.mark.parametrize("width", [None, WIDE])
 @pytest.mark.parametrize("n_q,n_kv,d", [(1, 1, 64), (2, 1, 128), (8, 2, 128), (8, 1, 64), (8, 8, 128)])
 @pytest.mark.parametrize("lens,q_lens", [([2], [2]), ([9], [9]), ([40, 7], [3, 7]), ([5, 130, 1, 0, 17], [1, 5, 1, 2, 17]),
                                          ([200, 64, 300], [127, 64, 129]), ([3, 500], [5, 33]), ([1000], [40])])
-def test_attention_chunks(n_q, n_kv, d, lens, q_lens):
+def test_attention_chunks(n_q, n_kv, d, lens, q_lens, width):
     """Chunks from two rows on, whole prompts and continued ones; more rows than positions (zeros first)."""
     r = np.random.default_rng(sum(lens) + n_q)
-    got = check_attention(shape_of(n_q, n_kv, d), *attention_case(r, n_q, n_kv, d, lens, q_lens), lens, q_lens)
+    got = check_attention(shape_of(n_q, n_kv, d), *attention_case(r, n_q, n_kv, d, lens, q_lens, width=width), lens, q_lens)
     at = 0
     for n, m in zip(lens, q_lens):
         assert not got[at:at + max(0, m - n)].any()
         at += m
 
 
-def test_attention_padded_batch_and_empty_requests():
+@pytest.mark.parametrize("width", [9, WIDE])
+def test_attention_padded_batch_and_empty_requests(width):
     r = np.random.default_rng(11)
     lens, q_lens = [50, 0, 33, 20], [3, 0, 1, 20]
-    case = attention_case(r, 4, 2, 64, lens, q_lens, width=9)
+    case = attention_case(r, 4, 2, 64, lens, q_lens, width=width)
     check_attention(shape_of(4, 2, 64), *case, lens, q_lens, pad_rows=13)
 
 
+@pytest.mark.parametrize("width", [None, WIDE])
 @pytest.mark.parametrize("exps", [(0, 0), (2, -3), (-5, 20)])
 @pytest.mark.parametrize("q_scale", [1e-4, 1.0, 30.0, 1e18])
-def test_attention_magnitudes(exps, q_scale):
+def test_attention_magnitudes(exps, q_scale, width):
     """Flat to one-hot weights; queries far outside fp16's range."""
     r = np.random.default_rng(12)
     lens, q_lens = [120, 1, 16, 100], [1, 1, 1, 50]
     scale = q_scale if q_scale < 1e10 else 1.0
-    pool, bt, q = attention_case(r, 4, 2, 64, lens, q_lens, scale)
+    pool, bt, q = attention_case(r, 4, 2, 64, lens, q_lens, scale, width=width)
     if q_scale > 1e10:  # one row large, where its scores stay apart: one-hot
         q[0] = (q[0].float() * q_scale).to(torch.bfloat16)
         q[1] = (q[1].float() / q_scale).to(torch.bfloat16)
@@ -536,11 +542,12 @@ def test_attention_bad_pages_and_lengths_are_reported():
     check_attention(shape, pool, good, q, lens, [1, 1], handle=h)
 
 
-def test_attention_bad_rows_stay_inside():
+@pytest.mark.parametrize("width", [None, WIDE])
+def test_attention_bad_rows_stay_inside(width):
     r = np.random.default_rng(15)
     shape = shape_of(4, 2, 64)
     lens = [40, 20, 30]
-    pool, bt, q = attention_case(r, 4, 2, 64, lens, [2, 3, 1])
+    pool, bt, q = attention_case(r, 4, 2, 64, lens, [2, 3, 1], width=width)
     h = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
     for begin in ([0, 2, 5, 900], [0, -4, 5, 6], [2 ** 31 - 1, 2, 5, 6], [3, 2, 1, 0], [-2 ** 31, 0, 2 ** 31 - 1, 6]):
         run_attention(shape, pool, bt, q, lens, [2, 3, 1], begin=begin, handle=h, poll=False)
@@ -571,11 +578,12 @@ def test_attention_refusals():
         _lib.attention_kv4(h, q[:2], _lib.KvCache(shape, 8, _lib.NF_KV_BF16, bf, bf), bt, sl, torch.empty_like(q))
 
 
-def test_attention_repeats_bit_for_bit_in_a_graph_and_on_another_stream():
+@pytest.mark.parametrize("width", [None, WIDE])
+def test_attention_repeats_bit_for_bit_in_a_graph_and_on_another_stream(width):
     r = np.random.default_rng(16)
     shape = shape_of(8, 2, 128)
     lens, q_lens = [700, 3, 260, 150], [1, 1, 1, 140]
-    pool, bt, q = attention_case(r, 8, 2, 128, lens, q_lens)
+    pool, bt, q = attention_case(r, 8, 2, 128, lens, q_lens, width=width)
     h = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
     cache = _lib.KvCache(shape, pool.shape[0], _lib.NF_KV_FP4, torch.from_numpy(pool).to(DEV))
     qd, btd, ld = q.to(DEV), dev32(bt), dev32(lens)
@@ -610,12 +618,12 @@ def poison(r, pool, bt, n, lo, d):
 
 @pytest.mark.parametrize("n_q,n_kv,d", [(1, 1, 64), (4, 2, 128), (8, 2, 64), (8, 1, 128)])
 @pytest.mark.parametrize("lens,q_lens", [([40], [12]), ([9], [9]), ([300, 5], [200, 1]), ([1000, 33], [70, 17]), ([17, 200], [17, 8])])
-@pytest.mark.parametrize("seed", [0, 1, 2])
-def test_attention_nan_reaches_the_rows_that_see_it(n_q, n_kv, d, lens, q_lens, seed):
+@pytest.mark.parametrize("seed,width", [(0, None), (1, None), (2, WIDE), (3, WIDE)])
+def test_attention_nan_reaches_the_rows_that_see_it(n_q, n_kv, d, lens, q_lens, seed, width):
     """A NaN of K or V at a position of the chunk: rows before it keep their values."""
     r = np.random.default_rng(100 * seed + lens[0])
     shape = shape_of(n_q, n_kv, d)
-    pool, bt, q = attention_case(r, n_q, n_kv, d, lens, q_lens)
+    pool, bt, q = attention_case(r, n_q, n_kv, d, lens, q_lens, width=width)
     poison(r, pool, bt, lens[0], lens[0] - q_lens[0], d)
     got = run_attention(shape, pool, bt, q, lens, q_lens)
     q64 = q.double().numpy()
@@ -629,12 +637,12 @@ def test_attention_nan_reaches_the_rows_that_see_it(n_q, n_kv, d, lens, q_lens, 
     assert (np.abs(got - want)[clean] <= bound[clean]).all()
 
 
-@pytest.mark.parametrize("q_len", [1, 9, 60])
+@pytest.mark.parametrize("q_len,width", [(1, None), (9, None), (60, None), (60, WIDE), (70, WIDE)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_attention_a_bad_query_spoils_its_own_row(q_len, bad):
+def test_attention_a_bad_query_spoils_its_own_row(q_len, bad, width):
     r = np.random.default_rng(q_len)
     lens, q_lens = [200, 70], [q_len, q_len]
-    pool, bt, q = attention_case(r, 4, 2, 64, lens, q_lens)
+    pool, bt, q = attention_case(r, 4, 2, 64, lens, q_lens, width=width)
     shape = shape_of(4, 2, 64)
     good = run_attention(shape, pool, bt, q, lens, q_lens)
     q[0, 1, 5] = bad
@@ -644,22 +652,24 @@ def test_attention_a_bad_query_spoils_its_own_row(q_len, bad):
     assert np.array_equal(got, good)
 
 
+@pytest.mark.parametrize("width", [None, WIDE])
 @pytest.mark.parametrize("n_q,n_kv,d,lens,q_lens", [
     (8, 1, 128, [6000], [130]), (4, 4, 64, [5000, 3, 900, 64], [77, 3, 65, 64]), (8, 2, 128, [2500, 60, 16, 18, 200], [900, 17, 16, 18, 1]), (2, 1, 64, [333, 32, 5000], [33, 32, 31]),
     (2, 2, 128, [1500], [1500]), (16, 2, 64, [40, 0, 10, 700, 8], [40, 30, 40, 128, 9])])
-def test_attention_long_chunks(n_q, n_kv, d, lens, q_lens):
+def test_attention_long_chunks(n_q, n_kv, d, lens, q_lens, width):
     """Tiles cut between CTAs, chunks on both sides of what one kernel takes, tiles without a position."""
     r = np.random.default_rng(lens[0])
-    check_attention(shape_of(n_q, n_kv, d), *attention_case(r, n_q, n_kv, d, lens, q_lens), lens, q_lens, pad_rows=3)
+    check_attention(shape_of(n_q, n_kv, d), *attention_case(r, n_q, n_kv, d, lens, q_lens, width=width), lens, q_lens, pad_rows=3)
 
 
+@pytest.mark.parametrize("width", [None, 1000])
 @pytest.mark.parametrize("n_q,n_kv", [(2, 2), (8, 1)])
-def test_attention_many_chunks(n_q, n_kv):
+def test_attention_many_chunks(n_q, n_kv, width):
     """More requests than threads, every third of them with rows for the tiles."""
     r = np.random.default_rng(n_q)
     q_lens = np.where(np.arange(700) % 3 == 0, 64 * n_kv // n_q - 1 + np.arange(700) % 5, np.arange(700) % 4)
     lens = np.maximum(q_lens + r.integers(-2, 60, 700), 0)
-    check_attention(shape_of(n_q, n_kv, 64), *attention_case(r, n_q, n_kv, 64, lens, q_lens), lens, q_lens)
+    check_attention(shape_of(n_q, n_kv, 64), *attention_case(r, n_q, n_kv, 64, lens, q_lens, width=width), lens, q_lens)
 
 
 def test_attention_two_handles_at_once():
@@ -667,7 +677,7 @@ def test_attention_two_handles_at_once():
     shape = shape_of(8, 2, 128)
     jobs = []
     for lens, q_lens in (([3000, 40], [300, 1]), ([2000, 500, 7], [1, 200, 7])):
-        pool, bt, q = attention_case(r, 8, 2, 128, lens, q_lens)
+        pool, bt, q = attention_case(r, 8, 2, 128, lens, q_lens, width=WIDE)
         h = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
         cache = _lib.KvCache(shape, pool.shape[0], _lib.NF_KV_FP4, torch.from_numpy(pool).to(DEV))
         args = (h, q.to(DEV), cache, dev32(bt), dev32(lens))
