@@ -31,7 +31,7 @@
 // The rings run on over the ends of units.
 //
 // Measured (1985 rows over 4099 positions, 32 query and 8 KV heads of 128, 166
-// GFLOP, beside 63 decode rows): 213 us for this kernel, 232 for the call, 38 %
+// GFLOP, beside 63 decode rows): 209 us for this kernel, 231 for the call, 38 %
 // of the cuBLAS bf16 rate.  What bounds it: the softmax warps, two on each of an
 // SM's four schedulers, which issue in 37 % of the cycles; they wait for scores
 // and for their own chains, and a sixth of the waits is for instructions (four
