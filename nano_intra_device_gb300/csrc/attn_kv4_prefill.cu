@@ -16,8 +16,8 @@
 //    in the case below).
 //  * One thread issues the products, tile by tile: P V of one tile and its next S
 //    run while the other tile's softmax does.  S of a tile stands in 128 columns
-//    of tensor memory, P over their first half: products run in their order, so
-//    the S that follows needs no barrier but P's.
+//    of tensor memory, P over their first half; the next S waits until P is read,
+//    as products into different accumulators have no order of their own (12 us).
 //  * Four softmax warps a tile, a thread a row: no exchange between threads.
 //    Online softmax with a lazily raised maximum (base 2), P as fp16 of 2^7 times
 //    its share of the running maximum, denominators summed in fp32.
@@ -31,15 +31,16 @@
 // The rings run on over the ends of units.
 //
 // Measured (1985 rows over 4099 positions, 32 query and 8 KV heads of 128, 166
-// GFLOP, beside 63 decode rows): 209 us for this kernel, 231 for the call, 38 %
-// of the cuBLAS bf16 rate.  What bounds it: the softmax warps, two on each of an
-// SM's four schedulers, which issue in 37 % of the cycles; they wait for scores
+// GFLOP, beside 63 decode rows): about 222 us for this kernel, 243 for the
+// call, 36 % of the cuBLAS bf16 rate.  What bounds it: the softmax warps, two on each of an
+// SM's four schedulers, which issue in a third of the cycles; they wait for scores
 // and for their own chains, and a sixth of the waits is for instructions (four
 // roles' unrolled loops).  Tried and slower: two threads a row with the tiles one
 // after the other (290; three quarters of the scores' reads and an exchange of
 // maxima a block), four threads a row (354: 80 registers, spills), exponentials
 // by the old maximum before the new one is known (327), P through shared memory
-// (no difference), one lane polling for its warp (387 against 309).
+// with S issued ahead (274), S in two halves around the wait for P (355), one lane
+// polling for its warp (387 against 309).
 //
 // Every wait is bounded; on expiry the kernel flags ST_TIMEOUT, every role
 // leaves its loop, and the products issued finish before tensor memory is freed.
@@ -58,8 +59,8 @@ constexpr int KP_WARPS = 16;         // registers are dealt by warpgroups of fou
                                      // MMA warp and three that only take part in the prologue
 constexpr int KP_THREADS = KP_WARPS * 32;
 // 512 = 4 x 128 registers a thread at launch, dealt again by role (104 / 176 / 56:
-// 237 us against 232, 112 / 168 / 64: 247)
-constexpr int KP_DQ_REGS = 96, KP_SM_REGS = 184, KP_MMA_REGS = 48;
+// 245 us against 243, 96 / 184 / 48: 251)
+constexpr int KP_DQ_REGS = 80, KP_SM_REGS = 184, KP_MMA_REGS = 64;
 static_assert(KP_DQ_REGS + 2 * KP_SM_REGS + KP_MMA_REGS == 512, "the shares of the launch's registers");
 constexpr int KP_M = 128;            // query vectors of a tile (tensor-memory lanes)
 constexpr int KP_N = 128;            // positions of a key block
@@ -76,6 +77,7 @@ struct KpBars {
   uint64_t v_full[KP_VST], v_empty[KP_VST];
   uint64_t s_full[2];                        // by tile: S of a block, and all products before it
   uint64_t p_full[2];                        // its softmax warps: P written (and O rescaled)
+  uint64_t pv_done[2];                       // P is read: S of the next block may take its columns
   uint64_t o_full[2];                        // the last product of a piece
   uint64_t meet[2];                          // a bounded barrier of a tile's softmax warps
   uint64_t drain;
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
       mbar_init(&bars->q_full[i], KP_SM_WARPS / 2);
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], KP_SM_WARPS / 2);
+      mbar_init(&bars->pv_done[i], 1);
       mbar_init(&bars->o_full[i], 1);
       mbar_init(&bars->meet[i], KP_SM_WARPS / 2);
     }
@@ -505,6 +508,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     uint32_t n = 0;                  // blocks
     uint32_t np0 = 0, np1 = 0;       // pieces and steps of either tile
     uint32_t st0 = 0, st1 = 0;
+    uint32_t pv0 = 0, pv1 = 0;       // and the products that an S followed
     auto s_product = [&](int t, uint32_t block) {
       const uint32_t k_addr = sbase + Lay::K_OFF + (block % KP_KST) * Lay::KV_BYTES;
 #pragma unroll
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           const bool more = j + 1 < p.j1;
           ok = mbar_wait(&bars->v_full[vs], (n / KP_VST) & 1, tmo, abort_flag);
           for (int t = 0; t < p.nt && ok; ++t) {
-            // P over S, then the next S over P: the products run in their order
+            // P over S, then the next S over P
             ok = mbar_wait(&bars->p_full[t], (t ? st1++ : st0++) & 1, tmo, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -547,8 +551,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
             any = true;
             if (t == p.nt - 1) tc_commit(&bars->v_empty[vs]);
             if (more) {
-              if (t == 0) ok = k_wait(n + 1);
+              tc_commit(&bars->pv_done[t]);
+              ok = (t > 0 || k_wait(n + 1)) && mbar_wait(&bars->pv_done[t], (t ? pv1++ : pv0++) & 1, tmo, abort_flag);
               if (!ok) break;
+              tc_fence_after();
               s_product(t, n + 1);
               if (t == p.nt - 1) tc_commit(&bars->k_empty[(n + 1) % KP_KST]);
             } else {
