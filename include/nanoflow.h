@@ -530,8 +530,18 @@ nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t 
                         nf_kv4* out);
 /* The caller sees to it that no call on the handle is still running. */
 void nf_kv4_destroy(nf_kv4 h);
-/* As nf_plan_poll, for the calls on this handle. */
+/* As nf_plan_poll, for the calls on this handle.  After NF_ERR_TIMEOUT the
+ * outputs of the calls since the last poll are undefined; the handle is as new. */
 nf_status nf_kv4_poll(nf_kv4 h, int wait);
+/* Limit of every device-side wait in the calls made (or captured) from now on,
+ * in [1, 1e10] (2e9 at first). */
+nf_status nf_kv4_set_timeout(nf_kv4 h, int64_t timeout_ns);
+/* Failure-detection self-test, as nf_plan_selftest_wait: in the calls from now
+ * on, CTA `cta` of the kernel of longer chunks leaves out an arrival for its
+ * block-th block of keys (part 0) or values (part 1).  What waits for it gives
+ * up after the handle's limit and nf_kv4_poll returns NF_ERR_TIMEOUT; a CTA
+ * without such a block computes as ever.  cta < 0 ends it. */
+nf_status nf_kv4_selftest_drop(nf_kv4 h, int32_t cta, int32_t part, int32_t block);
 
 /* Causal GQA attention of a step's tokens over the cache, which must already
  * hold the step's K and V.

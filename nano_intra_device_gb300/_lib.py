@@ -135,6 +135,8 @@ _SIGS = {
     "nf_kv4_create": (c_int, [POINTER(nf_model_shape), c_int32, c_int32, POINTER(c_void_p)]),
     "nf_kv4_destroy": (None, [c_void_p]),
     "nf_kv4_poll": (c_int, [c_void_p, c_int]),
+    "nf_kv4_set_timeout": (c_int, [c_void_p, c_int64]),
+    "nf_kv4_selftest_drop": (c_int, [c_void_p, c_int32, c_int32, c_int32]),
     "nf_attention_kv4": (c_int, [c_void_p, c_void_p, POINTER(nf_kv_cache), c_void_p, c_void_p, c_void_p,
                                  c_int32, c_int32, c_void_p, c_void_p]),
     "nf_plan_buffer_size": (c_int, [c_void_p, c_int32, POINTER(c_size_t)]),
@@ -564,6 +566,14 @@ class Kv4:
 
     def poll(self, wait=True):
         check(lib().nf_kv4_poll(self.h, 1 if wait else 0))
+
+    def set_timeout(self, timeout_ns):
+        """nf_kv4_set_timeout: the limit of the device-side waits of later calls."""
+        check(lib().nf_kv4_set_timeout(self.h, int(timeout_ns)))
+
+    def selftest_drop(self, cta, part=0, block=0):
+        """nf_kv4_selftest_drop: a wait of later calls runs out (cta < 0: no more)."""
+        check(lib().nf_kv4_selftest_drop(self.h, cta, part, block))
 
     def close(self):
         if self.h:

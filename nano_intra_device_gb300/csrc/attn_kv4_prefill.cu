@@ -42,8 +42,10 @@
 // with S issued ahead (274), S in two halves around the wait for P (355), one lane
 // polling for its warp (387 against 309).
 //
-// Every wait is bounded; on expiry the kernel flags ST_TIMEOUT, every role
-// leaves its loop, and the products issued finish before tensor memory is freed.
+// Every wait is bounded; on expiry the kernel flags ST_TIMEOUT and every role
+// leaves its loop.  Whichever role gave up, the products issued and the stores into
+// tensor memory finish before it is freed; that wait has a limit of its own, as the
+// caller's may be shorter than a product.
 #include "common.cuh"
 #include "kv4.cuh"
 #include "kv4.h"
@@ -70,6 +72,7 @@ constexpr float KP_SLACK = 8.f;
 constexpr float KP_SHIFT = 7.f;
 constexpr uint32_t KP_TMEM_COLS = 512;
 constexpr int KP_KST = 2, KP_VST = 2;  // ring stages of K and V
+constexpr uint64_t KP_DRAIN_NS = 2000000000ull;
 
 struct KpBars {
   uint64_t q_full[2];                        // by tile: its softmax warps have written Q
@@ -440,6 +443,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
     load_codes();
     load_ids();
     uint32_t n = 0;  // blocks made
+    // the block whose arrival this warp leaves out (self-test of the waits)
+    const uint32_t drop = static_cast<int>(blockIdx.x) == a.drop_cta && warp == 2 * a.drop_part ? a.drop_block : ~0u;
     while (made.have) {
       const uint32_t st = n % nst;
       if (!wait(&empty[st], ((n / nst) & 1) ^ 1)) {
@@ -496,7 +501,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         }
       }
       fence_proxy_async_smem();
-      arrive(&full[st]);
+      __syncwarp();
+      if (lane == 0 && n != drop) mbar_arrive(&full[st]);
       ++n;
       load_codes();
       load_ids();
@@ -565,13 +571,14 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-    if (!ok && lane == 0) {
-      if (!*abort_flag) give_up();
-      if (any) {  // the products already issued finish before tensor memory goes away
-        tc_commit(&bars->drain);
-        mbar_wait(&bars->drain, 0, tmo);
-      }
+    if (!ok && lane == 0 && !*abort_flag) give_up();
+    // Another role may give up after the last product was issued, so this wait does
+    // not ask who did; otherwise the softmax warps wait for the same products.
+    if (any) {
+      tc_commit(&bars->drain);
+      if (!mbar_wait(&bars->drain, 0, KP_DRAIN_NS)) raise_status(a.status, ST_TIMEOUT);
     }
+    __syncwarp();
   } else {
     kp_regs_more<KP_SM_REGS>();
     // --------------------------------------------------- softmax and epilogue
@@ -823,6 +830,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
       }
     }
     if (!ok && !*abort_flag) give_up();
+    tc_wait_st();  // a rescaled row, if a wait behind it was given up
   }
 
   tc_fence_before();

@@ -20,6 +20,8 @@ struct nf_kv4_s {
   int *counters = nullptr, *tile_counters = nullptr;
   float *records = nullptr, *tiles = nullptr;
   size_t zeroed = 0;  // bytes from status on that a launch expects to be zero
+  int64_t timeout_ns = 2000000000;
+  int drop_cta = -1, drop_block = 0, drop_part = 0;
 };
 
 namespace {
@@ -299,6 +301,24 @@ nf_status nf_kv4_poll(nf_kv4 h, int wait) {
   return NF_OK;
 }
 
+nf_status nf_kv4_set_timeout(nf_kv4 h, int64_t timeout_ns) {
+  if (!h) return fail4(NF_ERR_INVALID_ARG, "handle is NULL");
+  if (timeout_ns < 1 || timeout_ns > 10000000000LL)
+    return fail4(NF_ERR_INVALID_ARG, "timeout_ns must lie in [1, 1e10]");
+  h->timeout_ns = timeout_ns;
+  return NF_OK;
+}
+
+nf_status nf_kv4_selftest_drop(nf_kv4 h, int32_t cta, int32_t part, int32_t block) {
+  if (!h) return fail4(NF_ERR_INVALID_ARG, "handle is NULL");
+  if (cta >= h->num_sms || (cta >= 0 && (part < 0 || part > 1 || block < 0)))
+    return fail4(NF_ERR_INVALID_ARG, "cta must be below %d, part 0 or 1, block >= 0", h->num_sms);
+  h->drop_cta = cta < 0 ? -1 : cta;
+  h->drop_part = part;
+  h->drop_block = block;
+  return NF_OK;
+}
+
 nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
                            const int32_t* block_table, const int32_t* seq_lens,
                            const int32_t* tok_begin, int32_t n_seq, int32_t n_tok, void* o,
@@ -336,7 +356,10 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim) * std::ldexp(1.0, cache->k_exp));
   a.v_scale = nf::exp2_int(cache->v_exp);
   a.status = h->status;
-  a.timeout_ns = 2000000000ULL;
+  a.timeout_ns = static_cast<unsigned long long>(h->timeout_ns);
+  a.drop_cta = h->drop_cta;
+  a.drop_part = h->drop_part;
+  a.drop_block = static_cast<uint32_t>(h->drop_block);
   a.grid = h->num_sms;
   a.records = h->records;
   a.counters = h->counters;

@@ -64,6 +64,10 @@ struct Kv4AttnArgs {
   float v_scale;     // 2^v_exp
   uint32_t* status;
   unsigned long long timeout_ns;
+  // self-test: CTA drop_cta (-1: none) leaves out an arrival for its block drop_block
+  // of K (drop_part 0) or V (1), so that what waits for it gives up
+  int drop_cta, drop_part;
+  uint32_t drop_block;
   int grid;              // CTAs, one an SM
   float* records;        // [grid][2] records of kv4_record_bytes
   int* counters;         // [grid], zero between launches

@@ -709,6 +709,47 @@ def test_attention_too_many_pages_for_a_call_is_reported():
     assert (o == 5.0).all()
 
 
+@pytest.mark.parametrize("cta", [0, 77])
+@pytest.mark.parametrize("part,block", [(0, 0), (1, 0), (0, 1), (1, 1), (0, 4), (1, 5)])
+def test_attention_a_lost_arrival_is_reported_and_the_handle_recovers(part, block, cta):
+    """A wait of the kernel of longer chunks runs out at several stages: with nothing issued, with scores or
+    weighted sums under way, with pieces of cut requests counted.  Then the handle is as new."""
+    r = np.random.default_rng(22)
+    shape = shape_of(8, 2, 128)
+    lens, q_lens = [6000, 40, 500], [900, 1, 200]
+    pool, bt, q = attention_case(r, 8, 2, 128, lens, q_lens, width=WIDE)
+    h = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
+    cache = _lib.KvCache(shape, pool.shape[0], _lib.NF_KV_FP4, torch.from_numpy(pool).to(DEV))
+    args = (h, q.to(DEV), cache, dev32(bt), dev32(lens))
+    begin = dev32(np.concatenate([[0], np.cumsum(q_lens)]))
+    good, got = (torch.empty(q.shape, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    _lib.attention_kv4(*args, good, begin)
+    h.poll()
+    h.set_timeout(20_000_000)
+    h.selftest_drop(cta, part, block)
+    for _ in range(2):
+        _lib.attention_kv4(*args, got, begin)
+        with pytest.raises(_lib.NanoflowError) as e:
+            h.poll()
+        assert e.value.code == _lib.NF_ERR_TIMEOUT
+        h.poll()  # reported once
+    h.selftest_drop(cta, part, 100_000)  # a block that no CTA has: nothing is left out
+    for _ in range(3):
+        got.zero_()
+        _lib.attention_kv4(*args, got, begin)
+        h.poll()
+        assert torch.equal(got, good)
+    h.selftest_drop(-1)
+    _lib.attention_kv4(*args, got, begin)
+    h.poll()
+    assert torch.equal(got, good)
+    for bad in ((lambda: h.set_timeout(0)), (lambda: h.set_timeout(10 ** 10 + 1)), (lambda: h.selftest_drop(10 ** 6)),
+                (lambda: h.selftest_drop(0, 2)), (lambda: h.selftest_drop(0, 0, -1))):
+        with pytest.raises(_lib.NanoflowError) as e:
+            bad()
+        assert e.value.code == _lib.NF_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------------ sizes past 32 bits
 
 def test_a_pool_past_32_bits():

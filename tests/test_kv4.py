@@ -244,3 +244,8 @@ def test_binding_checks_a_calls_tensors():
                 dict(seq_lens=z(2).long()), dict(o=z(n - 1, row, t=b)), dict(o=z(n, row)), dict(o=z(row, n, t=b).T), dict(tok_begin=z(2)), dict(cache=other)):
         with pytest.raises(ValueError):
             _lib.attention_kv4(handle, **(good | bad))
+
+
+def test_handle_settings_refusals(L):
+    assert "NULL" in _refused(L.nf_kv4_set_timeout(None, 1000))
+    assert "NULL" in _refused(L.nf_kv4_selftest_drop(None, -1, 0, 0))
