@@ -14,12 +14,12 @@
 struct nf_kv4_s {
   nf_model_shape shape{};
   int num_pages = 0, max_pages = 0, device = 0, num_sms = 0;
-  // one allocation: status word (256 bytes), arrival counters, split records of
-  // the two kernels
+  // one allocation: status word and the copy that a poll takes of it (256 bytes),
+  // arrival counters, split records of the two kernels
   uint32_t* status = nullptr;
   int *counters = nullptr, *tile_counters = nullptr;
   float *records = nullptr, *tiles = nullptr;
-  size_t zeroed = 0;  // bytes from status on that a launch expects to be zero
+  size_t counted = 0;  // bytes of the arrival counters, which a launch expects to be zero
   int64_t timeout_ns = 2000000000;
   int drop_cta = -1, drop_block = 0, drop_part = 0;
 };
@@ -56,6 +56,23 @@ int sm_count() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   return n;
 }
+
+// Zeros in device memory once this returns.  A memset on the default stream would
+// neither be complete nor come before a call on a non-blocking stream, and would
+// wait for whatever the default stream has to do.
+cudaError_t zero_now(void* p, size_t bytes) {
+  cudaStream_t s = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(p, 0, bytes, s);
+  const cudaError_t w = cudaStreamSynchronize(s);
+  cudaStreamDestroy(s);
+  return e != cudaSuccess ? e : w;
+}
+
+// status[1] = status[0], which becomes zero, in one step: a bit that a running call
+// raises meanwhile is taken or stays.
+__global__ void take_status_kernel(uint32_t* status) { status[1] = atomicExch(status, 0u); }
 
 // The fields of a shape that the cache's operators use.
 nf_status check_heads(const nf_model_shape* s) {
@@ -254,9 +271,9 @@ nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t 
   const size_t cnt = ((size_t)sms * 8 + 255) / 256 * 256;
   const size_t rec = ((size_t)sms * 2 * nf::kv4_record_bytes(shape->head_dim) + 255) / 256 * 256;
   const size_t tiles = (size_t)sms * 2 * nf::kv4_tile_record_bytes(shape->head_dim);
-  h->zeroed = 256 + 2 * cnt;
-  if (cudaMalloc(&h->status, h->zeroed + rec + tiles) != cudaSuccess ||
-      cudaMemset(h->status, 0, h->zeroed) != cudaSuccess) {
+  h->counted = 2 * cnt;
+  if (cudaMalloc(&h->status, 256 + h->counted + rec + tiles) != cudaSuccess ||
+      zero_now(h->status, 256 + h->counted) != cudaSuccess) {
     cudaGetLastError();
     nf_kv4_destroy(h);
     return fail4(NF_ERR_OOM, "cudaMalloc of the workspace failed");
@@ -285,12 +302,13 @@ nf_status nf_kv4_poll(nf_kv4 h, int wait) {
   if (wait) NF_CUDA4(cudaDeviceSynchronize());
   NF_CUDA4(cudaGetLastError());
   uint32_t st = 0;
-  NF_CUDA4(cudaMemcpy(&st, h->status, 4, cudaMemcpyDeviceToHost));
-  if (st) NF_CUDA4(cudaMemset(h->status, 0, 4));
+  take_status_kernel<<<1, 1>>>(h->status);
+  NF_CUDA4(cudaGetLastError());
+  NF_CUDA4(cudaMemcpy(&st, h->status + 1, 4, cudaMemcpyDeviceToHost));
   if (st & nf::ST_TIMEOUT) {
     // pieces that were given up never arrived: the counters start over
     NF_CUDA4(cudaDeviceSynchronize());
-    NF_CUDA4(cudaMemset(h->status, 0, h->zeroed));
+    NF_CUDA4(zero_now(h->counters, h->counted));
     return fail4(NF_ERR_TIMEOUT, "a device wait timed out (status 0x%x)", st);
   }
   if (st)

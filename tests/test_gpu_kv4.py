@@ -750,6 +750,35 @@ def test_attention_a_lost_arrival_is_reported_and_the_handle_recovers(part, bloc
         assert e.value.code == _lib.NF_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("width", [None, WIDE])
+def test_a_new_handle_on_a_stream_beside_a_busy_default_stream(width):
+    """The handle's counters are zero when the handle is there, whatever the default stream still has to do."""
+    r = np.random.default_rng(23)
+    shape = shape_of(8, 2, 128)
+    lens, q_lens = [5000, 3, 260], [130, 1, 1]
+    pool, bt, q = attention_case(r, 8, 2, 128, lens, q_lens, width=width)
+    cache = _lib.KvCache(shape, pool.shape[0], _lib.NF_KV_FP4, torch.from_numpy(pool).to(DEV))
+    qd, btd, ld = q.to(DEV), dev32(bt), dev32(lens)
+    begin = dev32(np.concatenate([[0], np.cumsum(q_lens)]))
+    first = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
+    good, got = torch.empty_like(qd), torch.full_like(qd, 5.0)
+    _lib.attention_kv4(first, qd, cache, btd, ld, good, begin)
+    first.poll()
+    a, side = torch.randn(8192, 8192, device=DEV), torch.cuda.Stream()
+    used = torch.ones(64 << 20, dtype=torch.uint8, device=DEV)  # memory that is not zero, for the handle to get
+    torch.cuda.synchronize()
+    del used
+    torch.cuda.empty_cache()
+    for _ in range(30):
+        a = a @ a
+        a = a / a.abs().max()
+    h = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
+    _lib.attention_kv4(h, qd, cache, btd, ld, got, begin, stream=side)
+    side.synchronize()
+    assert torch.equal(got, good)
+    h.poll()
+
+
 # ------------------------------------------------------------------ sizes past 32 bits
 
 def test_a_pool_past_32_bits():
