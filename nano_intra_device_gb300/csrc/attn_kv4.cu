@@ -22,8 +22,10 @@
 //    2^14): bf16's 8 bits fit fp16's 11 down to 2^-28 of the largest element.
 //  * P enters as fp16 of 2^7 times its share of the running maximum (2^-11
 //    relative, exact zero only below 2^-32); the denominators sum the fp32
-//    values.  The maximum is raised only when a score passes it by 2^8, so p
-//    stays below 2^15.
+//    values.  The maximum m is raised only when p, as it is computed, would pass
+//    2^15 (a score 2^8 times the maximum's share): beyond 2^24 a score's steps reach
+//    what KA_SHIFT - m rounds off, so a bound on the score itself would not keep p
+//    within fp16.
 //
 // The pages come by 16-byte asynchronous copies into a ring of two stages a warp,
 // which runs on over the ends of units; nothing but the warp itself waits for
@@ -73,6 +75,9 @@ constexpr uint32_t KA_FIXED = 5;
 constexpr uint32_t KA_MIN_QUOTA = 8;  // fewest slots of a warp (1, 4, 8: the same)
 constexpr float KA_LAZY = 8.f;
 constexpr float KA_SHIFT = 7.f;
+// What stands for -m where nothing was seen: any score passes the maximum, and a
+// hidden one stays -infinity.
+constexpr float KA_UNSEEN = 3.402823466e38f;
 
 template <int D>
 struct KaLayout {
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
 #pragma unroll
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY;          // reference maxima of the columns h0, h1 (base 2)
-    float2 n2 = make_float2(KA_SHIFT, KA_SHIFT);   // what p's exponent adds: KA_SHIFT - m (m finite)
+    float2 n2 = make_float2(KA_UNSEEN, KA_UNSEEN); // what p's exponent adds: KA_SHIFT - m
     float2 l2 = make_float2(0.f, 0.f);             // this lane's share of the denominators
     const int plim = u.p1 * KV4_P;  // positions past the piece are another warp's
     const int lim0 = min(u.len + i0, plim), lim1 = min(u.len + i1, plim);  // the first hidden positions
@@ -525,7 +530,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
         x0 = fmaxf(x0, fmaxf(sc[p][0], sc[p][2]));
         x1 = fmaxf(x1, fmaxf(sc[p][1], sc[p][3]));
       }
-      if (__any_sync(0xffffffffu, x0 > m0 + KA_LAZY || x1 > m1 + KA_LAZY)) {
+      if (__any_sync(0xffffffffu, x0 + n2.x > KA_LAZY + KA_SHIFT || x1 + n2.y > KA_LAZY + KA_SHIFT)) {
         float y0 = x0, y1 = x1;
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
@@ -547,14 +552,14 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
         l2.y *= c1;
         m0 = r0;
         m1 = r1;
-        n2.x = m0 == -INFINITY ? KA_SHIFT : KA_SHIFT - m0;
-        n2.y = m1 == -INFINITY ? KA_SHIFT : KA_SHIFT - m1;
+        n2.x = m0 == -INFINITY ? KA_UNSEEN : KA_SHIFT - m0;
+        n2.y = m1 == -INFINITY ? KA_UNSEEN : KA_SHIFT - m1;
       }
       uint32_t pt[PG][2];
 #pragma unroll
       for (int p = 0; p < PG; ++p) {
         // the scaled scores are rounded before the maximum is taken off (no fused
-        // step), so that the largest is at most 2^8 of it at any magnitude
+        // step), as where the largest was compared
         float2 lo = __fadd2_rn(make_float2(sc[p][0], sc[p][1]), n2), hi = __fadd2_rn(make_float2(sc[p][2], sc[p][3]), n2);
         lo.x = ex2_approx(lo.x);
         lo.y = ex2_approx(lo.y);

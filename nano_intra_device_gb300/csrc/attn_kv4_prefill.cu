@@ -70,6 +70,7 @@ constexpr int KP_REGION = 128 * 128; // 128 rows x 128 bytes: 64 fp16 columns of
 constexpr int KP_FIXED = 1;          // blocks' worth of a unit's fixed cost (2, 4: 235, 232 us)
 constexpr float KP_SLACK = 8.f;
 constexpr float KP_SHIFT = 7.f;
+constexpr float KP_UNSEEN = 3.402823466e38f;  // stands for -m where nothing was seen
 constexpr uint32_t KP_TMEM_COLS = 512;
 constexpr int KP_KST = 2, KP_VST = 2;  // ring stages of K and V
 constexpr uint64_t KP_DRAIN_NS = 2000000000ull;
@@ -638,6 +639,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         arrive(&bars->q_full[t]);
       }
       float m_ref = -INFINITY, l = 0.f;
+      float nm = KP_UNSEEN;  // what the exponents add: KP_SHIFT - m_ref
       for (int j = p.j0; j < p.j1; ++j, ++n, ++blk) {
         if (!wait(&bars->s_full[t], n & 1)) {
           ok = false;
@@ -669,9 +671,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           mx = kp_max3(kp_max3(mx8[0], mx8[1], mx8[2]), kp_max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * scale;
         }
         float corr = 1.f;
-        if (mx > m_ref + KP_SLACK) {  // also from -inf, where O and l are still zero
+        if (mx + nm > KP_SLACK + KP_SHIFT) {  // also from -inf, where O and l are still zero
           corr = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mx);
           m_ref = mx;
+          nm = KP_SHIFT - mx;
           l *= corr;
         }
         // a raised maximum rescales the row of O; the product of the block before is
@@ -688,10 +691,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
           }
         }
         // p = 2^(s scale - m + shift); m = -inf: nothing seen yet, all p are 0
-        const float nm = m_ref == -INFINITY ? KP_SHIFT : KP_SHIFT - m_ref;
-        if (__any_sync(0xffffffffu, fabsf(m_ref) > 3e7f && m_ref != -INFINITY)) {
-          // beyond fp32's whole numbers the fused step could pass the maximum's own
-          // rounding by more than the slack
+        if (__any_sync(0xffffffffu, fabsf(m_ref) > 8e6f && m_ref != -INFINITY)) {
+          // Scores from 2^23 on have steps of 1 and more: the fused step could pass what
+          // was compared, and with it fp16's range, by a power of two or more.  Below,
+          // half a step is at most 2^-1: p stays under 2^15.5.
 #pragma unroll
           for (int i = 0; i < KP_N; ++i) x[i] = ex2_approx(__fadd_rn(__fmul_rn(x[i], scale), nm));
         } else {

@@ -503,6 +503,50 @@ def test_attention_magnitudes(exps, q_scale, width):
     check_attention(shape_of(4, 2, 64), pool, bt, q, lens, q_lens, exps)
 
 
+def ladder_pool(d, n, steps, value=1.5):
+    """A cache of one request and KV head: K holds 2688 in channel 0 and steps[p // 64] in channel 16, V is constant."""
+    pages = -(-n // 16)
+    pool = np.zeros((pages, 1, 2, 9 * d), np.uint8)
+    for p in range(n):
+        k = np.zeros((1, d))
+        k[0, 0], k[0, 16] = 2688.0, steps[p // 64]
+        orc.put(pool, p, 0, *orc.quantise(k, 0))
+        orc.put(pool, p, 1, *orc.quantise(np.full((1, d), value), 0))
+    return pool
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("chunk", [False, True])
+def test_attention_scores_in_coarse_steps(chunk, d):
+    """Scores of 2^20 to 2^30, where fp32's steps reach those by which a maximum may be passed before it is
+    raised: whatever the weights come to, they are finite and add up to one.  V is constant, so the output is
+    that constant, up to a weight's half step in fp16 (2^-11) and the output's in bf16 (2^-8)."""
+    n, steps = 300, [0.0, 1.0, 1.5, 2.0, 3.0]
+    pool = ladder_pool(d, n, steps)
+    rows = []
+    for e in range(20, 31):
+        for f in (1.0, 1.19, 1.41, 1.68):
+            for b in (22.0, 36.0, 40.0, 42.0, 44.0, 45.0, 46.0, 48.0, 56.0, 64.0, 72.0, 80.0, 88.0, 90.0, 112.0, 128.0):
+                rows.append((2.0 ** e * f * np.sqrt(d) / 1.4427 / 2688, b * np.sqrt(d / 64)))
+    n_q = 8 if chunk else 1
+    q = np.zeros((len(rows), d))
+    q[:, 0], q[:, 16] = np.array(rows).T
+    q = torch.from_numpy(q.reshape(-1, n_q, d)).to(torch.bfloat16)
+    shape = shape_of(n_q, 1, d)
+    pages = pool.shape[0]
+    if chunk:  # 200 chunks of 44 rows: every CTA has several blocks of a chunk to itself
+        n_seq, q_lens = 200, [44] * 200
+        q = q.repeat(100, 1, 1)
+        bt = np.full((n_seq, WIDE), -1)
+        bt[:, :pages] = np.arange(pages)
+    else:
+        n_seq, q_lens = len(rows), [1] * len(rows)
+        bt = np.tile(np.arange(pages), (n_seq, 1))
+    got = run_attention(shape, pool, bt, q, [n] * n_seq, q_lens)
+    assert np.isfinite(got).all()
+    assert np.abs(got - 1.5).max() <= 1.5 * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16)
+
+
 def test_attention_sink_and_faint_tail():
     """One position far above two thousand faint ones, whose sum still counts."""
     r = np.random.default_rng(13)
