@@ -555,7 +555,8 @@ nf_status nf_kv4_selftest_drop(nf_kv4 h, int32_t cta, int32_t part, int32_t bloc
  * a batch padded to n_tok rows is fine.
  * What a row does not see cannot reach it, whatever it holds.  A NaN that it
  * sees makes NaN of every channel (NaN in K) or of its block's channels at
- * least (NaN in V).
+ * least (NaN in V), and so does a NaN or an infinity in its query (every
+ * channel of that head).
  * A page id outside the pool reads page 0, a length outside
  * [0, 16 * max_pages_per_seq] counts as 0, rows outside [0, n_tok) are left
  * out, and rows that together would read 2^32 pages of a KV head or more are

@@ -448,7 +448,9 @@ __global__ void __launch_bounds__(KA_THREADS, 1) attn_kv4_kernel(const Kv4AttnAr
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
       const int kq = top > 0.f ? max(-126, min(120, 14 - e)) : 0;
-      const float mul = exp2_int(kq);
+      // an infinity makes every score of the vector infinite or NaN, and their softmax
+      // NaN, also where all are -inf, which would pass for hidden ones
+      const float mul = top == INFINITY ? __int_as_float(0x7FC00000) : exp2_int(kq);
 #pragma unroll
       for (int j = 0; j < KS; ++j)
 #pragma unroll

@@ -626,7 +626,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         }
         const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
         const int kq = top > 0.f ? max(-126, min(120, 14 - e)) : 0;
-        const float mul = exp2_int(kq);
+        // a vector with an infinity: NaN scores (attn_kv4.cu)
+        const float mul = top == INFINITY ? __int_as_float(0x7FC00000) : exp2_int(kq);
         scale = fmaxf(a.scale_log2 * exp2_int(-kq), 1.17549435e-38f);  // 0 times a hidden score's -inf is NaN
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {

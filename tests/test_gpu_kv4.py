@@ -547,6 +547,27 @@ def test_attention_scores_in_coarse_steps(chunk, d):
     assert np.abs(got - 1.5).max() <= 1.5 * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16)
 
 
+@pytest.mark.parametrize("width,q_len", [(None, 1), (None, 20), (WIDE, 20)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+def test_attention_an_infinite_query_is_nan(bad, width, q_len):
+    """Scores of one infinity, of either sign, have no softmax: NaN, also where all of them are minus infinity.
+    A row that sees no position is zero all the same."""
+    d = 64
+    pool = ladder_pool(d, 40, [1.0])
+    bt = np.full((2, width or 3), -1)
+    bt[:, :3] = np.arange(3)
+    lens, q_lens = [40, 5], [q_len, q_len]
+    r = np.random.default_rng(24)
+    q = torch.from_numpy(r.standard_normal((2 * q_len, 8, d))).to(torch.bfloat16)
+    q[:, 3, 0] = bad     # against 2688 everywhere
+    q[:, 5, 40] = bad    # against 0 everywhere
+    got = run_attention(shape_of(8, 1, d), pool, bt, q, lens, q_lens)
+    blind = np.concatenate([np.zeros(q_len, bool), np.arange(q_len) < q_len - 5])
+    assert not got[blind].any()
+    for h in range(8):
+        assert np.isnan(got[~blind, h]).all() if h in (3, 5) else np.isfinite(got[:, h]).all()
+
+
 def test_attention_sink_and_faint_tail():
     """One position far above two thousand faint ones, whose sum still counts."""
     r = np.random.default_rng(13)
