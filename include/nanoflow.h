@@ -524,7 +524,7 @@ nf_status nf_kv4_read(const nf_model_shape* shape, const nf_kv_cache* cache, con
  * the status word, made on the current device; like a plan it serves one stream
  * at a time, and two captured graphs that use it must not run at once.  The
  * workspace is about 43 MB at head_dim 128, half of that at 64.
- * Shapes as nf_model_shape allows; 1 <= max_pages_per_seq. */
+ * Shapes as nf_model_shape allows; 1 <= max_pages_per_seq <= 2^26. */
 typedef struct nf_kv4_s* nf_kv4;
 nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t max_pages_per_seq,
                         nf_kv4* out);

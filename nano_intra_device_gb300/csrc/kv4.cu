@@ -91,6 +91,9 @@ nf_status check_heads(const nf_model_shape* s) {
 
 // Slots and pool rows are 32-bit: num_pages * 16 below 2^31.
 constexpr int kMaxPages = (1 << 27) - 1;
+// Pages of a request in attention: the kernels count positions in 32 bits, past a
+// request's last one by up to two key blocks, so the last 2^30 are left out.
+constexpr int kMaxSeqPages = 1 << 26;
 
 nf_status check_cache(const nf_kv_cache* c, bool fp4_only) {
   if (!c) return fail4(NF_ERR_INVALID_ARG, "cache is NULL");
@@ -252,8 +255,10 @@ nf_status nf_kv4_create(const nf_model_shape* shape, int32_t num_pages, int32_t 
   if (!out) return fail4(NF_ERR_INVALID_ARG, "out is NULL");
   *out = nullptr;
   NF_TRY4(check_heads(shape));
-  if (num_pages < 1 || num_pages > kMaxPages || max_pages_per_seq < 1 || max_pages_per_seq > kMaxPages)
-    return fail4(NF_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must lie in [1, %d]", kMaxPages);
+  if (num_pages < 1 || num_pages > kMaxPages)
+    return fail4(NF_ERR_INVALID_ARG, "num_pages must lie in [1, %d] (got %d)", kMaxPages, num_pages);
+  if (max_pages_per_seq < 1 || max_pages_per_seq > kMaxSeqPages)
+    return fail4(NF_ERR_INVALID_ARG, "max_pages_per_seq must lie in [1, %d] (got %d)", kMaxSeqPages, max_pages_per_seq);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();

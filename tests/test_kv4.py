@@ -249,3 +249,10 @@ def test_binding_checks_a_calls_tensors():
 def test_handle_settings_refusals(L):
     assert "NULL" in _refused(L.nf_kv4_set_timeout(None, 1000))
     assert "NULL" in _refused(L.nf_kv4_selftest_drop(None, -1, 0, 0))
+
+
+def test_handle_refuses_requests_whose_positions_pass_32_bits(L):
+    h = ctypes.c_void_p()
+    for width in ((1 << 26) + 1, (1 << 27) - 1):
+        assert "max_pages_per_seq" in _refused(L.nf_kv4_create(ctypes.byref(_shape()), 8, width, ctypes.byref(h)))
+        assert not h
