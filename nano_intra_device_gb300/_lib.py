@@ -456,11 +456,28 @@ def _dense(name, t, dtype, *shape):
                          f"got {t.dtype} {list(t.shape)}")
 
 
-def _arg(name, t, dtype, n):
-    """The address of a call's tensor, which has to hold n contiguous elements of dtype."""
+def _arg(name, t, dtype, n, dev):
+    """The address of a call's tensor, which has to hold n contiguous elements of dtype on device dev."""
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: need {n} contiguous elements of {dtype}, got {t.dtype} {list(t.shape)}")
+    return _on(name, t, dev)
+
+
+def _on(name, t, dev):
+    """The address of a tensor that has to be on device dev (as get_device() numbers it: -1 the CPU)."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the call's other tensors are on {'cpu' if dev < 0 else f'cuda:{dev}'}")
     return t.data_ptr()
+
+
+def _call_stream(dev, stream):
+    """The stream handle of a call whose tensors are on device dev: a GPU, and the current one."""
+    import torch
+    if dev < 0:
+        raise ValueError("the call's tensors have to be on a CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the call's tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return stream_handle(stream)
 
 
 class KvCache:
@@ -474,9 +491,14 @@ class KvCache:
         s = make_shape(shape)
         if fmt == NF_KV_FP4:
             _dense("packed pool", k, torch.uint8, num_pages, s.n_kv_heads, 2, 9 * s.head_dim)
+        elif v is None:
+            raise ValueError("a 16-bit cache has a K pool and a V pool")
         else:
             for n, t in (("K pool", k), ("V pool", v)):
                 _dense(n, t, torch.bfloat16, num_pages, s.n_kv_heads, s.page_size, s.head_dim)
+        self.dev = k.get_device()
+        if v is not None:
+            _on("V pool", v, self.dev)
         self.k, self.v = k, v
         self.heads = (s.n_kv_heads, s.head_dim)
         self.types = (torch.bfloat16, torch.int32)
@@ -513,6 +535,8 @@ class BlockTables:
                                 ("tok_begin", tok_begin, n + 1), ("tok_seq", tok_seq, cap), ("tok_pos", tok_pos, cap),
                                 ("tok_slot", tok_slot, cap)):
             _dense(name, t, i, *shape)
+            _on(name, t, held.get_device())
+        self.dev = held.get_device()
         self._keep = (held, seq_lens, block_table, ring, state_in, state_out, tok_begin, tok_seq, tok_pos, tok_slot)
         self.a = (ptr(held), ptr(seq_lens), n, ptr(block_table), block_table.shape[1], ptr(ring), ring.numel(),
                   ptr(state_in), ptr(state_out), ptr(tok_begin), ptr(tok_seq), ptr(tok_pos), ptr(tok_slot), cap)
@@ -520,7 +544,7 @@ class BlockTables:
 
 def block_tables(args: BlockTables, stream=None):
     """nf_block_tables: block tables and slot maps of a step from request lengths."""
-    check(lib().nf_block_tables(*args.a, stream_handle(stream)))
+    check(lib().nf_block_tables(*args.a, _call_stream(args.dev, stream)))
 
 
 def qk_norm_rope(shape, qkv, q_gain, k_gain, tok_pos, tok_slot, q, cache: KvCache, stream=None):
@@ -529,28 +553,28 @@ def qk_norm_rope(shape, qkv, q_gain, k_gain, tok_pos, tok_slot, q, cache: KvCach
     (bf16, i32), n = cache.types, qkv.shape[0]
     if qkv.dtype is not bf16 or qkv.dim() != 2 or qkv.stride(1) != 1:
         raise ValueError("qkv: need bf16 [n_tok, width] with contiguous rows")
-    s = make_shape(shape)
+    s, dev = make_shape(shape), cache.dev
     d = s.head_dim
     if cache.heads != (s.n_kv_heads, d):
         raise ValueError("the cache was made for another shape")
     if qkv.shape[1] < (s.n_q_heads + 2 * s.n_kv_heads) * d:
         raise ValueError("qkv: rows too short for the shape")
-    check(lib().nf_qk_norm_rope(ctypes.byref(s), qkv.data_ptr(), qkv.stride(0),
-                                None if q_gain is None else _arg("q_gain", q_gain, bf16, d),
-                                None if k_gain is None else _arg("k_gain", k_gain, bf16, d),
-                                _arg("tok_pos", tok_pos, i32, n), _arg("tok_slot", tok_slot, i32, n), n,
-                                _arg("q", q, bf16, n * s.n_q_heads * d), ctypes.byref(cache.c),
-                                stream_handle(stream)))
+    check(lib().nf_qk_norm_rope(ctypes.byref(s), _on("qkv", qkv, dev), qkv.stride(0),
+                                None if q_gain is None else _arg("q_gain", q_gain, bf16, d, dev),
+                                None if k_gain is None else _arg("k_gain", k_gain, bf16, d, dev),
+                                _arg("tok_pos", tok_pos, i32, n, dev), _arg("tok_slot", tok_slot, i32, n, dev), n,
+                                _arg("q", q, bf16, n * s.n_q_heads * d, dev), ctypes.byref(cache.c),
+                                _call_stream(dev, stream)))
 
 
 def kv4_read(shape, cache: KvCache, slots, k, v, stream=None):
     """nf_kv4_read: rows of the 4-bit cache by slot, as bf16 k, v [n, n_kv, d]."""
-    s, (bf16, i32), n = make_shape(shape), cache.types, slots.numel()
+    s, (bf16, i32), n, dev = make_shape(shape), cache.types, slots.numel(), cache.dev
     if cache.heads != (s.n_kv_heads, s.head_dim):
         raise ValueError("the cache was made for another shape")
     size = n * s.n_kv_heads * s.head_dim
-    check(lib().nf_kv4_read(ctypes.byref(s), ctypes.byref(cache.c), _arg("slots", slots, i32, n), n,
-                            _arg("k", k, bf16, size), _arg("v", v, bf16, size), stream_handle(stream)))
+    check(lib().nf_kv4_read(ctypes.byref(s), ctypes.byref(cache.c), _arg("slots", slots, i32, n, dev), n,
+                            _arg("k", k, bf16, size, dev), _arg("v", v, bf16, size, dev), _call_stream(dev, stream)))
 
 
 class Kv4:
@@ -590,18 +614,18 @@ class Kv4:
 def attention_kv4(handle: Kv4, q, cache: KvCache, block_table, seq_lens, o, tok_begin=None, stream=None):
     """nf_attention_kv4: attention of a step's tokens over the 4-bit cache (tok_begin None: one row
     per request)."""
-    (bf16, i32), n, rows = cache.types, seq_lens.numel(), q.shape[0]
+    (bf16, i32), n, rows, dev = cache.types, seq_lens.numel(), q.shape[0], cache.dev
     if block_table.shape[1] != handle.max_pages:
         raise ValueError(f"block_table: need rows of {handle.max_pages} entries, got {block_table.shape[1]}")
     if cache.heads != handle.heads:
         raise ValueError("the cache was made for another shape than the handle")
     if o.dtype is not bf16 or o.numel() < rows * handle.row or not o.is_contiguous():
         raise ValueError("o: need contiguous bf16 rows, as many as q's at least")
-    check(lib().nf_attention_kv4(handle.h, _arg("q", q, bf16, rows * handle.row), ctypes.byref(cache.c),
-                                 _arg("block_table", block_table, i32, n * handle.max_pages),
-                                 _arg("seq_lens", seq_lens, i32, n),
-                                 None if tok_begin is None else _arg("tok_begin", tok_begin, i32, n + 1), n, rows,
-                                 o.data_ptr(), stream_handle(stream)))
+    check(lib().nf_attention_kv4(handle.h, _arg("q", q, bf16, rows * handle.row, dev), ctypes.byref(cache.c),
+                                 _arg("block_table", block_table, i32, n * handle.max_pages, dev),
+                                 _arg("seq_lens", seq_lens, i32, n, dev),
+                                 None if tok_begin is None else _arg("tok_begin", tok_begin, i32, n + 1, dev), n, rows,
+                                 _on("o", o, dev), _call_stream(dev, stream)))
 
 
 def plan_search(shape, batch, profile_json=None, num_sms=152, n_layers=1):

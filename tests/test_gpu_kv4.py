@@ -844,6 +844,25 @@ def test_a_new_handle_on_a_stream_beside_a_busy_default_stream(width):
     h.poll()
 
 
+def test_binding_refuses_tensors_of_another_device():
+    """One tensor of a call on the CPU: refused on the host, before its address goes anywhere."""
+    shape, b = shape_of(4, 2, 64), torch.bfloat16
+    z = lambda *n, t=torch.int32: torch.zeros(n, dtype=t, device=DEV)  # noqa: E731
+    cache = _lib.KvCache(shape, 8, _lib.NF_KV_FP4, z(8, 2, 2, 576, t=torch.uint8))
+    with pytest.raises(ValueError, match="V pool"):
+        _lib.KvCache(shape, 8, _lib.NF_KV_BF16, z(8, 2, 16, 64, t=b), z(8, 2, 16, 64, t=b).cpu())
+    h = _lib.Kv4(shape, 8, 5)
+    for call, good in ((lambda *a: _lib.block_tables(_lib.BlockTables(*a)), [z(3), z(3), z(3, 4), z(8), z(2), z(4), z(4), z(9), z(9), z(9)]),
+                       (lambda *a: _lib.qk_norm_rope(shape, *a, cache), [z(3, 512, t=b), z(64, t=b), z(64, t=b), z(3), z(3) - 1, z(3, 256, t=b)]),
+                       (lambda *a: _lib.kv4_read(shape, cache, *a), [z(3), z(3, 128, t=b), z(3, 128, t=b)]),
+                       (lambda q, *a: _lib.attention_kv4(h, q, cache, *a), [z(3, 256, t=b), z(2, 5), z(2), z(3, 256, t=b), z(3)])):
+        call(*good)
+        for at in range(len(good)):
+            with pytest.raises(ValueError, match="cpu|cuda"):
+                call(*[t.cpu() if i == at else t for i, t in enumerate(good)])
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ sizes past 32 bits
 
 def test_a_pool_past_32_bits():

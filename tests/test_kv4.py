@@ -256,3 +256,21 @@ def test_handle_refuses_requests_whose_positions_pass_32_bits(L):
     for width in ((1 << 26) + 1, (1 << 27) - 1):
         assert "max_pages_per_seq" in _refused(L.nf_kv4_create(ctypes.byref(_shape()), 8, width, ctypes.byref(h)))
         assert not h
+
+
+def test_binding_refuses_tensors_of_the_cpu():
+    """Right types and sizes, but addresses that no kernel may get."""
+    i, b = torch.int32, torch.bfloat16
+    z = lambda *n, t=i: torch.zeros(n, dtype=t)  # noqa: E731
+    cache = _lib.KvCache(SHAPE, 8, _lib.NF_KV_FP4, torch.zeros(8, 2, 2, 576, dtype=torch.uint8))
+    n, row = 3, SHAPE.n_q * 64
+    calls = (lambda: _lib.block_tables(_lib.BlockTables(z(3), z(3), z(3, 4), z(8), z(2), z(4), z(4), z(9), z(9), z(9))),
+             lambda: _lib.qk_norm_rope(SHAPE, z(n, 512, t=b), z(64, t=b), None, z(n), z(n), z(n, row, t=b), cache),
+             lambda: _lib.kv4_read(SHAPE, cache, z(n), z(n, 128, t=b), z(n, 128, t=b)),
+             lambda: _lib.attention_kv4(types.SimpleNamespace(h=None, max_pages=5, heads=(2, 64), row=row), z(n, row, t=b), cache, z(2, 5), z(2),
+                                        z(n, row, t=b), z(3)))
+    for call in calls:
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    with pytest.raises(ValueError, match="V pool"):
+        _lib.KvCache(SHAPE, 8, _lib.NF_KV_BF16, z(8, 2, 16, 64, t=b))
