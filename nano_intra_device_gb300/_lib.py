@@ -194,13 +194,18 @@ def ptr(t):
     return None if t is None else c_void_p(t.data_ptr())
 
 
-def stream_handle(stream=None):
+def stream_handle(stream=None, dev=None):
+    """The cudaStream_t of a torch stream, or of the current stream of the current device (dev, where the
+    caller knows it)."""
     import torch
     if stream is not None:
         return c_void_p(stream.cuda_stream)
-    # the current stream's handle alone: a torch.cuda.Stream object around it takes
-    # 3 us, as long as a launch
-    return c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    if dev is None:
+        dev = torch.cuda.current_device()
+    # the current stream's handle alone, where this torch has a query for it: a
+    # torch.cuda.Stream object around it takes 3 us, as long as a launch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return c_void_p(raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream)
 
 
 def make_shape(shape) -> nf_model_shape:
@@ -460,7 +465,7 @@ def _arg(name, t, dtype, n, dev):
     """The address of a call's tensor, which has to hold n contiguous elements of dtype on device dev."""
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: need {n} contiguous elements of {dtype}, got {t.dtype} {list(t.shape)}")
-    return _on(name, t, dev)
+    return t.data_ptr() if t.get_device() == dev else _on(name, t, dev)
 
 
 def _on(name, t, dev):
@@ -475,9 +480,10 @@ def _call_stream(dev, stream):
     import torch
     if dev < 0:
         raise ValueError("the call's tensors have to be on a CUDA device")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the call's tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return stream_handle(stream)
+    current = torch.cuda.current_device()
+    if dev != current:
+        raise ValueError(f"the call's tensors are on cuda:{dev}, the current device is cuda:{current}")
+    return stream_handle(stream, dev)
 
 
 class KvCache:

@@ -2,9 +2,11 @@
 its host-only plan search returns valid plans."""
 import ctypes
 import os
+import types
 
 import numpy as np
 import pytest
+import torch
 
 from nano_intra_device_gb300 import _lib, workload as wl
 
@@ -327,3 +329,18 @@ def test_search_picks_the_fastest_profiled_plan_of_the_same_batch(L, tmp_path):
     assert o.executor == _lib.NF_EXEC_SEQUENTIAL and o.n_attn == 1 and t == pytest.approx(26.3e3)
     o8, _ = _lib.plan_search(s8, b8, str(p), 152, n_layers=8)  # another layer count: the model
     assert _lib.plan_predict(s8, b8, o8, str(p), 152, 8) > 0
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_stream_handle_of_the_current_stream(monkeypatch, raw):
+    """With torch's query for the raw handle, and by the public stream object where a torch lacks it."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: types.SimpleNamespace(cuda_stream=1000 + dev))
+    if raw:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 2000 + dev, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    base = 2000 if raw else 1000
+    assert _lib.stream_handle().value == base + 3
+    assert _lib.stream_handle(None, 5).value == base + 5
+    assert _lib.stream_handle(types.SimpleNamespace(cuda_stream=7)).value == 7
