@@ -239,6 +239,19 @@ def test_append_many_tokens(n_tok):
 
 
 @pytest.mark.parametrize("fmt", [_lib.NF_KV_FP4, _lib.NF_KV_BF16])
+@pytest.mark.parametrize("n_q,n_kv,d", [(2, 1, 64), (8, 4, 128), (16, 8, 64)])
+@pytest.mark.parametrize("per_sm,more", [(6, -1), (6, 0), (6, 5), (12, -1), (12, 0), (12, 3), (24, -1), (24, 0), (24, 5)])
+def test_append_on_both_sides_of_every_number_of_tokens_a_cta_takes(per_sm, more, n_q, n_kv, d, fmt):
+    """One token a CTA below 6 an SM, then 2, from 12 on 4, from 24 on 8, there in two launches where whole
+    warps of heads are queries or keys (the last two shapes), with odd tails."""
+    n_tok = per_sm * torch.cuda.get_device_properties(0).multi_processor_count + more
+    r = np.random.default_rng(n_tok + d)
+    x, pos, slot = append_case(r, n_tok, n_q, n_kv, d, n_tok // 16 + 2, 5000)
+    slot[3::101] = -1
+    check_append(shape_of(n_q, n_kv, d), x, gains_of(r, d), pos, slot, fmt, n_tok // 16 + 2, (1, -1))
+
+
+@pytest.mark.parametrize("fmt", [_lib.NF_KV_FP4, _lib.NF_KV_BF16])
 @pytest.mark.parametrize("n_tok,n_q,n_kv,d", [(3700, 8, 8, 64), (5001, 8, 2, 128), (4000, 16, 4, 64)])
 def test_append_of_thousands(fmt, n_tok, n_q, n_kv, d):
     r = np.random.default_rng(n_tok)
@@ -501,6 +514,47 @@ def test_attention_magnitudes(exps, q_scale, width):
         assert np.abs(got[1] - want[1]).max() <= 2.0 ** -8 * np.abs(want[1]).max()
         return
     check_attention(shape_of(4, 2, 64), pool, bt, q, lens, q_lens, exps)
+
+
+@pytest.mark.parametrize("width", [None, WIDE])
+@pytest.mark.parametrize("exps", [(0, 0), (-5, 20)])
+def test_attention_extreme_queries_inside_a_chunk(exps, width):
+    """Rows of a chunk 10^18 times larger and smaller than their neighbours, in one call.
+
+    A huge row's weights are one-hot where its two largest scores lie further apart than twice a score's error
+    (d 2^-24 of its mass, as above) and 20 more: e^-20 is far below the output's half step.  A tiny row's scores
+    are all zero to 2^-50, so its output is the mean.  The others keep the ordinary bound."""
+    r = np.random.default_rng(25)
+    d, lens, q_lens = 64, [120, 300, 100], [1, 150, 50]
+    pool, bt, q = attention_case(r, 4, 2, d, lens, q_lens, width=width)
+    big, small = [0, 3, 40, 100, 149, 170, 200], [1, 17, 90, 155, 199]
+    q[big] = (q[big].float() * 1e18).to(torch.bfloat16)
+    q[small] = (q[small].float() * 1e-18).to(torch.bfloat16)
+    shape = shape_of(4, 2, d)
+    got = run_attention(shape, pool, bt, q, lens, q_lens, exps)
+    q64 = q.double().numpy()
+    want, mag = orc.attention(q64, pool, exps, bt, lens, q_lens)
+    assert np.isfinite(got).all()
+    top, vtop = (np.nan_to_num(np.abs(orc.take(pool, range(pool.shape[0] * 16), i, exps[i]))).max() for i in (0, 1))
+    mass = np.abs(q64).sum(-1, keepdims=True) * top / np.sqrt(d)
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * d * 2.0 ** -24 * mass) * mag + max(lens) * 2.0 ** -32 * vtop
+    plain = np.setdiff1d(np.arange(len(q)), big)
+    assert (np.abs(got - want) <= bound)[plain].all()
+    seq = np.repeat(np.arange(3), q_lens)
+    begin = np.concatenate([[0], np.cumsum(q_lens)])
+    apart = 0
+    for i in big:
+        s = seq[i]
+        see = lens[s] - q_lens[s] + i - begin[s] + 1
+        k = orc.take(pool, [int(bt[s, p // 16]) * 16 + p % 16 for p in range(see)], 0, exps[0])
+        for h in range(4):
+            x = np.sort(k[:, h // 2] @ q64[i, h] / np.sqrt(d))
+            if x[-1] - x[-2] > 2 * d * 2.0 ** -24 * mass[i, h, 0] + 20:
+                apart += 1
+                assert (np.abs(got[i, h] - want[i, h]) <= 2.0 ** -8 * np.abs(want[i, h]) + see * 2.0 ** -32 * vtop).all()
+            else:  # whatever the weights, a mean of the values that the row sees
+                assert (np.abs(got[i, h]) <= vtop * (1 + 2.0 ** -8)).all()
+    assert apart >= 20
 
 
 def ladder_pool(d, n, steps, value=1.5):
@@ -923,6 +977,32 @@ def test_rows_past_32_bits():
     assert ks.any() and all(torch.equal(a[-64:], b.roll(-(n % 64), 0)) for a, b in ((k, ks), (v, vs)))
 
 
+@pytest.mark.parametrize("rows,pages", [(1, 1 << 26), (9, 1 << 22)])
+def test_attention_of_the_longest_requests(rows, pages):
+    """2^30 positions, the most that a request may have, and a chunk over 2^26: every page is the same one, so
+    the output is that of its 16 positions.  The fp32 sums of a warp (of a CTA of the tiles) take
+    pages / (12 x 100) (blocks / 100) additions at least a hundred SMs share: each errs by 2^-24."""
+    d, n_q = 64, 8
+    shape = shape_of(n_q, 1, d)
+    r = np.random.default_rng(26)
+    pool = filled_pool(r, 1, 1, d)
+    q = torch.from_numpy(r.standard_normal((rows, n_q, d))).to(torch.bfloat16)
+    bt = torch.zeros(1, pages, dtype=torch.int32, device=DEV)
+    h = _lib.Kv4(shape, 1, pages)
+    cache = _lib.KvCache(shape, 1, _lib.NF_KV_FP4, torch.from_numpy(pool).to(DEV))
+    o = torch.empty(rows, n_q, d, dtype=torch.bfloat16, device=DEV)
+    _lib.attention_kv4(h, q.to(DEV), cache, bt, dev32([16 * pages]), o, dev32([0, rows]))
+    h.poll()
+    got = o.double().cpu().numpy()
+    q64 = q.double().numpy()
+    want, mag = (np.concatenate(x) for x in zip(*(orc.attention(q64[i:i + 1], pool, (0, 0), np.zeros((1, 1), int), [16], [1]) for i in range(rows))))
+    top = np.abs(orc.take(pool, range(16), 0, 0)).max()
+    mass = np.abs(q64).sum(-1, keepdims=True) * top / np.sqrt(d)
+    adds = pages / 1200 if rows == 1 else pages / 8 / 100 * 16  # a block is 16 steps of 8 positions
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -20 + 2 * adds * 2.0 ** -24 + 2 * d * 2.0 ** -24 * mass + rows / pages) * mag
+    assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / mag).max()
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("n_q,n_kv,d", [(8, 2, 128), (4, 4, 64)])
@@ -971,3 +1051,90 @@ def test_a_served_batch(n_q, n_kv, d):
         bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -20 + 2 * d * 2.0 ** -24 * np.abs(q64).sum(-1, keepdims=True) * 10) * mag
         assert (np.abs(o.double().cpu().numpy() - ref) <= bound).all()
         held = lens
+
+
+def test_the_attention_half_of_a_layer():
+    """RMSNorm, QKV GEMM, tables, append, attention and the O GEMM with its residual over the 4-bit cache: a
+    prompt step call by call, every stage against float64 from the stage before, then decode steps of the same
+    padded batch in one captured graph, bit for bit what single calls give."""
+    n_q, n_kv, d, hidden = 8, 2, 64, 256
+    shape = shape_of(n_q, n_kv, d)
+    r = np.random.default_rng(27)
+    n, width, num, cap = 5, 6, 24, 64
+    width_qkv = (n_q + 2 * n_kv) * d
+    rnd = lambda *s, std=1.0: torch.from_numpy(std * r.standard_normal(s)).to(torch.bfloat16)  # noqa: E731
+    norm, w_qkv, w_o = 1 + 0.1 * rnd(hidden), rnd(width_qkv, hidden, std=0.06), rnd(hidden, n_q * d, std=0.05)
+    gains = gains_of(r, d)
+    g = dict(norm=norm.to(DEV), w_qkv=w_qkv.to(DEV), w_o=w_o.to(DEV), q=gains[0].to(DEV), k=gains[1].to(DEV))
+    xs = rnd(cap, hidden).to(DEV)
+    lens0 = np.array([20, 1, 0, 16, 17])
+
+    def state():
+        z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device=DEV)  # noqa: E731
+        pool = torch.full((num, n_kv, 2, 9 * d), 0x7F, dtype=torch.uint8, device=DEV)
+        s = dict(held=z(n), lens=dev32(lens0), bt=z(n, width) - 1, ring=torch.arange(num, dtype=torch.int32, device=DEV), st=dev32([0, num]),
+                 out=z(4), begin=z(n + 1), seq=z(cap), pos=z(cap), slot=z(cap) - 1, pool=pool, cache=_lib.KvCache(shape, num, _lib.NF_KV_FP4, pool),
+                 handle=_lib.Kv4(shape, num, width))
+        b = torch.bfloat16
+        s |= dict(n1=z(cap, hidden, t=b), qkv=z(cap, width_qkv, t=b), q=z(cap, n_q, d, t=b), o=z(cap, n_q, d, t=b), y=z(cap, hidden, t=b))
+        s["args"] = _lib.BlockTables(s["held"], s["lens"], s["bt"], s["ring"], s["st"], s["out"], s["begin"], s["seq"], s["pos"], s["slot"])
+        return s
+
+    def step(s):
+        s["slot"].fill_(-1)  # rows behind the step's tokens store nothing
+        _lib.block_tables(s["args"])
+        _lib.rmsnorm(xs, g["norm"], s["n1"], 1e-5)
+        _lib.gemm(s["n1"], g["w_qkv"], s["qkv"])
+        _lib.qk_norm_rope(shape, s["qkv"], g["q"], g["k"], s["pos"], s["slot"], s["q"], s["cache"])
+        _lib.attention_kv4(s["handle"], s["q"], s["cache"], s["bt"], s["lens"], s["o"], s["begin"])
+        _lib.gemm(s["o"].view(cap, -1), g["w_o"], s["y"], R=xs, epilogue=_lib.NF_EPI_RESID)
+
+    def grow(s):  # the next step: every request one token longer
+        s["st"].copy_(s["out"][:2])
+        s["held"].copy_(s["lens"])
+        s["lens"].add_(1)
+
+    a = state()
+    step(a)
+    a["handle"].poll()
+    h = {k: v.double().cpu().numpy() for k, v in a.items() if isinstance(v, torch.Tensor) and v.dtype == torch.bfloat16}
+    x64, tok = xs.double().cpu().numpy(), int(lens0.sum())
+    assert host(a["out"]).tolist() == [6, num - 6, tok, 0]  # 2 + 1 + 0 + 1 + 2 pages
+
+    def near(got, ref, mass, k):  # one rounding to bf16, k products summed in fp32
+        assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + k * 2.0 ** -24 * mass).all()
+
+    n1 = x64 / np.sqrt((x64 * x64).mean(-1, keepdims=True) + float(np.float32(1e-5))) * norm.double().numpy()
+    near(h["n1"], n1, np.abs(n1), hidden)
+    w64, o64 = w_qkv.double().numpy(), w_o.double().numpy()
+    near(h["qkv"], h["n1"] @ w64.T, np.abs(h["n1"]) @ np.abs(w64).T, hidden)
+    u, pos, slot = h["qkv"].reshape(cap, -1, d), host(a["pos"]), host(a["slot"])
+    want = np.full((num, n_kv, 2, 9 * d), 0x7F, np.uint8)
+    keys = orc.norm_rope(u[:tok, n_q:n_q + n_kv], gains[1].double().numpy(), pos[:tok], 1e4, float(np.float32(1e-5)))
+    for i in range(tok):
+        orc.put(want, int(slot[i]), 0, *orc.quantise(keys[i], 0))
+        orc.put(want, int(slot[i]), 1, *orc.quantise(u[i, n_q + n_kv:], 0))
+    assert np.array_equal(host(a["pool"]), want)
+    ref, mag = orc.attention(h["q"][:tok], want, (0, 0), host(a["bt"]), lens0, lens0)
+    mass = np.abs(h["q"][:tok]).sum(-1, keepdims=True) * np.nan_to_num(np.abs(orc.take(want, slot[:tok], 0, 0))).max() / np.sqrt(d)
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -20 + 2 * d * 2.0 ** -24 * mass) * mag + 64 * 2.0 ** -32 * 8
+    assert (np.abs(h["o"][:tok] - ref) <= bound).all() and not h["o"][tok:].any()
+    of = h["o"].reshape(cap, -1)
+    near(h["y"], x64 + of @ o64.T, np.abs(x64) + np.abs(of) @ np.abs(o64).T, n_q * d + 1)
+
+    b = state()
+    step(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grow(b)
+        step(b)
+    for _ in range(4):
+        grow(a)
+        step(a)
+        graph.replay()
+        for k in ("bt", "ring", "out", "begin", "slot", "pool", "q", "o", "y"):
+            assert torch.equal(a[k], b[k]), k
+    for s in (a, b):
+        s["handle"].poll()
+    assert host(a["out"])[2:].tolist() == [n, 0] and host(a["lens"]).tolist() == (lens0 + 4).tolist()
