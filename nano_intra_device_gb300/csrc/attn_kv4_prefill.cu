@@ -107,18 +107,6 @@ struct KpLayout {
   static constexpr int REC = 2 * TREC;
 };
 
-__device__ __forceinline__ uint32_t kp_sw128(int r, int c) {
-  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
-}
-__device__ __forceinline__ void kp_st16(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ uint32_t kp_pack(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 template <int N>
 __device__ __forceinline__ void kp_regs_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -126,11 +114,6 @@ __device__ __forceinline__ void kp_regs_less() {
 template <int N>
 __device__ __forceinline__ void kp_regs_more() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-__device__ __forceinline__ float kp_max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 // 32 lanes x 16 columns, as the 32-column forms.
 __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -478,7 +461,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         for (int k = 0; k < CW; ++k) {  // chunk of 8 channels: one word, two chunks a scale
           const int ch = NCH == 2 ? k ^ (4 * hf) : 4 * hf + k;
           const uint32_t s2 = f[k / 2];
-          kp_st16(row + ((ch ^ (pos & 7)) << 4),
+          st_shared_v4(row + ((ch ^ (pos & 7)) << 4),
                   make_uint4(hmul2_u(e2m1_to_f16x2<0>(w[i][k]), s2), hmul2_u(e2m1_to_f16x2<1>(w[i][k]), s2),
                              hmul2_u(e2m1_to_f16x2<2>(w[i][k]), s2), hmul2_u(e2m1_to_f16x2<3>(w[i][k]), s2)));
         }
@@ -619,9 +602,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         for (int c = 0; c < D / 8; ++c) {
           uint4 v = q4[c];
           if (!live) v = make_uint4(0, 0, 0, 0);
-          top = fmaxf(top, kp_max3(kp_max3(fabsf(bf16lo(v.x)), fabsf(bf16hi(v.x)), fabsf(bf16lo(v.y))),
-                                   kp_max3(fabsf(bf16hi(v.y)), fabsf(bf16lo(v.z)), fabsf(bf16hi(v.z))),
-                                   fmaxf(fabsf(bf16lo(v.w)), fabsf(bf16hi(v.w)))));
+          top = fmaxf(top, fmax3(fmax3(fabsf(bf16lo(v.x)), fabsf(bf16hi(v.x)), fabsf(bf16lo(v.y))),
+                                 fmax3(fabsf(bf16hi(v.y)), fabsf(bf16lo(v.z)), fabsf(bf16hi(v.z))),
+                                 fmaxf(fabsf(bf16lo(v.w)), fabsf(bf16hi(v.w)))));
           own[c] = v;
         }
         const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
@@ -632,9 +615,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           const uint4 v = own[c];
-          kp_st16(sbase + t * Lay::Q_BYTES + (c >> 3) * KP_REGION + kp_sw128(r, c & 7),
-                  make_uint4(kp_pack(bf16lo(v.x) * mul, bf16hi(v.x) * mul), kp_pack(bf16lo(v.y) * mul, bf16hi(v.y) * mul),
-                             kp_pack(bf16lo(v.z) * mul, bf16hi(v.z) * mul), kp_pack(bf16lo(v.w) * mul, bf16hi(v.w) * mul)));
+          st_shared_v4(sbase + t * Lay::Q_BYTES + (c >> 3) * KP_REGION + sw128(r, c & 7),
+                  make_uint4(pack_f16(bf16lo(v.x) * mul, bf16hi(v.x) * mul), pack_f16(bf16lo(v.y) * mul, bf16hi(v.y) * mul),
+                             pack_f16(bf16lo(v.z) * mul, bf16hi(v.z) * mul), pack_f16(bf16lo(v.w) * mul, bf16hi(v.w) * mul)));
         }
         fence_proxy_async_smem();
         arrive(&bars->q_full[t]);
@@ -662,14 +645,14 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
         {
           float mx8[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mx8[i] = kp_max3(x[i], x[8 + i], x[16 + i]);
+          for (int i = 0; i < 8; ++i) mx8[i] = fmax3(x[i], x[8 + i], x[16 + i]);
 #pragma unroll
           for (int i = 24; i < KP_N - 8; i += 16)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mx8[k] = kp_max3(mx8[k], x[i + k], x[i + 8 + k]);
+            for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], x[i + k], x[i + 8 + k]);
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], x[KP_N - 8 + k]);
-          mx = kp_max3(kp_max3(mx8[0], mx8[1], mx8[2]), kp_max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * scale;
+          mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * scale;
         }
         float corr = 1.f;
         if (mx + nm > KP_SLACK + KP_SHIFT) {  // also from -inf, where O and l are still zero
@@ -735,7 +718,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) attn_kv4_prefill_kernel(const K
 #pragma unroll
           for (int i = 0; i < 32; ++i) ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = kp_pack(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]);
+          for (int i = 0; i < 32; ++i) w[i] = pack_f16(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]);
           tc_st_32x32b_x32(s_tmem + 32 * c, w);
         }
         tc_wait_st();

@@ -81,25 +81,6 @@ struct TpLayout {
   static constexpr int SMEM = 1024 + BAR_OFF + static_cast<int>(sizeof(TpBars));
 };
 
-// Byte offset of 16-byte chunk c (elements 8c .. 8c + 7 of a 64-column
-// region) of row r, in the 128-byte swizzle the TMA boxes and the MMA
-// descriptors use (regions are 1024-byte aligned).
-__device__ __forceinline__ uint32_t sw128(int r, int c) {
-  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-               "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
 template <int GRP, int NCH>
 __global__ void __launch_bounds__(TP_THREADS, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap tmK,

@@ -55,6 +55,12 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t v) {
   *reinterpret_cast<uint32_t*>(&h) = v;
   return __half22float2(h);
 }
+// lo in the low half
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // max that keeps a NaN
 __device__ __forceinline__ float fmax_nan(float a, float b) {
   float r;
