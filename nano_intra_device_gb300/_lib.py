@@ -200,12 +200,14 @@ def stream_handle(stream=None, dev=None):
     import torch
     if stream is not None:
         return c_void_p(stream.cuda_stream)
-    if dev is None:
-        dev = torch.cuda.current_device()
+    return c_void_p(_current_stream(torch, torch.cuda.current_device() if dev is None else dev))
+
+
+def _current_stream(torch, dev):
     # the current stream's handle alone, where this torch has a query for it: a
     # torch.cuda.Stream object around it takes 3 us, as long as a launch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return c_void_p(raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream)
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def make_shape(shape) -> nf_model_shape:
@@ -483,7 +485,7 @@ def _call_stream(dev, stream):
     current = torch.cuda.current_device()
     if dev != current:
         raise ValueError(f"the call's tensors are on cuda:{dev}, the current device is cuda:{current}")
-    return stream_handle(stream, dev)
+    return _current_stream(torch, dev) if stream is None else stream.cuda_stream
 
 
 class KvCache:
@@ -509,6 +511,7 @@ class KvCache:
         self.heads = (s.n_kv_heads, s.head_dim)
         self.types = (torch.bfloat16, torch.int32)
         self.c = nf_kv_cache(fmt, num_pages, k.data_ptr(), None if v is None else v.data_ptr(), k_exp, v_exp)
+        self.ref = ctypes.byref(self.c)
 
 
 def kv4_pool_bytes(shape, num_pages):
@@ -569,7 +572,7 @@ def qk_norm_rope(shape, qkv, q_gain, k_gain, tok_pos, tok_slot, q, cache: KvCach
                                 None if q_gain is None else _arg("q_gain", q_gain, bf16, d, dev),
                                 None if k_gain is None else _arg("k_gain", k_gain, bf16, d, dev),
                                 _arg("tok_pos", tok_pos, i32, n, dev), _arg("tok_slot", tok_slot, i32, n, dev), n,
-                                _arg("q", q, bf16, n * s.n_q_heads * d, dev), ctypes.byref(cache.c),
+                                _arg("q", q, bf16, n * s.n_q_heads * d, dev), cache.ref,
                                 _call_stream(dev, stream)))
 
 
@@ -579,7 +582,7 @@ def kv4_read(shape, cache: KvCache, slots, k, v, stream=None):
     if cache.heads != (s.n_kv_heads, s.head_dim):
         raise ValueError("the cache was made for another shape")
     size = n * s.n_kv_heads * s.head_dim
-    check(lib().nf_kv4_read(ctypes.byref(s), ctypes.byref(cache.c), _arg("slots", slots, i32, n, dev), n,
+    check(lib().nf_kv4_read(ctypes.byref(s), cache.ref, _arg("slots", slots, i32, n, dev), n,
                             _arg("k", k, bf16, size, dev), _arg("v", v, bf16, size, dev), _call_stream(dev, stream)))
 
 
@@ -627,7 +630,7 @@ def attention_kv4(handle: Kv4, q, cache: KvCache, block_table, seq_lens, o, tok_
         raise ValueError("the cache was made for another shape than the handle")
     if o.dtype is not bf16 or o.numel() < rows * handle.row or not o.is_contiguous():
         raise ValueError("o: need contiguous bf16 rows, as many as q's at least")
-    check(lib().nf_attention_kv4(handle.h, _arg("q", q, bf16, rows * handle.row, dev), ctypes.byref(cache.c),
+    check(lib().nf_attention_kv4(handle.h, _arg("q", q, bf16, rows * handle.row, dev), cache.ref,
                                  _arg("block_table", block_table, i32, n * handle.max_pages, dev),
                                  _arg("seq_lens", seq_lens, i32, n, dev),
                                  None if tok_begin is None else _arg("tok_begin", tok_begin, i32, n + 1, dev), n, rows,
