@@ -557,6 +557,12 @@ nf_status nf_kv4_selftest_drop(nf_kv4 h, int32_t cta, int32_t part, int32_t bloc
  * sees makes NaN of every channel (NaN in K) or of its block's channels at
  * least (NaN in V), and so does a NaN or an infinity in its query (every
  * channel of that head).
+ * Arithmetic: K and V enter the products exactly, q in fp16 scaled by a power of
+ * two a head (elements below 2^-28 of the head's largest lose bits), the
+ * softmax's weights in fp16 (each off by at most 2^-11 of itself, or 2^-32 of
+ * the largest; nf_attention's decode rows keep 16 bits).  Products' sums, maxima
+ * and denominators are fp32, o is rounded to bf16 once.  Scores have to stay
+ * within fp32's range, as they do below |q| 2^k_exp = 2^112.
  * A page id outside the pool reads page 0, a length outside
  * [0, 16 * max_pages_per_seq] counts as 0, rows outside [0, n_tok) are left
  * out, and rows that together would read 2^32 pages of a KV head or more are

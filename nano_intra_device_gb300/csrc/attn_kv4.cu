@@ -21,7 +21,10 @@
 //  * Q enters in fp16 scaled by a power of two a column (its largest element to
 //    2^14): bf16's 8 bits fit fp16's 11 down to 2^-28 of the largest element.
 //  * P enters as fp16 of 2^7 times its share of the running maximum (2^-11
-//    relative, exact zero only below 2^-32); the denominators sum the fp32
+//    relative, exact zero only below 2^-32).  Its lower bits would take a second
+//    product with V, 8 more matrix instructions beside the 16 of a page, in a kernel
+//    bound by issue; without them the error of the bf16 output to the formula in 64
+//    bits is 1 % above that of fp32 weights.  The denominators sum the fp32
 //    values.  The maximum m is raised only when p, as it is computed, would pass
 //    2^15 (a score 2^8 times the maximum's share): beyond 2^24 a score's steps reach
 //    what KA_SHIFT - m rounds off, so a bound on the score itself would not keep p

@@ -123,11 +123,16 @@ nf_status check_cache(const nf_kv_cache* c, bool fp4_only) {
 // requests of 500: 78 / 177, 129 / 182, 178 / 184.  With 8 query heads 70 / 66 at
 // 64, with 64 heads 68 / 64 at 64 and 93 / 62 at 96.
 constexpr int kSmallVecs = 64;
-// A launch of tiles takes 35 to 40 us however little there is to do (its roles'
-// code comes from memory once).  So where the kernel of few rows can at most visit
-// this many (page, KV head, 8 vectors) an SM, by the longest request that the
-// handle allows, every request goes there: 128 vectors of one request of 2000
-// positions (105 an SM) 25 / 43 us, of 8000 (421) 43 / 51, of 32,000 (1684) 113 / 68.
+// The tiles' fixed cost is higher: a second launch, and a short unit is cut into
+// pieces of one block, up to about 16, which one CTA joins one after the other.  One
+// request of 32 rows and 4 heads a KV head, tiles / few rows, in a graph: over 100
+// positions (one block, no join) 20.6 / 12.2 us, 500: 22.2 / 18.2, 2000: 32.7 / 19.9,
+// 8000: 41.1 / 36.9; by single calls 32,000: 68 / 113.  So where the kernel of few
+// rows can at most visit this many (page, KV head, 8 vectors) an SM, every request
+// goes there.  The lengths are on the device, so the bound takes every request to be
+// as long as the handle allows: a handle much wider than its requests sends chunks
+// past kSmallVecs to the tiles however short they are (the 32 rows over 2000
+// positions: 20 us in a handle of 512 pages a request, 33 in one of 40,000).
 constexpr int kFewVisits = 500;
 
 // Frequencies of (theta, head_dim), computed once for each pair in use: 64

@@ -259,7 +259,9 @@ __global__ void __launch_bounds__(BT_THREADS) block_tables_kernel(const BlockTab
 // bits against borders of at most 7.
 //
 // Measured: 64 tokens of 32 + 8 + 8 heads of 128 into 4 bits 6 us, into bf16 2048
-// tokens 16.4 us (50 MB: 7.4 at the copy rate).  8191 tokens of 64 + 8 + 8 heads
+// tokens 16.4 us (50 MB: 7.4 at the copy rate): 512 CTAs of 4 tokens, 304 of which
+// are resident at 106 registers, so 1.7 waves of 16 warps an SM, which memory latency
+// bounds.  8191 tokens of 64 + 8 + 8 heads
 // into 4 bits: 28 us for keys and values, which are bound by issue (the codes'
 // and borders' arithmetic), then 46 us for the queries at 64 % of the DRAM rate.
 constexpr int QK_THREADS = 256;

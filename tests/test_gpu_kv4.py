@@ -898,6 +898,33 @@ def test_a_new_handle_on_a_stream_beside_a_busy_default_stream(width):
     h.poll()
 
 
+def test_polls_without_waiting_report_a_status_once():
+    """Polls beside a running call on another stream: the bit is reported by one of them and never again."""
+    r = np.random.default_rng(28)
+    shape = shape_of(4, 2, 64)
+    lens = [40, 20]
+    pool, bt, q = attention_case(r, 4, 2, 64, lens, [1, 1])
+    bt[1, 0] = -5
+    h = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
+    cache = _lib.KvCache(shape, pool.shape[0], _lib.NF_KV_FP4, torch.from_numpy(pool).to(DEV))
+    args = (h, q.to(DEV), cache, dev32(bt), dev32(lens), torch.empty(2, 4, 64, dtype=torch.bfloat16, device=DEV))
+    a, side = torch.randn(4096, 4096, device=DEV), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            a = a @ a
+            a = a / a.abs().max()
+        _lib.attention_kv4(*args)
+    reports = 0
+    for wait in [False] * 50 + [True] * 2:
+        try:
+            h.poll(wait)
+        except _lib.NanoflowError as e:
+            assert e.code == _lib.NF_ERR_DEVICE
+            reports += 1
+    assert reports == 1
+
+
 def test_binding_refuses_tensors_of_another_device():
     """One tensor of a call on the CPU: refused on the host, before its address goes anywhere."""
     shape, b = shape_of(4, 2, 64), torch.bfloat16
