@@ -31,7 +31,7 @@
 // The rings run on over the ends of units.
 //
 // Measured (1985 rows over 4099 positions, 32 query and 8 KV heads of 128, 166
-// GFLOP, beside 63 decode rows): 219 us for this kernel, 243 for the
+// GFLOP, beside 63 decode rows): 221 us for this kernel, 244 for the
 // call, 36 % of the cuBLAS bf16 rate.  What bounds it: the softmax warps, two on each of an
 // SM's four schedulers, which issue in a third of the cycles; they wait for scores
 // and for their own chains, and a sixth of the waits is for instructions (four
