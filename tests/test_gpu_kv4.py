@@ -898,6 +898,36 @@ def test_a_new_handle_on_a_stream_beside_a_busy_default_stream(width):
     h.poll()
 
 
+@pytest.mark.parametrize("limit", [1, 1000, 4000, 16_000])
+def test_attention_limits_shorter_than_its_waits(limit):
+    """Limits of the order of a wait, so that any role may be the one that gives up: a call computes or reports
+    a timeout, and with the ordinary limit the handle is as new."""
+    r = np.random.default_rng(29)
+    shape = shape_of(8, 2, 128)
+    lens, q_lens = [3000, 40, 500], [500, 1, 200]
+    pool, bt, q = attention_case(r, 8, 2, 128, lens, q_lens, width=WIDE)
+    h = _lib.Kv4(shape, pool.shape[0], bt.shape[1])
+    cache = _lib.KvCache(shape, pool.shape[0], _lib.NF_KV_FP4, torch.from_numpy(pool).to(DEV))
+    args = (h, q.to(DEV), cache, dev32(bt), dev32(lens))
+    begin = dev32(np.concatenate([[0], np.cumsum(q_lens)]))
+    good, got = (torch.empty(q.shape, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    _lib.attention_kv4(*args, good, begin)
+    h.poll()
+    for _ in range(5):
+        got.zero_()
+        h.set_timeout(limit)
+        _lib.attention_kv4(*args, got, begin)
+        try:
+            h.poll()
+            assert torch.equal(got, good)
+        except _lib.NanoflowError as e:
+            assert e.code == _lib.NF_ERR_TIMEOUT
+        h.set_timeout(2_000_000_000)
+        _lib.attention_kv4(*args, got, begin)
+        h.poll()
+        assert torch.equal(got, good)
+
+
 def test_polls_without_waiting_report_a_status_once():
     """Polls beside a running call on another stream: the bit is reported by one of them and never again."""
     r = np.random.default_rng(28)
