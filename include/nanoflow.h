@@ -573,6 +573,89 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
                            const int32_t* tok_begin, int32_t n_seq, int32_t n_tok, void* o,
                            void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Products in 8-bit floating point.  A layer's projections are bound by the
+ * bytes of their weights at decode batches and by the tensor rate at larger
+ * ones ("NanoFlow: Towards Optimal LLM Serving Throughput", "The Intra-Device
+ * Parallelism Mechanism"); 8-bit operands halve the one and double the other.
+ * The entry points bring activations and weights into the format and multiply
+ * them, for one matrix or by experts; they stand beside nf_rmsnorm and nf_gemm.
+ *
+ * Format.  A value is its e4m3 code (sign, 4 exponent and 3 mantissa bits,
+ * largest 448, no infinity) times the fp32 scale of its block of 128:
+ *   s = max(max |y| / 448, 2^-126),  q = e4m3(y / s),
+ * both quotients rounded to fp32 first, to nearest, ties to even (where s is
+ * below 2^-100, y / s may be an ulp off).  A block that holds a NaN or an
+ * infinity has a NaN for its scale and for its codes.
+ * Rows (activations) have a scale for each 128 consecutive columns of a row,
+ *   laid out by column block: s [ceil(cols / 128)][rows].
+ * Weights have one for each block of 128 x 128: s [ceil(rows / 128)]
+ *   [ceil(cols / 128)].
+ * The last block of a row or column may be shorter.  Codes are dense row-major
+ * with rows of a multiple of 16 columns, 16-byte aligned.
+ * None of these calls allocates or holds anything between calls: they may run
+ * at once on several streams and in captured graphs. */
+
+/* RMSNorm of x + r to 8-bit rows: h = x + r, y = h * g / sqrt(mean(h^2) + eps),
+ * all in fp32 (the squares' sum must stay within its range); y becomes q and s.
+ * x, r, h: device bf16 [rows, hidden]; r NULL: h = x.  h (the residual of the
+ * next addition, rounded to bf16) may be NULL, must be without r, and may be x
+ * or r itself.  g: device bf16 [hidden].  q: device e4m3 [rows, hidden], s:
+ * device fp32 [ceil(hidden / 128)][rows].  hidden: a multiple of 16, <= 32768. */
+nf_status nf_rmsnorm_fp8(const void* x, const void* r, const void* g, void* h, void* q, float* s,
+                         int32_t rows, int32_t hidden, float eps, void* stream);
+
+/* Rows to 8 bits: row i of q and s is that of row index[i] of x (device bf16
+ * [src_rows, cols]); index: device int32 [rows], e.g. the tokens of the experts'
+ * rows, or NULL: row i (src_rows = rows).  An index outside [0, src_rows) gives
+ * a row of zeros.  cols: a multiple of 16, <= 32768. */
+nf_status nf_quant_fp8(const void* x, int32_t src_rows, const int32_t* index, void* q, float* s,
+                       int32_t rows, int32_t cols, void* stream);
+
+/* Weights to 8 bits: w device bf16 [mats, rows, cols], q e4m3 of the same
+ * shape, s fp32 [mats][ceil(rows / 128)][ceil(cols / 128)].  Gate and up rows of
+ * a SwiGLU product are two matrices.  cols: a multiple of 16. */
+nf_status nf_quant_fp8_weights(const void* w, void* q, float* s, int32_t mats, int32_t rows,
+                               int32_t cols, void* stream);
+
+/* C = A * B^T of 8-bit operands, fp32 sums.
+ * A: device e4m3 rows [M, K], a_s [ceil(K / 128)][M].  B: device e4m3 weights
+ *   [N, K], b_s [ceil(N / 128)][ceil(K / 128)].
+ * epilogue: NF_EPI_STORE, NF_EPI_RESID, NF_EPI_SWIGLU as for nf_gemm, C (and R)
+ *   device bf16 [M, N].  SwiGLU: B holds 2 N rows, gate rows then up rows, each
+ *   a matrix of its own scales: b_s [2][ceil(N / 128)][ceil(K / 128)].
+ *   NF_EPI_SWIGLU_FP8: the SwiGLU's fp32 values to 8-bit rows without a rounding
+ *   between, C device e4m3 [M, N], c_s [ceil(N / 128)][M]; c_s is not used by
+ *   the others.
+ * K a multiple of 16, N of 8 (NF_EPI_SWIGLU_FP8: of 16); M = 0 does nothing.
+ * C must not overlap A or B; C = R is allowed.  The product of a row's and a
+ * column's scale has to stay within fp32's range.  A NaN scale makes NaN of its
+ * row's (its 128 columns') outputs.
+ * max_sms caps the grid (0 = all SMs). */
+#define NF_EPI_SWIGLU_FP8 3
+nf_status nf_gemm_fp8(const void* A, const float* a_s, const void* B, const float* b_s, void* C,
+                      float* c_s, const void* R, int32_t M, int32_t N, int32_t K, int32_t epilogue,
+                      int32_t max_sms, void* stream);
+
+/* The same by groups of rows ("NanoFlow: Towards Optimal LLM Serving
+ * Throughput", MoE models: a grouped GEMM in which experts compute on different
+ * tokens): rows [group_off[e], group_off[e + 1]) of A and C go with matrix e of
+ * B, b_s: [groups][N or 2 N][K] and its scales.  group_off: device int32
+ * [groups + 1], read on the device, groups in [1, 128]; groups may be empty.  Rows
+ * of C and entries of c_s outside [group_off[0], group_off[groups]) stay as they
+ * are.  Offsets count within [0, M], and one below the one before it as that
+ * one.  No NF_EPI_RESID. */
+nf_status nf_gemm_fp8_grouped(const void* A, const float* a_s, const void* B, const float* b_s,
+                              const int32_t* group_off, int32_t groups, void* C, float* c_s,
+                              int32_t M, int32_t N, int32_t K, int32_t epilogue, int32_t max_sms,
+                              void* stream);
+
+/* Waits for `stream`, then reports and clears what the products of this section
+ * have flagged on the current device since the last poll: NF_OK, or
+ * NF_ERR_TIMEOUT if a bounded wait gave up (2 s; outputs since then are
+ * undefined). */
+nf_status nf_fp8_poll(void* stream);
+
 /* Copy one of the plan's device buffers (written by the last step or
  * metadata call on the plan's device) to dst (host or device), synchronously.
  * bytes must not exceed the buffer size (nf_plan_buffer_size). */

@@ -21,6 +21,7 @@ NF_OK, NF_ERR_INVALID_ARG, NF_ERR_UNSUPPORTED, NF_ERR_OOM, NF_ERR_CUDA, NF_ERR_T
 NF_EXEC_SEQUENTIAL, NF_EXEC_STREAMS = 0, 1
 NF_ATTN_AUTO, NF_ATTN_MMA = 0, 2
 NF_EPI_STORE, NF_EPI_RESID, NF_EPI_SWIGLU = 0, 1, 2
+NF_EPI_SWIGLU_FP8 = 3
 NF_KV_BF16, NF_KV_FP4 = 0, 1
 (NF_BUF_TOK_SEQ, NF_BUF_TOK_POS, NF_BUF_TOK_SLOT, NF_BUF_ITEMS, NF_BUF_ITEM_SEG, NF_BUF_N1,
  NF_BUF_Q, NF_BUF_O, NF_BUF_H, NF_BUF_N2, NF_BUF_A, NF_BUF_MOE_OFF, NF_BUF_MOE_PERM,
@@ -125,6 +126,14 @@ _SIGS = {
     "nf_gemm": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p]),
     "nf_gemm_wrows": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
                               c_int32, c_int32, c_void_p]),
+    "nf_rmsnorm_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_float, c_void_p]),
+    "nf_quant_fp8": (c_int, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p]),
+    "nf_quant_fp8_weights": (c_int, [c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p]),
+    "nf_gemm_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32,
+                            c_int32, c_int32, c_void_p]),
+    "nf_gemm_fp8_grouped": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
+                                    c_int32, c_int32, c_int32, c_int32, c_void_p]),
+    "nf_fp8_poll": (c_int, [c_void_p]),
     "nf_kv4_pool_bytes": (c_int, [POINTER(nf_model_shape), c_int32, POINTER(c_size_t)]),
     "nf_block_tables": (c_int, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_int32, c_void_p,
                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p]),
@@ -453,8 +462,6 @@ def gemm_wrows(A, B, C, R=None, epilogue=NF_EPI_STORE, splits=0, max_sms=0, stre
                               stream_handle(stream)))
 
 
-# ------------------------------------------------------ the 4-bit KV cache
-
 def _dense(name, t, dtype, *shape):
     """Check a tensor that a call's addresses are taken from (None in shape: any extent)."""
     if t.dtype != dtype or not t.is_contiguous() or t.dim() != len(shape) or \
@@ -487,6 +494,94 @@ def _call_stream(dev, stream):
         raise ValueError(f"the call's tensors are on cuda:{dev}, the current device is cuda:{current}")
     return _current_stream(torch, dev) if stream is None else stream.cuda_stream
 
+
+# ------------------------------------------------------ 8-bit products
+
+_TYPES = []
+
+
+def _types():
+    """(e4m3, bf16, fp32, int32), looked up once."""
+    if not _TYPES:
+        import torch
+        _TYPES.extend((torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32))
+    return _TYPES
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def rmsnorm_fp8(x, g, q, s, eps, r=None, h=None, stream=None):
+    """nf_rmsnorm_fp8: RMSNorm of x (+ r, kept in h) to 8-bit rows q [rows, hidden] e4m3 and
+    s [ceil(hidden / 128), rows] fp32."""
+    (e4m3, bf16, f32, _), (rows, n), dev = _types(), x.shape, x.get_device()
+    size = rows * n
+    check(lib().nf_rmsnorm_fp8(_arg("x", x, bf16, size, dev), None if r is None else _arg("r", r, bf16, size, dev),
+                               _arg("g", g, bf16, n, dev), None if h is None else _arg("h", h, bf16, size, dev),
+                               _arg("q", q, e4m3, size, dev), _arg("s", s, f32, _blocks(n) * rows, dev), rows, n, eps,
+                               _call_stream(dev, stream)))
+
+
+def quant_fp8(x, q, s, index=None, stream=None):
+    """nf_quant_fp8: rows of x (those of index, where given) to 8 bits, q [rows, cols] e4m3 and
+    s [ceil(cols / 128), rows] fp32."""
+    (e4m3, bf16, f32, i32), (src, n), dev = _types(), x.shape, x.get_device()
+    rows = src if index is None else index.numel()
+    check(lib().nf_quant_fp8(_arg("x", x, bf16, src * n, dev), src, None if index is None else _arg("index", index, i32, rows, dev),
+                             _arg("q", q, e4m3, rows * n, dev), _arg("s", s, f32, _blocks(n) * rows, dev), rows, n,
+                             _call_stream(dev, stream)))
+
+
+def quant_fp8_weights(w, q, s, stream=None):
+    """nf_quant_fp8_weights: matrices w [..., rows, cols] to 8 bits, q e4m3 of that shape and
+    s [..., ceil(rows / 128), ceil(cols / 128)] fp32."""
+    (e4m3, bf16, f32, _), (rows, n), dev, size = _types(), w.shape[-2:], w.get_device(), w.numel()
+    mats = size // (rows * n) if size else 0
+    check(lib().nf_quant_fp8_weights(_arg("w", w, bf16, size, dev), _arg("q", q, e4m3, size, dev),
+                                     _arg("s", s, f32, mats * _blocks(rows) * _blocks(n), dev), mats, rows, n,
+                                     _call_stream(dev, stream)))
+
+
+def _product(a, a_s, b, b_s, groups, c, c_s, epilogue, dev):
+    """The checked addresses and sizes of an 8-bit product: (A, a_s, B, b_s), (C, c_s), (M, N, K)."""
+    e4m3, bf16, f32, _ = _types()
+    (m, k), n = a.shape, c.shape[1]
+    two = 2 if epilogue in (NF_EPI_SWIGLU, NF_EPI_SWIGLU_FP8) else 1
+    kb, nb = _blocks(k), _blocks(n)
+    eight = epilogue == NF_EPI_SWIGLU_FP8
+    if eight and c_s is None:
+        raise ValueError("c_s: an 8-bit output needs its scales")
+    return ((_arg("a", a, e4m3, m * k, dev), _arg("a_s", a_s, f32, kb * m, dev),
+             _arg("b", b, e4m3, groups * two * n * k, dev), _arg("b_s", b_s, f32, groups * two * nb * kb, dev)),
+            (_arg("c", c, e4m3 if eight else bf16, m * n, dev), _arg("c_s", c_s, f32, nb * m, dev) if eight else None),
+            (m, n, k))
+
+
+def gemm_fp8(a, a_s, b, b_s, c, c_s=None, r=None, epilogue=NF_EPI_STORE, max_sms=0, stream=None):
+    """nf_gemm_fp8: c [M, N] = a [M, K] b^T of 8-bit operands; b [N, K], for the SwiGLU epilogues
+    [2 N, K].  NF_EPI_SWIGLU_FP8: c e4m3 with scales c_s, else bf16."""
+    dev = a.get_device()
+    ins, outs, size = _product(a, a_s, b, b_s, 1, c, c_s, epilogue, dev)
+    check(lib().nf_gemm_fp8(*ins, *outs, None if r is None else _arg("r", r, c.dtype, size[0] * size[1], dev), *size,
+                            epilogue, max_sms, _call_stream(dev, stream)))
+
+
+def gemm_fp8_grouped(a, a_s, b, b_s, group_off, c, c_s=None, epilogue=NF_EPI_STORE, max_sms=0, stream=None):
+    """nf_gemm_fp8_grouped: rows [group_off[e], group_off[e + 1]) of a times b[e]^T; group_off int32
+    [groups + 1] on the device, b [groups, N or 2 N, K]."""
+    dev, groups = a.get_device(), group_off.numel() - 1
+    ins, outs, size = _product(a, a_s, b, b_s, groups, c, c_s, epilogue, dev)
+    check(lib().nf_gemm_fp8_grouped(*ins, _arg("group_off", group_off, _types()[3], groups + 1, dev), groups, *outs, *size,
+                                    epilogue, max_sms, _call_stream(dev, stream)))
+
+
+def fp8_poll(stream=None):
+    """nf_fp8_poll: wait for the stream, then report and clear what the 8-bit products flagged."""
+    check(lib().nf_fp8_poll(stream_handle(stream)))
+
+
+# ------------------------------------------------------ the 4-bit KV cache
 
 class KvCache:
     """The nf_kv_cache of one layer, and the tensors it points to.

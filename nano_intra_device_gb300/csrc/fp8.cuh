@@ -1,0 +1,76 @@
+// Device-side helpers of the 8-bit operators: e4m3 products on tcgen05, packed
+// fp32 arithmetic, the scale of a block and its codes.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "fp8.h"
+
+namespace nf {
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs (K = 32 an instruction), fp32 accumulate.
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (both K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Two fp32 values a register pair: one instruction for both.  Volatile: an
+// accumulator read from tensor memory must not be used ahead of the wait for it.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack_f32x2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 pack_b32x2(uint32_t a, uint32_t b) {
+  f32x2 r;
+  asm volatile("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void fma_f32x2(f32x2& d, f32x2 a, f32x2 b) {
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+
+// The larger magnitude; a NaN on either side stays.
+__device__ __forceinline__ float absmax_nan(float m, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+  return r;
+}
+// The scale of a block whose largest magnitude is `top`: NaN where that is not finite.
+__device__ __forceinline__ float f8_scale(float top) {
+  return top <= 3.402823466e38f ? fmaxf(top / 448.f, 1.17549435e-38f) : __int_as_float(0x7fffffff);
+}
+// y / s in fp32, s > 0 with its rounded reciprocal inv: the product errs by an ulp or
+// two, its remainder y - q s is exact in a fused multiply-add, and one correction by it
+// gives the rounded quotient (P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990); where s < 2^-100 the remainder may underflow
+// and the quotient be an ulp off.  A block's values are often exact ties of codes (a
+// ratio of two 8-bit significands times 448), so the product alone would settle 1 code
+// in 500 of a bf16 tensor otherwise.
+__device__ __forceinline__ float f8_quotient(float y, float s, float inv) {
+  const float q = y * inv;
+  return fmaf(fmaf(-q, s, y), inv, q);
+}
+// Four values over their scale s (inv its reciprocal) as codes, value 0 in the low byte.
+__device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d, float s, float inv) {
+  const float2 x = make_float2(f8_quotient(a, s, inv), f8_quotient(b, s, inv));
+  const float2 y = make_float2(f8_quotient(c, s, inv), f8_quotient(d, s, inv));
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+}  // namespace nf

@@ -1,0 +1,53 @@
+// Launch interface between the C ABI of the 8-bit operators (fp8.cu) and their kernels.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace nf {
+
+constexpr int F8_BLOCK = 128;        // columns (and, for weights, rows) of a scale's block
+constexpr int F8_MAX_GROUPS = 128;   // groups of rows of one product
+constexpr int F8_MAX_COLS = 32768;   // columns of a row that one CTA norms or quantises
+
+enum { F8_STORE = 0, F8_RESID = 1, F8_SWIGLU = 2, F8_SWIGLU8 = 3 };
+
+// Rows to 8 bits: out row i is that of x row index[i] (NULL: i), an index outside
+// [0, src_rows) a row of zeros.  g != NULL: RMSNorm first, of x + r (r NULL: x);
+// h != NULL receives x + r.
+struct F8RowsArgs {
+  const __nv_bfloat16 *x, *r, *g;
+  __nv_bfloat16* h;
+  const int* index;
+  int src_rows, rows, cols;
+  float eps;
+  uint8_t* q;
+  float* s;  // [ceil(cols / 128)][rows]
+};
+cudaError_t launch_f8_rows(const F8RowsArgs& a, cudaStream_t stream);
+
+// mats matrices [rows, cols] to 8 bits in 128 x 128 blocks, scales [mats][row block][column block].
+cudaError_t launch_f8_weights(const __nv_bfloat16* w, uint8_t* q, float* s, int mats, int rows,
+                              int cols, cudaStream_t stream);
+
+struct F8GemmArgs {
+  int M, N, K;           // N: output columns (the features for SwiGLU)
+  const float* a_s;      // [ceil(K / 128)][M]
+  const float* b_s;      // [groups][1, SwiGLU: 2][ceil(N / 128)][ceil(K / 128)]
+  const int* group_off;  // NULL: one group of all rows; else device [groups + 1]
+  int groups;
+  __nv_bfloat16* C;      // STORE, RESID, SWIGLU
+  const __nv_bfloat16* R;
+  uint8_t* q;            // SWIGLU8
+  float* c_s;            // SWIGLU8: [ceil(N / 128)][M]
+  unsigned long long timeout_ns;
+};
+// tmA: the rows of A, tmB: all groups' rows of B, both in boxes of 128 rows x 128 columns.
+cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                           const F8GemmArgs& args, int sms, cudaStream_t stream);
+// The bits that the kernels of launch_gemm_f8 raised on the current device, and zeros
+// in their place; waits for the stream.
+cudaError_t take_gemm_f8_status(uint32_t* bits, cudaStream_t stream);
+
+}  // namespace nf

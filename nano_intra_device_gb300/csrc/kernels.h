@@ -234,6 +234,10 @@ bool make_pool_tmap_pages(CUtensorMap* map, const void* pool, int num_pages, int
 // d = 64 the 2-D map above.
 bool make_pool_tmap_groups(CUtensorMap* map, const void* pool, int num_pages, int n_kv,
                            int page_size, int head_dim);
+// A 2-D map over rows of 8-bit values (cols a multiple of 16): boxes of box_rows
+// rows x 128 columns in the 128-byte swizzle.
+bool make_tmap_8bit(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                    uint32_t box_rows);
 // A 4-D map over rows of 128 bf16 (rows a multiple of 16): box = 16 rows as
 // [8-row group][64-column half][8 rows][64 columns].
 bool make_tmap_bf16_groups128(CUtensorMap* map, const void* base, uint64_t rows);
