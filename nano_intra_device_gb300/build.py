@@ -21,7 +21,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libnanoflow.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "gemm_tc.cu", "gemm_wrows.cu", "attn_mma.cu", "attn_prefill.cu", "meta.cu", "moe.cu", "rmsnorm.cu", "runtime.cu",
-           "kv4.cu", "kv4_ops.cu", "attn_kv4.cu", "attn_kv4_prefill.cu", "fp8.cu", "fp8_quant.cu", "gemm_fp8.cu", "profile.cu", "search.cpp", "noalloc.cu", "selftest.cu"]
+           "kv4.cu", "kv4_ops.cu", "attn_kv4.cu", "attn_kv4_prefill.cu", "fp8.cu", "fp8_quant.cu", "gemm_fp8.cu", "gemm_fp8_wrows.cu", "profile.cu", "search.cpp", "noalloc.cu", "selftest.cu"]
 
 
 def nvcc() -> str:

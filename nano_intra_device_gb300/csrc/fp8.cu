@@ -70,8 +70,13 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
     return fail8(NF_ERR_INVALID_ARG, "scales and offsets must be 4-byte aligned");
   const int sms = sm_count();
   if (sms <= 0) return fail8(NF_ERR_CUDA, "no CUDA device");
+  const bool capped = max_sms > 0 && max_sms < sms;
+  const int rows = (M + groups - 1) / groups;
+  const bool few = !capped && rows <= (groups > 1 ? 32 : 128);
+  nf::F8RowsChoice c{};
+  if (few) c = nf::gemm_f8_wrows_choice(epilogue, M, N, K, groups);
   CUtensorMap ta, tb;
-  if (!nf::make_tmap_8bit(&ta, A, M, K, 128) ||
+  if (!nf::make_tmap_8bit(&ta, A, M, K, few ? c.tok : 128) ||
       !nf::make_tmap_8bit(&tb, B, static_cast<uint64_t>(groups) * N * (two ? 2 : 1), K, 128))
     return fail8(NF_ERR_CUDA, "tensor map creation failed");
   nf::F8GemmArgs g{};
@@ -87,8 +92,12 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
   g.q = eight ? static_cast<uint8_t*>(C) : nullptr;
   g.c_s = c_s;
   g.timeout_ns = kTimeoutNs;
-  NF_CUDA8(nf::launch_gemm_f8(epilogue, ta, tb, g, max_sms > 0 && max_sms < sms ? max_sms : sms,
-                              static_cast<cudaStream_t>(stream)));
+  if (few) {
+    g.splits = c.splits;
+    NF_CUDA8(nf::launch_gemm_f8_wrows(epilogue, c.tok, tb, ta, g, c.units, static_cast<cudaStream_t>(stream)));
+  } else {
+    NF_CUDA8(nf::launch_gemm_f8(epilogue, ta, tb, g, capped ? max_sms : sms, static_cast<cudaStream_t>(stream)));
+  }
   return NF_OK;
 }
 
@@ -175,8 +184,10 @@ nf_status nf_gemm_fp8_grouped(const void* A, const float* a_s, const void* B, co
 }
 
 nf_status nf_fp8_poll(void* stream) {
-  uint32_t bits = 0;
+  uint32_t bits = 0, more = 0;
   NF_CUDA8(nf::take_gemm_f8_status(&bits, static_cast<cudaStream_t>(stream)));
+  NF_CUDA8(nf::take_gemm_f8_wrows_status(&more, static_cast<cudaStream_t>(stream)));
+  bits |= more;
   if (!bits) return NF_OK;
   return fail8(NF_ERR_TIMEOUT, "nf_gemm_fp8: a device-side wait timed out (status 0x%x)", bits);
 }

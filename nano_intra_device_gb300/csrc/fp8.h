@@ -41,6 +41,7 @@ struct F8GemmArgs {
   const __nv_bfloat16* R;
   uint8_t* q;            // SWIGLU8
   float* c_s;            // SWIGLU8: [ceil(N / 128)][M]
+  int splits;            // few rows: CTAs of a cluster, which split K
   unsigned long long timeout_ns;
 };
 // tmA: the rows of A, tmB: all groups' rows of B, both in boxes of 128 rows x 128 columns.
@@ -49,5 +50,18 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
 // The bits that the kernels of launch_gemm_f8 raised on the current device, and zeros
 // in their place; waits for the stream.
 cudaError_t take_gemm_f8_status(uint32_t* bits, cudaStream_t stream);
+
+
+// The same for few rows: tiles of 128 features x tok rows of A (tmX: the rows of A in
+// boxes of tok rows; tok 16, 32, 64 and, but for SwiGLU, 128), `units` clusters of
+// args.splits CTAs.
+struct F8RowsChoice {
+  int tok, splits;
+  long long units;
+};
+F8RowsChoice gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups);
+cudaError_t launch_gemm_f8_wrows(int epi, int tok, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                                 const F8GemmArgs& args, long long units, cudaStream_t stream);
+cudaError_t take_gemm_f8_wrows_status(uint32_t* bits, cudaStream_t stream);
 
 }  // namespace nf

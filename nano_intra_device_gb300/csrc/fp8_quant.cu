@@ -23,6 +23,8 @@ __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
 // 16 neighbouring threads hold a block of 128.
 template <int VPT, bool NORM, bool RES>
 __global__ void __launch_bounds__(512) f8_rows_kernel(const F8RowsArgs a) {
+  pdl_trigger();
+  pdl_wait();
   const int row = blockIdx.x, nvec = a.cols / 8;
   const int from = a.index ? a.index[row] : row;
   const bool there = from >= 0 && from < a.src_rows;
@@ -98,16 +100,17 @@ __global__ void __launch_bounds__(512) f8_rows_kernel(const F8RowsArgs a) {
 
 template <int VPT>
 cudaError_t launch_rows(const F8RowsArgs& a, int threads, cudaStream_t stream) {
-  if (!a.g) f8_rows_kernel<VPT, false, false><<<a.rows, threads, 0, stream>>>(a);
-  else if (a.r) f8_rows_kernel<VPT, true, true><<<a.rows, threads, 0, stream>>>(a);
-  else f8_rows_kernel<VPT, true, false><<<a.rows, threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (!a.g) return launch_dependent(f8_rows_kernel<VPT, false, false>, a.rows, threads, 0, stream, a);
+  if (a.r) return launch_dependent(f8_rows_kernel<VPT, true, true>, a.rows, threads, 0, stream, a);
+  return launch_dependent(f8_rows_kernel<VPT, true, false>, a.rows, threads, 0, stream, a);
 }
 
 // One CTA a 128 x 128 block: thread t has vector t % 16 of the rows t / 16 + 16 i.
 __global__ void __launch_bounds__(256)
     f8_weights_kernel(const __nv_bfloat16* __restrict__ w, uint8_t* __restrict__ q, float* __restrict__ s,
                       int rows, int cols, int row_blocks, int col_blocks) {
+  pdl_trigger();
+  pdl_wait();
   const int cb = blockIdx.x % col_blocks;
   const int rb = blockIdx.x / col_blocks % row_blocks;
   const size_t mat = blockIdx.x / col_blocks / row_blocks;
@@ -166,9 +169,8 @@ cudaError_t launch_f8_weights(const __nv_bfloat16* w, uint8_t* q, float* s, int 
   const long long rb = (rows + F8_BLOCK - 1) / F8_BLOCK, cb = (cols + F8_BLOCK - 1) / F8_BLOCK;
   if (mats * rb * cb <= 0) return cudaSuccess;
   if (mats * rb * cb > 0x7fffffffLL) return cudaErrorInvalidValue;
-  f8_weights_kernel<<<static_cast<unsigned>(mats * rb * cb), 256, 0, stream>>>(
-      w, q, s, rows, cols, static_cast<int>(rb), static_cast<int>(cb));
-  return cudaGetLastError();
+  return launch_dependent(f8_weights_kernel, static_cast<unsigned>(mats * rb * cb), 256, 0, stream, w, q, s, rows, cols,
+                          static_cast<int>(rb), static_cast<int>(cb));
 }
 
 }  // namespace nf

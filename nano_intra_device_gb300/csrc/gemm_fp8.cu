@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const bool grouped = args.group_off != nullptr;
   const uint64_t tmo = args.timeout_ns;
 
+  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&tail->full[s], 1);
@@ -90,6 +91,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(&tail->tmem_base, TMEM_COLS);
     tmem_relinquish();
   }
+  pdl_wait();  // nothing before this reads or writes global memory
   if (warp == 2 && grouped) {
     // Rows and tiles of the groups.  Offsets are held within [0, M], and one below
     // the one before it counts as that one, so no offset leads out of a tensor.
@@ -149,10 +151,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     return x;
   };
 
+  uint32_t issued = 0, phases = 0;  // thread 0: the ring's stages and the phase of their last load
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FEW));
     if (warp == 0 && lane == 0) {
-      uint32_t st = 0, ph = 0, issued = 0, phases = 0;
+      uint32_t st = 0, ph = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
         const Tile x = decode(u);
@@ -180,8 +183,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) {
         raise_status(&g_status, ST_TIMEOUT);
         *abort_flag = 1;
-        for (int s = 0; s < STAGES; ++s)
-          if (issued & (1u << s)) mbar_wait(&tail->full[s], phases >> s & 1, tmo);
       }
     }
     if (warp == 1 && lane == 0) {
@@ -301,8 +302,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           unpack_f32x2(sum[i], g0, g1);
           unpack_f32x2(sum[32 + i], u0, u1);
           const bool in = n0 + 2 * i < args.N;  // N is even
-          o[2 * i] = in ? g0 / (1.f + __expf(-g0)) * u0 : 0.f;
-          o[2 * i + 1] = in ? g1 / (1.f + __expf(-g1)) * u1 : 0.f;
+          o[2 * i] = in ? __fdividef(g0, 1.f + __expf(-g0)) * u0 : 0.f;
+          o[2 * i + 1] = in ? __fdividef(g1, 1.f + __expf(-g1)) * u1 : 0.f;
           top = absmax_nan(absmax_nan(top, o[2 * i]), o[2 * i + 1]);
         }
         // The block's 128 features are this thread's and those of the other half's warp;
@@ -361,8 +362,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (SW) {
                 float u0, u1;
                 unpack_f32x2(sum[32 + j * 4 + i], u0, u1);
-                w[2 * i] = w[2 * i] / (1.f + __expf(-w[2 * i])) * u0;
-                w[2 * i + 1] = w[2 * i + 1] / (1.f + __expf(-w[2 * i + 1])) * u1;
+                w[2 * i] = __fdividef(w[2 * i], 1.f + __expf(-w[2 * i])) * u0;
+                w[2 * i + 1] = __fdividef(w[2 * i + 1], 1.f + __expf(-w[2 * i + 1])) * u1;
               }
             }
             if (EPI == F8_RESID) {
@@ -391,22 +392,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag)  // loads in flight land before shared memory goes away
+    for (int s = 0; s < STAGES; ++s)
+      if (issued & (1u << s)) mbar_wait(&tail->full[s], phases >> s & 1, tmo);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
 }
 
-__global__ void take_status_kernel(uint32_t* out) { *out = atomicExch(&g_status, 0u); }
 __device__ uint32_t g_taken;
+__global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0u); }
 
 template <int EPI>
 cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const F8GemmArgs& args, int grid,
                    cudaStream_t stream) {
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(gemm_f8_kernel<EPI>), SMEM);
   if (e != cudaSuccess) return e;
-  gemm_f8_kernel<EPI><<<grid, THREADS, SMEM, stream>>>(tmA, tmB, args);
-  return cudaGetLastError();
+  return launch_dependent(gemm_f8_kernel<EPI>, grid, THREADS, SMEM, stream, tmA, tmB, args);
 }
 
 }  // namespace
@@ -432,7 +435,7 @@ cudaError_t take_gemm_f8_status(uint32_t* bits, cudaStream_t stream) {
   void* at = nullptr;
   cudaError_t e = cudaGetSymbolAddress(&at, g_taken);
   if (e != cudaSuccess) return e;
-  take_status_kernel<<<1, 1, 0, stream>>>(static_cast<uint32_t*>(at));
+  take_status_kernel<<<1, 1, 0, stream>>>();
   e = cudaGetLastError();
   if (e == cudaSuccess) e = cudaMemcpyAsync(bits, at, 4, cudaMemcpyDeviceToHost, stream);
   return e == cudaSuccess ? cudaStreamSynchronize(stream) : e;

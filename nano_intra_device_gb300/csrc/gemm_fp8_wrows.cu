@@ -1,0 +1,544 @@
+// The product of gemm_fp8.cu for few rows of A (a decode step, an expert's few
+// tokens): B's rows are the 128-row operand and A's the N side.
+//
+// Such a product streams B once, 1 byte a value, and is bound by HBM.  So
+//  * a tile is 128 features x TOK rows of A (16, 32, 64 or 128), its ring mostly B;
+//  * the K range is split over the CTAs of a thread-block cluster (up to 8), each
+//    with its own slice of B, and summed through distributed shared memory in rank
+//    order, without workspace and the same at every run;
+//  * two CTAs an SM (at most 113 KB each): one's first loads and last sums run under
+//    the other's stream;
+//  * a block of K has its own accumulator, as in gemm_fp8.cu, but here a thread's row
+//    is a feature and the scale changes from column to column: the products of A's
+//    and B's scales go through a few floats of shared memory a warp;
+//  * the exchange lays the sums out by row of A, 128 features a warp, so that SwiGLU,
+//    the residual and the scale of an 8-bit output are a warp's own.
+// By experts, a grid for the most tiles that the rows can make is launched and the
+// CTAs find their group from the offsets; those past the last tile leave.
+// Launched as a programmatic dependent of the kernel ahead.
+// Every wait is bounded.  After one gave up the CTAs of a cluster still meet at the
+// same exchange and the barrier before exit.
+#include <atomic>
+#include <type_traits>
+
+#include "fp8.cuh"
+#include "kernels.h"
+
+namespace nf {
+namespace {
+
+constexpr int WM = 128, BK = F8_BLOCK;
+constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_STAGES = 8;
+constexpr int TAIL_BYTES = 256;
+
+template <int EPI, int TOK>
+struct Cfg {
+  static constexpr int NA = EPI >= F8_SWIGLU ? 2 : 1;   // operands of B (gate, up)
+  static constexpr int COLS = NA * TOK;                 // columns of an accumulator
+  static constexpr int HALVES = COLS > 64 ? 2 : 1;      // summing warps: 4 a half
+  static constexpr int MINE = COLS / HALVES;            // columns of a thread
+  static constexpr int THREADS = 64 + 128 * HALVES;
+  static constexpr int ACCS = COLS <= 32 ? 4 : 2;       // accumulators, in turn
+  static constexpr int TMEM = ACCS * COLS < 32 ? 32 : ACCS * COLS;
+  static constexpr int STAGE = NA * WM * BK + TOK * BK;
+  static constexpr int SCALES = 4 * HALVES * 2 * MINE * 4;
+  static constexpr int PER_SM = HALVES == 2 ? 1 : 2;     // CTAs
+  static constexpr int LIMIT = PER_SM == 2 ? 115712 : 232448;
+  static constexpr int FIT = (LIMIT - 1024 - TAIL_BYTES - SCALES) / STAGE;
+  static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + SCALES + TAIL_BYTES;
+  static_assert(STAGES >= 2 && SMEM <= LIMIT, "ring");
+  static_assert(COLS * WM * 4 <= STAGES * STAGE, "the exchange reuses the ring");
+  static_assert((TMEM & (TMEM - 1)) == 0 && TMEM <= 512 / PER_SM, "two CTAs' accumulators");
+};
+
+struct Tail {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t tfull[4];
+  uint64_t tempty[4];
+  uint64_t drain;
+  uint64_t ready;  // every rank's sums are in its shared memory
+  uint32_t tmem_base;
+  int abort;
+  int e, m0, m_lim, wt;  // this cluster's tile (m_lim 0: none)
+};
+static_assert(sizeof(Tail) <= TAIL_BYTES, "barrier block");
+
+__device__ uint32_t g_status;
+
+// 32 lanes x 16 columns, as the 32-column form.
+__device__ __forceinline__ void tc_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// The two halves of cluster_sync_all, for threads that diverge in between.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int EPI, int TOK>
+__global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
+    gemm_f8_wrows_kernel(const __grid_constant__ CUtensorMap tmW,
+                         const __grid_constant__ CUtensorMap tmX, const F8GemmArgs args) {
+  using C = Cfg<EPI, TOK>;
+  constexpr int NA = C::NA, STAGES = C::STAGES, MINE = C::MINE, ACCS = C::ACCS;
+  constexpr uint32_t IDESC = idesc_e4m3_f32(WM, TOK);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  float* xbuf = reinterpret_cast<float*>(smem);  // [column][feature], once the ring is done
+  float* scales = reinterpret_cast<float*>(smem + STAGES * C::STAGE);
+  Tail* tail = reinterpret_cast<Tail*>(smem + STAGES * C::STAGE + C::SCALES);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = args.splits, rank = static_cast<int>(cluster_rank());
+  const int unit = static_cast<int>(cluster_id_x());
+  const int nk = (args.K + BK - 1) / BK, nb = (args.N + F8_BLOCK - 1) / F8_BLOCK;
+  const uint64_t tmo = args.timeout_ns;
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->empty[s], 1);
+    }
+    for (int a = 0; a < ACCS; ++a) {
+      mbar_init(&tail->tfull[a], 1);
+      mbar_init(&tail->tempty[a], 4 * C::HALVES);
+    }
+    mbar_init(&tail->drain, 1);
+    mbar_init(&tail->ready, S);
+    tail->abort = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tail->tmem_base, C::TMEM);
+    tmem_relinquish();
+  }
+  pdl_wait();  // nothing before this reads or writes global memory
+  if (warp == 2) {
+    if (!args.group_off) {
+      if (lane == 0) {
+        const int mt = (args.M + TOK - 1) / TOK;
+        tail->e = 0;
+        tail->m0 = unit % mt * TOK;
+        tail->m_lim = args.M;
+        tail->wt = unit / mt;
+      }
+    } else {
+      // The group of this unit; offsets as in gemm_fp8.cu: within [0, M], never falling.
+      int top = 0, tiles = 0;
+      if (lane == 0) tail->m_lim = tail->m0 = tail->e = tail->wt = 0;
+      __syncwarp();
+      for (int b = 0; b <= args.groups; b += 32) {
+        const int i = b + lane;
+        int o = i <= args.groups ? min(max(__ldg(args.group_off + i), 0), args.M) : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, o, d);
+          if (lane >= d) o = max(o, y);
+        }
+        o = max(o, top);
+        const int up = __shfl_up_sync(0xffffffffu, o, 1);
+        const int before = lane ? up : top;
+        const int mt = i > 0 && i <= args.groups ? (o - before + TOK - 1) / TOK : 0;
+        int t = mt * nb;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, t, d);
+          if (lane >= d) t += y;
+        }
+        t += tiles;  // tiles up to and with group i - 1
+        const int u = unit - (t - mt * nb);
+        if (u >= 0 && u < mt * nb) {
+          tail->e = i - 1;
+          tail->m0 = before + u % mt * TOK;
+          tail->m_lim = o;
+          tail->wt = u / mt;
+        }
+        top = __shfl_sync(0xffffffffu, o, 31);
+        tiles = __shfl_sync(0xffffffffu, t, 31);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_arrive();  // this CTA's barriers exist; each thread waits for the peers' further down
+  const uint32_t tmem_base = tail->tmem_base;
+  volatile int* abort_flag = &tail->abort;
+  const int e = tail->e, m0 = tail->m0, m_lim = tail->m_lim, wt = tail->wt;
+  const bool work = m0 < m_lim;  // the same in all CTAs of the cluster
+  const int kb0 = rank * nk / S, klen = work ? (rank + 1) * nk / S - kb0 : 0;
+  // The CTAs start together; each tile begins elsewhere in its K range, so that they do
+  // not all ask for the same columns of B's rows at once.
+  const int rot = klen > 0 ? static_cast<int>(static_cast<long long>(wt) * klen / nb) % klen : 0;
+  auto kb_at = [&](int i) { return kb0 + (i + rot >= klen ? i + rot - klen : i + rot); };
+
+  uint32_t issued = 0, phases = 0;  // thread 0: the ring's stages and the phase of their last load
+  if (warp == 0) {
+    if (lane == 0) {
+      const int w0 = e * NA * args.N + wt * WM;
+      uint32_t st = 0, ph = 0;
+      for (int i = 0; i < klen; ++i) {
+        if (!mbar_wait(&tail->empty[st], ph ^ 1, tmo, abort_flag)) {
+          raise_status(&g_status, ST_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        uint8_t* sa = smem + st * C::STAGE;
+        uint64_t* bar = &tail->full[st];
+        const int kx = kb_at(i) * BK;
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        tma_load_2d(sa, &tmW, bar, kx, w0);
+        if (NA == 2) tma_load_2d(sa + WM * BK, &tmW, bar, kx, w0 + args.N);
+        tma_load_2d(sa + NA * WM * BK, &tmX, bar, kx, m0);
+        issued |= 1u << st;
+        phases = (phases & ~(1u << st)) | ph << st;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t st = 0, ph = 0, acc = 0, aph = 0;
+      for (int i = 0; i < klen; ++i) {
+        if (!mbar_wait(&tail->tempty[acc], aph ^ 1, tmo, abort_flag) ||
+            !mbar_wait(&tail->full[st], ph, tmo, abort_flag)) {
+          raise_status(&g_status, ST_TIMEOUT);
+          *abort_flag = 1;
+          if (i) {  // the products already issued end before tensor memory goes away
+            tc_commit(&tail->drain);
+            mbar_wait(&tail->drain, 0, tmo);
+          }
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem + st * C::STAGE), d = tmem_base + acc * C::COLS;
+        const uint64_t w0 = desc_sw128_kmajor(sa), w1 = desc_sw128_kmajor(sa + WM * BK);
+        const uint64_t xd = desc_sw128_kmajor(sa + NA * WM * BK);
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k) {
+          tc_mma_e4m3(d, w0 + 2 * k, xd + 2 * k, IDESC, k != 0);
+          if (NA == 2) tc_mma_e4m3(d + TOK, w1 + 2 * k, xd + 2 * k, IDESC, k != 0);
+        }
+        tc_commit(&tail->empty[st]);
+        tc_commit(&tail->tfull[acc]);
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (++acc == ACCS) {
+          acc = 0;
+          aph ^= 1;
+        }
+      }
+    }
+  }
+  if (warp < 2 || !work) {
+    cluster_wait();
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int row = quarter * 32 + lane;  // feature of the tile
+    float* sc = scales + (warp - 2) * 2 * MINE;
+    f32x2 sum[MINE / 2];
+#pragma unroll
+    for (int i = 0; i < MINE / 2; ++i) sum[i] = 0;
+    // Column half * MINE + lane + 32 i of the accumulator: its row of A, its operand of B.
+    constexpr int CI = (MINE + 31) / 32, AHEAD = 3;
+    const float* bs = args.b_s + (static_cast<size_t>(e) * NA * nb + wt) * nk;
+    float px[AHEAD + 1][CI], pw[AHEAD + 1][CI];
+    auto fetch = [&](int i, int at) {
+#pragma unroll
+      for (int j = 0; j < CI; ++j) {
+        const int c = half * MINE + lane + 32 * j, t = m0 + c % TOK;
+        const bool on = i < klen && c < C::COLS && t < m_lim;
+        const int kb = i < klen ? kb_at(i) : 0;
+        px[at][j] = on ? __ldg(args.a_s + static_cast<size_t>(kb) * args.M + t) : 0.f;
+        pw[at][j] = on ? __ldg(bs + (c / TOK) * static_cast<size_t>(nb) * nk + kb) : 0.f;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(i, i);
+    uint32_t acc = 0, aph = 0;
+    bool ok = true;
+    for (int i = 0; i < klen; ++i) {
+      fetch(i + AHEAD, AHEAD);
+      float* p = sc + (i & 1) * MINE;
+#pragma unroll
+      for (int j = 0; j < CI; ++j)
+        if (lane + 32 * j < MINE) p[lane + 32 * j] = px[0][j] * pw[0][j];
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+        for (int j = 0; j < CI; ++j) {
+          px[a][j] = px[a + 1][j];
+          pw[a][j] = pw[a + 1][j];
+        }
+      // also makes p visible to the warp; it is overwritten two rounds later, behind the
+      // next round's vote
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&tail->tfull[acc], aph, tmo, abort_flag));
+      if (!ok) break;
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * C::COLS + half * MINE;
+      uint32_t v[MINE / 16 > 1 ? 2 : 1][16];
+      tc_ld_x16(tb, v[0]);
+#pragma unroll
+      for (int c = 0; c < MINE / 16; ++c) {
+        tc_wait_ld();
+        if (c + 1 < MINE / 16) {
+          tc_ld_x16(tb + 16 * (c + 1), v[(c + 1) & 1]);
+        } else {
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&tail->tempty[acc]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 s = *reinterpret_cast<const float4*>(p + 16 * c + 4 * j);
+          fma_f32x2(sum[8 * c + 2 * j], pack_b32x2(v[c & 1][4 * j], v[c & 1][4 * j + 1]), pack_f32x2(s.x, s.y));
+          fma_f32x2(sum[8 * c + 2 * j + 1], pack_b32x2(v[c & 1][4 * j + 2], v[c & 1][4 * j + 3]), pack_f32x2(s.z, s.w));
+        }
+      }
+      if (++acc == ACCS) {
+        acc = 0;
+        aph ^= 1;
+      }
+    }
+    if (!ok) {
+      raise_status(&g_status, ST_TIMEOUT);
+      *abort_flag = 1;
+    }
+    // The exchange: this CTA's sums to its shared memory (every product that read the
+    // ring has completed), then each rank adds all ranks' for its share of the rows.
+    // After a failure the ring may still be written: nothing is stored.
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < MINE / 2; ++j) {
+        float a, b;
+        unpack_f32x2(sum[j], a, b);
+        xbuf[(half * MINE + 2 * j) * WM + row] = a;
+        xbuf[(half * MINE + 2 * j + 1) * WM + row] = b;
+      }
+    }
+    cluster_wait();  // every peer's barriers exist
+    asm volatile("bar.sync 1, %0;" ::"n"(128 * C::HALVES) : "memory");
+    if (warp == 2 && lane == 0) {
+      fence_acq_rel_cluster();
+      const uint32_t at = smem_u32(&tail->ready);
+      for (int j = 0; j < S; ++j) mbar_arrive_remote(cluster_map(at, j));
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo))) {
+      raise_status(&g_status, ST_TIMEOUT);
+      *abort_flag = 1;
+    } else {
+      const int nv = min(TOK, m_lim - m0);
+      const int c0 = rank * nv / S, c1 = (rank + 1) * nv / S;
+      const int n = wt * WM + lane * 4;  // a lane's 4 features
+      const bool in = n < args.N;
+      const uint32_t xa = smem_u32(xbuf) + lane * 16;
+      for (int c = c0 + (warp - 2); c < c1; c += 4 * C::HALVES) {
+        const size_t t = static_cast<size_t>(m0 + c);
+        uint2 r = make_uint2(0u, 0u);
+        if (EPI == F8_RESID && in) r = __ldg(reinterpret_cast<const uint2*>(args.R + t * args.N + n));
+        float4 v0[MAX_CLUSTER], v1[MAX_CLUSTER];
+#pragma unroll
+        for (int j = 0; j < MAX_CLUSTER; ++j) {
+          if (j < S) {
+            const uint32_t at = cluster_map(xa, j) + c * (WM * 4);
+            v0[j] = ld_cluster_f4(at);
+            if (NA == 2) v1[j] = ld_cluster_f4(at + TOK * WM * 4);
+          }
+        }
+        float o[4] = {}, u[4] = {};
+#pragma unroll
+        for (int j = 0; j < MAX_CLUSTER; ++j) {
+          if (j < S) {
+            o[0] += v0[j].x; o[1] += v0[j].y; o[2] += v0[j].z; o[3] += v0[j].w;
+            if (NA == 2) {
+              u[0] += v1[j].x; u[1] += v1[j].y; u[2] += v1[j].z; u[3] += v1[j].w;
+            }
+          }
+        }
+        if (NA == 2) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = in ? __fdividef(o[k], 1.f + __expf(-o[k])) * u[k] : 0.f;
+        }
+        if (EPI == F8_RESID) {
+          o[0] += bf16lo(r.x); o[1] += bf16hi(r.x); o[2] += bf16lo(r.y); o[3] += bf16hi(r.y);
+        }
+        if (EPI == F8_SWIGLU8) {
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = absmax_nan(top, o[k]);
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) top = absmax_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const float s = f8_scale(top), inv = 1.f / s;
+          if (in) *reinterpret_cast<uint32_t*>(args.q + t * args.N + n) = f8_codes4(o[0], o[1], o[2], o[3], s, inv);
+          if (lane == 0) args.c_s[static_cast<size_t>(wt) * args.M + t] = s;
+        } else if (in) {
+          *reinterpret_cast<uint2*>(args.C + t * args.N + n) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag)  // loads in flight land before shared memory goes away
+    for (int s = 0; s < STAGES; ++s)
+      if (issued & (1u << s)) mbar_wait(&tail->full[s], phases >> s & 1, tmo);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM);
+  }
+  cluster_arrive();
+  cluster_wait();  // no CTA leaves while a peer may still read its sums
+}
+
+__device__ uint32_t g_taken;
+__global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0u); }
+
+template <int EPI, int TOK>
+void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, int clusters, int splits, cudaStream_t stream) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3(static_cast<unsigned>(clusters * splits), 1, 1);
+  cfg->blockDim = dim3(Cfg<EPI, TOK>::THREADS, 1, 1);
+  cfg->dynamicSmemBytes = Cfg<EPI, TOK>::SMEM;
+  cfg->stream = stream;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  // its barriers and tensor memory are made while the kernel ahead ends
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = at;
+  cfg->numAttrs = 2;
+}
+
+template <int EPI, int TOK>
+cudaError_t prepare() {
+  return set_smem_limit(reinterpret_cast<const void*>(gemm_f8_wrows_kernel<EPI, TOK>), Cfg<EPI, TOK>::SMEM);
+}
+
+template <int EPI, int TOK>
+cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const F8GemmArgs& args, int clusters,
+                   cudaStream_t stream) {
+  const cudaError_t e = prepare<EPI, TOK>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute at[2];
+  configure<EPI, TOK>(&cfg, at, clusters, args.splits, stream);
+  return cudaLaunchKernelEx(&cfg, gemm_f8_wrows_kernel<EPI, TOK>, tmW, tmX, args);
+}
+
+// Clusters of `splits` CTAs that the device holds at once; asked once a process.
+template <int EPI, int TOK>
+int most_clusters(int splits) {
+  static std::atomic<int> cache[MAX_CLUSTER + 1];
+  int n = cache[splits].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute at[2];
+    configure<EPI, TOK>(&cfg, at, 1, splits, nullptr);
+    cfg.numAttrs = 1;
+    if (prepare<EPI, TOK>() != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gemm_f8_wrows_kernel<EPI, TOK>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;
+    }
+    cache[splits].store(n, std::memory_order_relaxed);
+  }
+  return n > 0 ? n : 0;
+}
+
+// f(epilogue, rows of A of a tile) with both as compile-time constants; -1 for others.
+template <typename F>
+int dispatch(int epi, int tok, F f) {
+  using std::integral_constant;
+  auto at = [&](auto e) {
+    switch (tok) {
+      case 16: return f(e, integral_constant<int, 16>{});
+      case 32: return f(e, integral_constant<int, 32>{});
+      case 64: return f(e, integral_constant<int, 64>{});
+      case 128:
+        if constexpr (F8_SWIGLU > decltype(e)::value) return f(e, integral_constant<int, 128>{});
+      default: return -1;
+    }
+  };
+  switch (epi) {
+    case F8_STORE: return at(integral_constant<int, F8_STORE>{});
+    case F8_RESID: return at(integral_constant<int, F8_RESID>{});
+    case F8_SWIGLU: return at(integral_constant<int, F8_SWIGLU>{});
+    case F8_SWIGLU8: return at(integral_constant<int, F8_SWIGLU8>{});
+    default: return -1;
+  }
+}
+
+}  // namespace
+
+F8RowsChoice gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups) {
+  F8RowsChoice c{};
+  const int rows = (M + groups - 1) / groups;  // of a group, were they even
+  const int most = epi >= F8_SWIGLU ? 64 : 128;
+  // by groups: room for twice the mean, as B is read again for each further tile
+  const int want = groups > 1 ? 2 * rows : rows;
+  c.tok = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 || most == 64 ? 64 : 128;
+  const long long wt = (N + WM - 1) / WM;
+  c.units = groups > 1 ? wt * (M / c.tok + (M < groups ? M : groups)) : wt * ((M + c.tok - 1) / c.tok);
+  // As many CTAs as the device holds at once, but four blocks of K each at least.
+  const long long busy = wt * (groups > 1 ? (M < groups ? M : groups) : (M + c.tok - 1) / c.tok);
+  const int nk = (K + BK - 1) / BK;
+  c.splits = 1;
+  for (int s = 2; s <= MAX_CLUSTER && 4 * s <= nk; ++s)
+    if (busy <= dispatch(epi, c.tok, [&](auto e, auto k) { return most_clusters<decltype(e)::value, decltype(k)::value>(s); }))
+      c.splits = s;
+  return c;
+}
+
+cudaError_t launch_gemm_f8_wrows(int epi, int tok, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                                 const F8GemmArgs& args, long long units, cudaStream_t stream) {
+  if (units <= 0) return cudaSuccess;
+  if (args.splits < 1 || args.splits > MAX_CLUSTER || units * args.splits > 0x7fffffffLL)
+    return cudaErrorInvalidValue;
+  const int e = dispatch(epi, tok, [&](auto e, auto k) {
+    return static_cast<int>(launch<decltype(e)::value, decltype(k)::value>(tmW, tmX, args, static_cast<int>(units), stream));
+  });
+  return e < 0 ? cudaErrorInvalidValue : static_cast<cudaError_t>(e);
+}
+
+cudaError_t take_gemm_f8_wrows_status(uint32_t* bits, cudaStream_t stream) {
+  void* at = nullptr;
+  cudaError_t e = cudaGetSymbolAddress(&at, g_taken);
+  if (e != cudaSuccess) return e;
+  take_status_kernel<<<1, 1, 0, stream>>>();
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, at, 4, cudaMemcpyDeviceToHost, stream);
+  return e == cudaSuccess ? cudaStreamSynchronize(stream) : e;
+}
+
+}  // namespace nf
