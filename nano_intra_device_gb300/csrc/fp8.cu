@@ -77,7 +77,8 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
   if (few) c = nf::gemm_f8_wrows_choice(epilogue, M, N, K, groups);
   CUtensorMap ta, tb;
   if (!nf::make_tmap_8bit(&ta, A, M, K, few ? c.tok : 128) ||
-      !nf::make_tmap_8bit(&tb, B, static_cast<uint64_t>(groups) * N * (two ? 2 : 1), K, 128))
+      !nf::make_tmap_8bit(&tb, B, static_cast<uint64_t>(groups) * N * (two ? 2 : 1), K,
+                          two && !few ? 64 : 128))
     return fail8(NF_ERR_CUDA, "tensor map creation failed");
   nf::F8GemmArgs g{};
   g.M = M;

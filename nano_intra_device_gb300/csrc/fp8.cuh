@@ -23,6 +23,14 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// One lane of a converged warp.  Products are issued under it rather than under
+// `lane == 0`: their operands, computed by the whole warp, then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Two fp32 values a register pair: one instruction for both.  Volatile: an
 // accumulator read from tensor memory must not be used ahead of the wait for it.
 typedef unsigned long long f32x2;
@@ -41,6 +49,28 @@ __device__ __forceinline__ void unpack_f32x2(f32x2 v, float& a, float& b) {
 }
 __device__ __forceinline__ void fma_f32x2(f32x2& d, f32x2 a, f32x2 b) {
   asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+// One arrival of the lanes for which `yes` holds, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool yes) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(yes ? 1u : 0u)
+      : "memory");
+}
+// 4 bytes global -> shared (zeros where not `there`), and an arrival on an mbarrier once
+// this thread's copies so far have landed.
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// d += a b, a a value read from tensor memory.
+__device__ __forceinline__ void fma_loaded(float& d, uint32_t a, float b) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "f"(__uint_as_float(a)), "f"(b));
 }
 
 // The larger magnitude; a NaN on either side stays.
@@ -71,6 +101,23 @@ __device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
+}
+
+// The same for values that are themselves rounded, by the product with inv alone: off
+// the nearest code where the quotient lies within 2^-22 of a border, as the values do.
+__device__ __forceinline__ uint32_t f8_codes4_near(float a, float b, float c, float d, float inv) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+// silu(g) u = g u / (1 + 2^(-g log2 e)): exponential and reciprocal by the hardware's
+// approximations (2 and 1 units in the last place).  A g below -126 ln 2 gives zero, as
+// the reciprocal of anything above 2^126 does; infinite g: NaN or g u.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return g * r * u;
 }
 
 // A launch as a programmatic dependent of the stream's kernel ahead: the kernel may

@@ -44,7 +44,8 @@ struct F8GemmArgs {
   int splits;            // few rows: CTAs of a cluster, which split K
   unsigned long long timeout_ns;
 };
-// tmA: the rows of A, tmB: all groups' rows of B, both in boxes of 128 rows x 128 columns.
+// tmA: the rows of A in boxes of 128 rows, tmB: all groups' rows of B in boxes of 128
+// (SwiGLU: 64) rows, x 128 columns.
 cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& tmB,
                            const F8GemmArgs& args, int sms, cudaStream_t stream);
 // The bits that the kernels of launch_gemm_f8 raised on the current device, and zeros

@@ -6,12 +6,12 @@
 //  * A tile is 128 rows of A x 256 rows of B (SwiGLU: 128 features' gate and up rows),
 //    so a thread's row has one scale of A and a warp's columns one or two of B a
 //    block of K.  A ring stage is one block of K: 128 bytes a row, one swizzled row.
-//  * Scales are fp32 and change with every block of K, so a block's products go to an
-//    accumulator of their own in tensor memory (two, in turn), and eight warps
-//    add it, times its scale, to sums in registers (fp32, packed in pairs): while they
-//    do, the tensor core fills the other accumulator.
-//  * Warp 0 loads tiles by TMA, warp 1 issues the products, warps 4 to 11 sum and run
-//    the epilogue.  Persistent CTAs, one an SM.
+//  * Scales are fp32 and change with every block of K, so a block's products go to
+//    accumulators of their own in tensor memory (two, in turn, for each half of the
+//    columns), and eight warps, four a half, add them, times their scale, to sums in
+//    registers.  While they do, the tensor core fills the other accumulators.
+//  * Warp 0 loads tiles by TMA, warps 1 and 2 issue the products of a half each, warp 3
+//    copies the scales beside the tiles, warps 4 to 11 sum and run the epilogue.  Persistent CTAs, one an SM.
 //  * Every wait is bounded; one that gives up flags the status word, and the kernel
 //    drains what it has in flight (bounded) and frees tensor memory.
 #include "fp8.cuh"
@@ -28,22 +28,26 @@ constexpr int THREADS = 384;
 // the summing warps take 208: 4 * 32 * 72 + 8 * 32 * 208 = 62,464.
 constexpr int REGS_FEW = 72, REGS_SUM = 208;
 constexpr int TMEM_COLS = 512;
-constexpr int STORE_BYTES = 8 * 4096;  // 32 rows x 64 columns of bf16 a warp
-constexpr int TAIL_BYTES = 1280;
+constexpr int STORE_BYTES = 2048;  // of a summing warp: 32 rows x 64 bytes of output
+constexpr int TAIL_BYTES = 8192;
 
 struct Tail {
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
-  uint64_t tfull[2];
-  uint64_t tempty[2];
-  uint64_t pair[4];  // the two warps of 32 rows (SWIGLU8: the block's largest value)
-  uint64_t drain;
+  uint64_t tfull[4];   // accumulators: half h of the columns, in turn 2 h and 2 h + 1
+  uint64_t tempty[4];
+  uint64_t pair[4];    // the two warps of 32 rows (SWIGLU8: the block's largest value)
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
   int tile0[F8_MAX_GROUPS + 1];  // first tile of each group
   int row0[F8_MAX_GROUPS + 1];   // first row of each group
+  uint64_t sfull[8];
+  float a_s[8][BM];       // scales of the next blocks of K: of A's rows,
+  float b_s[8][2];        // and of B's halves (SwiGLU: of gate and up)
+  float top[2][8][32];    // SWIGLU8: by tile parity and warp, a row's largest value
 };
-constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + STORE_BYTES + TAIL_BYTES;
+constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 8 * STORE_BYTES + TAIL_BYTES;
 static_assert(sizeof(Tail) <= TAIL_BYTES && SMEM <= 232448, "shared memory");
 
 __device__ uint32_t g_status;
@@ -58,11 +62,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                    const F8GemmArgs args) {
   constexpr bool SW = EPI == F8_SWIGLU || EPI == F8_SWIGLU8;
   constexpr int TN = SW ? BN / 2 : BN;  // output columns of a tile
-  constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BN);
+  constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BN / 2);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  Tail* tail = reinterpret_cast<Tail*>(smem + STAGES * STAGE_BYTES + STORE_BYTES);
+  Tail* tail = reinterpret_cast<Tail*>(smem + STAGES * STAGE_BYTES + 8 * STORE_BYTES);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nk = (args.K + BK - 1) / BK, n_tiles = (args.N + TN - 1) / TN;
@@ -74,14 +78,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&tail->full[s], 1);
-      mbar_init(&tail->empty[s], 1);
+      mbar_init(&tail->empty[s], 2);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < 4; ++a) {
       mbar_init(&tail->tfull[a], 1);
-      mbar_init(&tail->tempty[a], 8);
+      mbar_init(&tail->tempty[a], 4);
     }
+    for (int a = 0; a < 2; ++a) mbar_init(&tail->drain[a], 1);
+    for (int a = 0; a < 8; ++a) mbar_init(&tail->sfull[a], 32);
     for (int a = 0; a < 4; ++a) mbar_init(&tail->pair[a], 2);
-    mbar_init(&tail->drain, 1);
     tail->abort = 0;
     fence_mbar_init();
     prefetch_tensormap(&tmA);
@@ -170,8 +175,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint64_t* bar = &tail->full[st];
           mbar_arrive_expect_tx(bar, STAGE_BYTES);
           tma_load_2d(sa, &tmA, bar, kb * BK, x.m0);
-          tma_load_2d(sa + A_BYTES, &tmB, bar, kb * BK, b0);
-          tma_load_2d(sa + A_BYTES + B_BYTES / 2, &tmB, bar, kb * BK, b1);
+          if (SW) {  // a half of the columns: 64 features' gate rows, then their up rows
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tma_load_2d(sa + A_BYTES + i * (B_BYTES / 4), &tmB, bar, kb * BK, (i & 1 ? b1 : b0) + (i >> 1) * 64);
+          } else {
+            tma_load_2d(sa + A_BYTES, &tmB, bar, kb * BK, b0);
+            tma_load_2d(sa + A_BYTES + B_BYTES / 2, &tmB, bar, kb * BK, b1);
+          }
           issued |= 1u << st;
           phases = (phases & ~(1u << st)) | ph << st;
           if (++st == STAGES) {
@@ -185,25 +196,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         *abort_flag = 1;
       }
     }
-    if (warp == 1 && lane == 0) {
+    if (warp == 1 || warp == 2) {
+      const int h = warp - 1;
+      const bool one = elect_one();
       uint32_t st = 0, ph = 0, acc = 0, aph = 0;
       bool ok = true, any = false;
       for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+#pragma unroll 1
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&tail->tempty[acc], aph ^ 1, tmo, abort_flag) ||
-              !mbar_wait(&tail->full[st], ph, tmo, abort_flag)) {
-            ok = false;
-            break;
-          }
+          // (the stage is there long before the accumulator is free)
+          const uint32_t sa = smem_u32(smem + st * STAGE_BYTES), d = tmem_base + (2 * h + acc) * (BN / 2);
+          const uint64_t ad = desc_sw128_kmajor(sa), bd = desc_sw128_kmajor(sa + A_BYTES + h * (B_BYTES / 2));
+          ok = __all_sync(0xffffffffu, mbar_wait(&tail->full[st], ph, tmo, abort_flag) &&
+                                           mbar_wait(&tail->tempty[2 * h + acc], aph ^ 1, tmo, abort_flag)) != 0;
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + st * STAGE_BYTES);
-          const uint64_t ad = desc_sw128_kmajor(sa), bd = desc_sw128_kmajor(sa + A_BYTES);
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < BK / 32; ++k)  // 32 codes = 32 bytes along the swizzled row
-            tc_mma_e4m3(tmem_base + acc * BN, ad + 2 * k, bd + 2 * k, IDESC, k != 0);
+            for (int k = 0; k < BK / 32; ++k)  // 32 codes = 32 bytes along the swizzled row
+              tc_mma_e4m3(d, ad + 2 * k, bd + 2 * k, IDESC, k != 0);
+            tc_commit(&tail->tfull[2 * h + acc]);
+            tc_commit(&tail->empty[st]);
+          }
           any = true;
-          tc_commit(&tail->empty[st]);
-          tc_commit(&tail->tfull[acc]);
           if (++st == STAGES) {
             st = 0;
             ph ^= 1;
@@ -214,157 +229,162 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      if (!ok) {
+      if (!ok && one) {
         raise_status(&g_status, ST_TIMEOUT);
         *abort_flag = 1;
         if (any) {  // the products already issued end before tensor memory goes away
-          tc_commit(&tail->drain);
-          mbar_wait(&tail->drain, 0, tmo);
+          tc_commit(&tail->drain[h]);
+          mbar_wait(&tail->drain[h], 0, tmo);
         }
       }
+    }
+    if (warp == 3) {
+      // Scales, copied beside the tiles: a slot is filled again 8 blocks of K later, when
+      // the stage's products of 4 blocks before are done, so the sums of 2 further before.
+      uint32_t st = 0, ph = 0, slot = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        const Tile x = decode(u);
+        const int b0 = SW ? x.tn : min(2 * x.tn, nb - 1), b1 = SW ? nb + x.tn : min(2 * x.tn + 1, nb - 1);
+        const float* as = args.a_s + x.m0 + lane;
+        const float* bs = args.b_s + (static_cast<size_t>(x.e) * (SW ? 2 : 1) * nb + (lane ? b1 : b0)) * nk;
+        const int rows = x.m_lim - x.m0 - lane;  // row 32 i of this lane's is there below it
+#pragma unroll 1
+        for (int kb = 0; kb < nk; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&tail->empty[st], ph ^ 1, tmo, abort_flag)) != 0;
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) copy4(&tail->a_s[slot][lane + 32 * i], rows > 32 * i ? as + 32 * i : args.a_s, rows > 32 * i);
+          if (lane < 2) copy4(&tail->b_s[slot][lane], bs + kb, true);
+          mbar_arrive_copied(&tail->sfull[slot]);
+          as += args.M;
+          slot = (slot + 1) % 8;
+          if (++st == STAGES) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        raise_status(&g_status, ST_TIMEOUT);
+        *abort_flag = 1;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SUM));
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int row_in_tile = quarter * 32 + lane;
-    // This thread's columns of the accumulator: chunks of 32 from col(c).  SwiGLU: 64
-    // features' gate columns, then the same features' up columns.
-    auto col = [&](int c) { return SW ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32; };
-    uint8_t* mine = smem + STAGES * STAGE_BYTES + (warp - 4) * 4096;
-    uint32_t acc = 0, aph = 0, parity = 0, pph = 0;
+    uint8_t* mine = smem + STAGES * STAGE_BYTES + (warp - 4) * STORE_BYTES;
+    // 16-byte chunk j of row r of the warp's 2 KB, so placed that rows are written and
+    // read eight lanes at a time without bank conflicts
+    auto slot = [&](int r, int j) { return reinterpret_cast<uint4*>(mine + r * 64 + ((j ^ (r >> 1 & 3)) << 4)); };
+    uint32_t acc = 0, aph = 0, parity = 0, slot8 = 0, sph = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const Tile x = decode(u);
-      const int m = x.m0 + row_in_tile;
-      const bool row_ok = m < x.m_lim;
-      const int blk = SW ? x.tn : min(2 * x.tn + half, nb - 1);
-      const float* bs0 = args.b_s + (static_cast<size_t>(x.e) * (SW ? 2 : 1) * nb + blk) * nk;
-      const float* bs1 = SW ? bs0 + static_cast<size_t>(nb) * nk : bs0;
-      const float* as = args.a_s + m;
-      f32x2 sum[64];
+      // This thread's sums: 128 columns of its half (SwiGLU: 64 features' gate columns,
+      // then their up columns).
+      float sum[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) sum[i] = 0;
-      // scales, two blocks of K ahead of their use
-      float sa[3], sb[3], sc[3];
-      auto scales = [&](int kb, int i) {
-        const bool on = kb < nk;
-        sa[i] = on && row_ok ? __ldg(as + static_cast<size_t>(kb) * args.M) : 0.f;
-        sb[i] = on ? __ldg(bs0 + kb) : 0.f;
-        if (SW) sc[i] = on ? __ldg(bs1 + kb) : 0.f;
-      };
-      scales(0, 0);
-      scales(1, 1);
+      for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+#pragma unroll 1
       for (int kb = 0; kb < nk; ++kb) {
-        scales(kb + 2, 2);
-        if (!__all_sync(0xffffffffu, mbar_wait(&tail->tfull[acc], aph, tmo, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&tail->sfull[slot8], sph, tmo, abort_flag) &&
+                                         mbar_wait(&tail->tfull[2 * half + acc], aph, tmo, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const float s0 = sa[0] * sb[0], s1 = SW ? sa[0] * sc[0] : s0;
-        const f32x2 p0 = pack_f32x2(s0, s0), p1 = pack_f32x2(s1, s1);
-        const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (2 * half + acc) * (BN / 2);
         uint32_t v[2][32];
-        tc_ld_32x32b_x32(tb + col(0), v[0]);
+        auto add = [&](int c, float s) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tc_wait_ld();
-          if (c < 3) {
-            tc_ld_32x32b_x32(tb + col(c + 1), v[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            if (lane == 0) mbar_arrive(&tail->tempty[acc]);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            fma_f32x2(sum[c * 16 + i], pack_b32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), c < 2 ? p0 : p1);
+          for (int i = 0; i < 32; ++i) fma_loaded(sum[c * 32 + i], v[c & 1][i], s);
+        };
+        tc_ld_32x32b_x32(tb, v[0]);
+        tc_ld_32x32b_x32(tb + 32, v[1]);
+        const float as = tail->a_s[slot8][row_in_tile];
+        const float s0 = as * tail->b_s[slot8][SW ? 0 : half], s1 = SW ? as * tail->b_s[slot8][1] : s0;
+        if (++slot8 == 8) {
+          slot8 = 0;
+          sph ^= 1;
         }
-        sa[0] = sa[1]; sa[1] = sa[2];
-        sb[0] = sb[1]; sb[1] = sb[2];
-        sc[0] = sc[1]; sc[1] = sc[2];
+        tc_wait_ld();
+        add(0, s0);
+        tc_ld_32x32b_x32(tb + 64, v[0]);
+        add(1, s0);
+        tc_ld_32x32b_x32(tb + 96, v[1]);
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(&tail->tempty[2 * half + acc], lane == 0);
+        add(2, s1);
+        add(3, s1);
         if (++acc == 2) {
           acc = 0;
           aph ^= 1;
         }
       }
       if (!ok) break;
-      // Epilogue, through the warp's own 4 KB: 32 rows x 128 bytes, 16-byte chunk j of
-      // row r at chunk j ^ (r & 7), so that rows are written and 128-byte lines stored
-      // without bank conflicts.
-      auto slot = [&](int r, int j) { return reinterpret_cast<uint4*>(mine + r * 128 + ((j ^ (r & 7)) << 4)); };
+      // Epilogue, 64 bytes of each of the warp's 32 rows at a time through its 2 KB.
+      const Tile x = decode(u);
       const int mw = x.m0 + quarter * 32;  // first row of this warp
       if (EPI == F8_SWIGLU8) {
         const int n0 = x.tn * TN + half * 64;
         float o[64], top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float g0, g1, u0, u1;
-          unpack_f32x2(sum[i], g0, g1);
-          unpack_f32x2(sum[32 + i], u0, u1);
-          const bool in = n0 + 2 * i < args.N;  // N is even
-          o[2 * i] = in ? __fdividef(g0, 1.f + __expf(-g0)) * u0 : 0.f;
-          o[2 * i + 1] = in ? __fdividef(g1, 1.f + __expf(-g1)) * u1 : 0.f;
-          top = absmax_nan(absmax_nan(top, o[2 * i]), o[2 * i + 1]);
+        for (int i = 0; i < 64; ++i) {
+          o[i] = n0 + i < args.N ? silu_mul(sum[i], sum[64 + i]) : 0.f;
+          top = absmax_nan(top, o[i]);
         }
-        // The block's 128 features are this thread's and those of the other half's warp;
-        // the codes take 2 KB of a warp's 4, so the largest values fit behind them.
-        auto top_at = [&](int w) {
-          return reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES + w * 4096 + 2048 + parity * 128);
-        };
-        top_at(warp - 4)[lane] = top;
+        // the block's 128 features are this thread's and those of the other half's warp
+        tail->top[parity][warp - 4][lane] = top;
         __syncwarp();
         if (lane == 0) mbar_arrive(&tail->pair[quarter]);
-        if (!__all_sync(0xffffffffu, mbar_wait(&tail->pair[quarter], pph, tmo, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&tail->pair[quarter], parity, tmo, abort_flag))) {
           ok = false;
           break;
         }
-        top = absmax_nan(top, top_at((warp - 4) ^ 4)[lane]);
+        top = absmax_nan(top, tail->top[parity][(warp - 4) ^ 4][lane]);
         parity ^= 1;
-        pph ^= 1;
         const float s = f8_scale(top), inv = 1.f / s;
-        auto slot8 = [&](int r, int j) { return reinterpret_cast<uint4*>(mine + r * 64 + ((j ^ (r >> 1 & 3)) << 4)); };
-        if (half == 0 && row_ok) args.c_s[static_cast<size_t>(x.tn) * args.M + m] = s;
+        if (half == 0 && mw + lane < x.m_lim) args.c_s[static_cast<size_t>(x.tn) * args.M + mw + lane] = s;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float* w = o + 16 * j;
-          *slot8(lane, j) = make_uint4(f8_codes4(w[0], w[1], w[2], w[3], s, inv), f8_codes4(w[4], w[5], w[6], w[7], s, inv),
-                                      f8_codes4(w[8], w[9], w[10], w[11], s, inv), f8_codes4(w[12], w[13], w[14], w[15], s, inv));
+          *slot(lane, j) = make_uint4(f8_codes4_near(w[0], w[1], w[2], w[3], inv), f8_codes4_near(w[4], w[5], w[6], w[7], inv),
+                                      f8_codes4_near(w[8], w[9], w[10], w[11], inv), f8_codes4_near(w[12], w[13], w[14], w[15], inv));
         }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = i * 8 + lane / 4, j = lane % 4, n = n0 + 16 * j;
           if (mw + r < x.m_lim && n < args.N)
-            *reinterpret_cast<uint4*>(args.q + static_cast<size_t>(mw + r) * args.N + n) = *slot8(r, j);
+            *reinterpret_cast<uint4*>(args.q + static_cast<size_t>(mw + r) * args.N + n) = *slot(r, j);
         }
         __syncwarp();
       } else {
 #pragma unroll
-        for (int h = 0; h < (SW ? 1 : 2); ++h) {
-          const int n0 = SW ? x.tn * TN + half * 64 : x.tn * TN + half * 128 + h * 64;
+        for (int h = 0; h < (SW ? 2 : 4); ++h) {
+          const int n0 = x.tn * TN + half * (TN / 2) + h * 32;
           if (EPI == F8_RESID) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = i * 4 + lane / 8, j = lane % 8, n = n0 + 8 * j;
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + lane / 4, j = lane % 4, n = n0 + 8 * j;
               uint4 w = make_uint4(0u, 0u, 0u, 0u);
               if (mw + r < x.m_lim && n < args.N)
-                w = __ldg(reinterpret_cast<const uint4*>(args.R + static_cast<size_t>(mw + r) * args.N + n));
+                w = *reinterpret_cast<const uint4*>(args.R + static_cast<size_t>(mw + r) * args.N + n);  // C may be R
               *slot(r, j) = w;
             }
             __syncwarp();
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             float w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              unpack_f32x2(sum[h * 32 + j * 4 + i], w[2 * i], w[2 * i + 1]);
-              if (SW) {
-                float u0, u1;
-                unpack_f32x2(sum[32 + j * 4 + i], u0, u1);
-                w[2 * i] = __fdividef(w[2 * i], 1.f + __expf(-w[2 * i])) * u0;
-                w[2 * i + 1] = __fdividef(w[2 * i + 1], 1.f + __expf(-w[2 * i + 1])) * u1;
-              }
+            for (int i = 0; i < 8; ++i) {
+              w[i] = sum[h * 32 + j * 8 + i];
+              if (SW) w[i] = silu_mul(w[i], sum[64 + h * 32 + j * 8 + i]);
             }
             if (EPI == F8_RESID) {
               const uint4 r = *slot(lane, j);
@@ -375,8 +395,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + lane / 8, j = lane % 8, n = n0 + 8 * j;
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + lane / 4, j = lane % 4, n = n0 + 8 * j;
             if (mw + r < x.m_lim && n < args.N)
               *reinterpret_cast<uint4*>(args.C + static_cast<size_t>(mw + r) * args.N + n) = *slot(r, j);
           }

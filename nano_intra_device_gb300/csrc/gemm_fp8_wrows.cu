@@ -268,9 +268,9 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
 #pragma unroll
     for (int i = 0; i < MINE / 2; ++i) sum[i] = 0;
     // Column half * MINE + lane + 32 i of the accumulator: its row of A, its operand of B.
-    constexpr int CI = (MINE + 31) / 32, AHEAD = 3;
+    constexpr int CI = (MINE + 31) / 32, AHEAD = 4;
     const float* bs = args.b_s + (static_cast<size_t>(e) * NA * nb + wt) * nk;
-    float px[AHEAD + 1][CI], pw[AHEAD + 1][CI];
+    float px[AHEAD][CI], pw[AHEAD][CI];  // a ring, in place, as in gemm_fp8.cu
     auto fetch = [&](int i, int at) {
 #pragma unroll
       for (int j = 0; j < CI; ++j) {
@@ -285,23 +285,15 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     for (int i = 0; i < AHEAD; ++i) fetch(i, i);
     uint32_t acc = 0, aph = 0;
     bool ok = true;
-    for (int i = 0; i < klen; ++i) {
-      fetch(i + AHEAD, AHEAD);
-      float* p = sc + (i & 1) * MINE;
+    auto block = [&](int i, int at) {
+      float* p = sc + (at & 1) * MINE;
 #pragma unroll
       for (int j = 0; j < CI; ++j)
-        if (lane + 32 * j < MINE) p[lane + 32 * j] = px[0][j] * pw[0][j];
-#pragma unroll
-      for (int a = 0; a < AHEAD; ++a)
-#pragma unroll
-        for (int j = 0; j < CI; ++j) {
-          px[a][j] = px[a + 1][j];
-          pw[a][j] = pw[a + 1][j];
-        }
+        if (lane + 32 * j < MINE) p[lane + 32 * j] = px[at][j] * pw[at][j];
+      fetch(i + AHEAD, at);
       // also makes p visible to the warp; it is overwritten two rounds later, behind the
       // next round's vote
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(&tail->tfull[acc], aph, tmo, abort_flag));
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&tail->tfull[acc], aph, tmo, abort_flag))) return false;
       __syncwarp();
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * C::COLS + half * MINE;
@@ -327,7 +319,13 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
         acc = 0;
         aph ^= 1;
       }
-    }
+      return true;
+    };
+#pragma unroll 1
+    for (int i = 0; i < klen && ok; i += AHEAD)
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+        if (ok && i + j < klen) ok = block(i + j, j);
     if (!ok) {
       raise_status(&g_status, ST_TIMEOUT);
       *abort_flag = 1;
@@ -363,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       for (int c = c0 + (warp - 2); c < c1; c += 4 * C::HALVES) {
         const size_t t = static_cast<size_t>(m0 + c);
         uint2 r = make_uint2(0u, 0u);
-        if (EPI == F8_RESID && in) r = __ldg(reinterpret_cast<const uint2*>(args.R + t * args.N + n));
+        if (EPI == F8_RESID && in) r = *reinterpret_cast<const uint2*>(args.R + t * args.N + n);  // C may be R
         float4 v0[MAX_CLUSTER], v1[MAX_CLUSTER];
 #pragma unroll
         for (int j = 0; j < MAX_CLUSTER; ++j) {
@@ -385,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
         }
         if (NA == 2) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = in ? __fdividef(o[k], 1.f + __expf(-o[k])) * u[k] : 0.f;
+          for (int k = 0; k < 4; ++k) o[k] = in ? silu_mul(o[k], u[k]) : 0.f;
         }
         if (EPI == F8_RESID) {
           o[0] += bf16lo(r.x); o[1] += bf16hi(r.x); o[2] += bf16lo(r.y); o[3] += bf16hi(r.y);
@@ -397,7 +395,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) top = absmax_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
           const float s = f8_scale(top), inv = 1.f / s;
-          if (in) *reinterpret_cast<uint32_t*>(args.q + t * args.N + n) = f8_codes4(o[0], o[1], o[2], o[3], s, inv);
+          if (in) *reinterpret_cast<uint32_t*>(args.q + t * args.N + n) = f8_codes4_near(o[0], o[1], o[2], o[3], inv);
           if (lane == 0) args.c_s[static_cast<size_t>(wt) * args.M + t] = s;
         } else if (in) {
           *reinterpret_cast<uint2*>(args.C + t * args.N + n) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
