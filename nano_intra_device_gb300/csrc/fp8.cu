@@ -125,7 +125,7 @@ nf_status nf_rmsnorm_fp8(const void* x, const void* r, const void* g, void* h, v
   a.eps = eps;
   a.q = static_cast<uint8_t*>(q);
   a.s = s;
-  NF_CUDA8(nf::launch_f8_rows(a, static_cast<cudaStream_t>(stream)));
+  NF_CUDA8(nf::launch_f8_rows(a, sm_count(), static_cast<cudaStream_t>(stream)));
   return NF_OK;
 }
 
@@ -147,7 +147,7 @@ nf_status nf_quant_fp8(const void* x, int32_t src_rows, const int32_t* index, vo
   a.cols = cols;
   a.q = static_cast<uint8_t*>(q);
   a.s = s;
-  NF_CUDA8(nf::launch_f8_rows(a, static_cast<cudaStream_t>(stream)));
+  NF_CUDA8(nf::launch_f8_rows(a, sm_count(), static_cast<cudaStream_t>(stream)));
   return NF_OK;
 }
 

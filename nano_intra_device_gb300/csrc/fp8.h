@@ -25,7 +25,7 @@ struct F8RowsArgs {
   uint8_t* q;
   float* s;  // [ceil(cols / 128)][rows]
 };
-cudaError_t launch_f8_rows(const F8RowsArgs& a, cudaStream_t stream);
+cudaError_t launch_f8_rows(const F8RowsArgs& a, int sms, cudaStream_t stream);
 
 // mats matrices [rows, cols] to 8 bits in 128 x 128 blocks, scales [mats][row block][column block].
 cudaError_t launch_f8_weights(const __nv_bfloat16* w, uint8_t* q, float* s, int mats, int rows,

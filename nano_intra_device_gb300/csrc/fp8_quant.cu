@@ -14,34 +14,48 @@
 namespace nf {
 namespace {
 
+constexpr int FEW_BLOCKS = 128, QV = 4;
+
 __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
   v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
   v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
 }
 
-// One CTA a row, VPT vectors of 8 columns a thread (vector j * blockDim + thread);
-// 16 neighbouring threads hold a block of 128.
-template <int VPT, bool NORM, bool RES>
-__global__ void __launch_bounds__(512) f8_rows_kernel(const F8RowsArgs a) {
+// Vector i of a row (v; nothing from nvec on): `top` is its largest magnitude, the
+// largest of 16 neighbouring threads the block's.  All lanes of a warp together.
+__device__ __forceinline__ void store_block(const F8RowsArgs& a, int row, int i, int nvec, const float (&v)[8], float top) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = absmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float s = f8_scale(top), inv = 1.f / s;
+  if (i < nvec) {
+    reinterpret_cast<uint2*>(a.q + static_cast<size_t>(row) * a.cols)[i] =
+        make_uint2(f8_codes4(v[0], v[1], v[2], v[3], s, inv), f8_codes4(v[4], v[5], v[6], v[7], s, inv));
+    if ((i & 15) == 0) a.s[static_cast<size_t>(i >> 4) * a.rows + row] = s;
+  }
+}
+
+// The norm: a row a warp (WARP) or a CTA, VPT vectors of 8 columns a thread, vector j *
+// (threads of a row) + thread, so that 16 neighbouring threads hold a block of 128.
+template <int VPT, bool RES, bool WARP>
+__global__ void __launch_bounds__(512) f8_norm_kernel(const F8RowsArgs a) {
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, nvec = a.cols / 8;
-  const int from = a.index ? a.index[row] : row;
-  const bool there = from >= 0 && from < a.src_rows;
-  const size_t at = static_cast<size_t>(there ? from : 0) * a.cols;
-  const uint4* xr = reinterpret_cast<const uint4*>(a.x + at);
-  float v[VPT][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int ti = WARP ? lane : threadIdx.x, tr = WARP ? 32 : blockDim.x, nvec = a.cols / 8;
+  const int row = WARP ? blockIdx.x * warps + warp : blockIdx.x;
+  if (row >= a.rows) return;  // (a whole warp)
+  const size_t at = static_cast<size_t>(row) * a.cols;
+  float v[VPT][8], ss = 0.f;
   uint4 xv[VPT], rv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int i = j * blockDim.x + threadIdx.x;
+    const int i = j * tr + ti;
     xv[j] = rv[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (there && i < nvec) {
-      xv[j] = xr[i];  // plain loads: h may be x or r
+    if (i < nvec) {  // plain loads: h may be x or r
+      xv[j] = reinterpret_cast<const uint4*>(a.x + at)[i];
       if (RES) rv[j] = reinterpret_cast<const uint4*>(a.r + at)[i];
     }
   }
-  float ss = 0.f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     unpack8(xv[j], v[j]);
@@ -50,59 +64,84 @@ __global__ void __launch_bounds__(512) f8_rows_kernel(const F8RowsArgs a) {
       unpack8(rv[j], r);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[j][k] += r[k];
-      const int i = j * blockDim.x + threadIdx.x;
+      const int i = j * tr + ti;
       if (a.h && i < nvec)
         reinterpret_cast<uint4*>(a.h + at)[i] = make_uint4(pack_bf16(v[j][0], v[j][1]), pack_bf16(v[j][2], v[j][3]),
                                                            pack_bf16(v[j][4], v[j][5]), pack_bf16(v[j][6], v[j][7]));
     }
-    if (NORM) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss += v[j][k] * v[j][k];
-    }
+    for (int k = 0; k < 8; ++k) ss += v[j][k] * v[j][k];
   }
-  if (NORM) {
-    __shared__ float red[32];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (!WARP) {
+    __shared__ float red[16];
+    if (lane == 0) red[warp] = ss;
     __syncthreads();
-    float tot = 0.f;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) tot += red[i];
-    const float scale = 1.f / sqrtf(tot / a.cols + a.eps);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int i = j * blockDim.x + threadIdx.x;
-      if (i < nvec) {
-        float g[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.g) + i), g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] = v[j][k] * scale * g[k];
-      }
-    }
+    ss = 0.f;
+    for (int i = 0; i < warps; ++i) ss += red[i];
   }
+  const float scale = 1.f / sqrtf(ss / a.cols + a.eps);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int i = j * blockDim.x + threadIdx.x;
+    const int i = j * tr + ti;
     float top = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = absmax_nan(top, v[j][k]);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = absmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float s = f8_scale(top), inv = 1.f / s;
     if (i < nvec) {
-      const uint2 c = make_uint2(f8_codes4(v[j][0], v[j][1], v[j][2], v[j][3], s, inv),
-                                 f8_codes4(v[j][4], v[j][5], v[j][6], v[j][7], s, inv));
-      reinterpret_cast<uint2*>(a.q + static_cast<size_t>(row) * a.cols)[i] = c;
-      if ((i & 15) == 0) a.s[static_cast<size_t>(i >> 4) * a.rows + row] = s;
+      float g[8];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(a.g) + i), g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[j][k] = v[j][k] * scale * g[k];
+        top = absmax_nan(top, v[j][k]);
+      }
     }
+    store_block(a, row, i, nvec, v[j], top);
   }
 }
 
-template <int VPT>
-cudaError_t launch_rows(const F8RowsArgs& a, int threads, cudaStream_t stream) {
-  if (!a.g) return launch_dependent(f8_rows_kernel<VPT, false, false>, a.rows, threads, 0, stream, a);
-  if (a.r) return launch_dependent(f8_rows_kernel<VPT, true, true>, a.rows, threads, 0, stream, a);
-  return launch_dependent(f8_rows_kernel<VPT, true, false>, a.rows, threads, 0, stream, a);
+template <int VPT, bool WARP>
+cudaError_t launch_norm(const F8RowsArgs& a, int threads, cudaStream_t stream) {
+  const int of_cta = WARP ? threads / 32 : 1;
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.rows) + of_cta - 1) / of_cta);
+  if (a.r) return launch_dependent(f8_norm_kernel<VPT, true, WARP>, grid, threads, 0, stream, 1, a);
+  return launch_dependent(f8_norm_kernel<VPT, false, WARP>, grid, threads, 0, stream, 1, a);
+}
+
+// Given values: a CTA takes 16 rows x V column blocks, 16 threads a block of 128, so that
+// the scales of neighbouring rows, next to one another in memory, are written together.
+template <int V>
+__global__ void __launch_bounds__(256) f8_quant_kernel(const F8RowsArgs a, int col_groups) {
+  pdl_trigger();
+  pdl_wait();
+  const int sub = threadIdx.x & 15, nvec = a.cols / 8;
+  const int group = blockIdx.x / col_groups, row = group * 16 + (threadIdx.x >> 4);
+  const int vec = (blockIdx.x - group * col_groups) * (V * 16) + sub;
+  const int from = row < a.rows ? a.index ? __ldg(a.index + row) : row : -1;
+  const bool there = from >= 0 && from < a.src_rows;
+  const uint4* x = reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(there ? from : 0) * a.cols);
+  uint4 u[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    u[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (there && vec + 16 * j < nvec) u[j] = __ldg(x + vec + 16 * j);
+  }
+  const int end = row < a.rows ? nvec : 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float v[8], top = 0.f;
+    unpack8(u[j], v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = absmax_nan(top, v[k]);
+    store_block(a, row, vec + 16 * j, end, v, top);
+  }
+}
+
+template <int V>
+cudaError_t launch_quant(const F8RowsArgs& a, cudaStream_t stream) {
+  const int col_groups = (a.cols + V * F8_BLOCK - 1) / (V * F8_BLOCK);
+  const long long grid = (static_cast<long long>(a.rows) + 15) / 16 * col_groups;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_dependent(f8_quant_kernel<V>, static_cast<unsigned>(grid), 256, 0, stream, 1, a, col_groups);
 }
 
 // One CTA a 128 x 128 block: thread t has vector t % 16 of the rows t / 16 + 16 i.
@@ -153,15 +192,21 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-cudaError_t launch_f8_rows(const F8RowsArgs& a, cudaStream_t stream) {
+cudaError_t launch_f8_rows(const F8RowsArgs& a, int sms, cudaStream_t stream) {
   if (a.rows <= 0) return cudaSuccess;
   if (a.cols % 16 || a.cols > F8_MAX_COLS) return cudaErrorInvalidValue;
   const int nvec = a.cols / 8;
+  if (!a.g) {
+    const long long blocks = static_cast<long long>(a.rows) * ((nvec + 15) / 16);
+    return blocks <= FEW_BLOCKS * sms ? launch_quant<1>(a, stream) : launch_quant<QV>(a, stream);
+  }
   auto threads = [&](int vpt) { return (nvec + 32 * vpt - 1) / (32 * vpt) * 32; };
-  if (nvec <= 512) return launch_rows<1>(a, threads(1), stream);
-  if (nvec <= 1024) return launch_rows<2>(a, threads(2), stream);
-  if (nvec <= 2048) return launch_rows<4>(a, threads(4), stream);
-  return launch_rows<8>(a, threads(8), stream);
+  if (nvec <= 32) return launch_norm<1, true>(a, 128, stream);
+  if (nvec <= 64) return launch_norm<2, true>(a, 128, stream);
+  if (nvec <= 512 && (nvec <= 128 || a.rows <= 8 * sms)) return launch_norm<1, false>(a, threads(1), stream);
+  if (nvec <= 1024) return launch_norm<2, false>(a, threads(2), stream);
+  if (nvec <= 2048) return launch_norm<4, false>(a, threads(4), stream);
+  return launch_norm<8, false>(a, threads(8), stream);
 }
 
 cudaError_t launch_f8_weights(const __nv_bfloat16* w, uint8_t* q, float* s, int mats, int rows,
@@ -169,7 +214,7 @@ cudaError_t launch_f8_weights(const __nv_bfloat16* w, uint8_t* q, float* s, int 
   const long long rb = (rows + F8_BLOCK - 1) / F8_BLOCK, cb = (cols + F8_BLOCK - 1) / F8_BLOCK;
   if (mats * rb * cb <= 0) return cudaSuccess;
   if (mats * rb * cb > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_dependent(f8_weights_kernel, static_cast<unsigned>(mats * rb * cb), 256, 0, stream, w, q, s, rows, cols,
+  return launch_dependent(f8_weights_kernel, static_cast<unsigned>(mats * rb * cb), 256, 0, stream, 1, w, q, s, rows, cols,
                           static_cast<int>(rb), static_cast<int>(cb));
 }
 

@@ -42,7 +42,6 @@ struct Tail {
   int abort;
   int tile0[F8_MAX_GROUPS + 1];  // first tile of each group
   int row0[F8_MAX_GROUPS + 1];   // first row of each group
-  uint64_t sfull[8];
   float a_s[8][BM];       // scales of the next blocks of K: of A's rows,
   float b_s[8][2];        // and of B's halves (SwiGLU: of gate and up)
   float top[2][8][32];    // SWIGLU8: by tile parity and warp, a row's largest value
@@ -77,15 +76,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&tail->full[s], 1);
+      mbar_init(&tail->full[s], 1 + 32);  // the tiles, the scales' 32 lanes
       mbar_init(&tail->empty[s], 2);
     }
     for (int a = 0; a < 4; ++a) {
-      mbar_init(&tail->tfull[a], 1);
+      mbar_init(&tail->tfull[a], 2);  // the products, and the scales as their issuer saw them
       mbar_init(&tail->tempty[a], 4);
     }
     for (int a = 0; a < 2; ++a) mbar_init(&tail->drain[a], 1);
-    for (int a = 0; a < 8; ++a) mbar_init(&tail->sfull[a], 32);
     for (int a = 0; a < 4; ++a) mbar_init(&tail->pair[a], 2);
     tail->abort = 0;
     fence_mbar_init();
@@ -216,6 +214,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int k = 0; k < BK / 32; ++k)  // 32 codes = 32 bytes along the swizzled row
               tc_mma_e4m3(d, ad + 2 * k, bd + 2 * k, IDESC, k != 0);
             tc_commit(&tail->tfull[2 * h + acc]);
+            mbar_arrive(&tail->tfull[2 * h + acc]);
             tc_commit(&tail->empty[st]);
           }
           any = true;
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) copy4(&tail->a_s[slot][lane + 32 * i], rows > 32 * i ? as + 32 * i : args.a_s, rows > 32 * i);
           if (lane < 2) copy4(&tail->b_s[slot][lane], bs + kb, true);
-          mbar_arrive_copied(&tail->sfull[slot]);
+          mbar_arrive_copied(&tail->full[st]);
           as += args.M;
           slot = (slot + 1) % 8;
           if (++st == STAGES) {
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // 16-byte chunk j of row r of the warp's 2 KB, so placed that rows are written and
     // read eight lanes at a time without bank conflicts
     auto slot = [&](int r, int j) { return reinterpret_cast<uint4*>(mine + r * 64 + ((j ^ (r >> 1 & 3)) << 4)); };
-    uint32_t acc = 0, aph = 0, parity = 0, slot8 = 0, sph = 0;
+    uint32_t acc = 0, aph = 0, parity = 0, slot8 = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
       // This thread's sums: 128 columns of its half (SwiGLU: 64 features' gate columns,
@@ -289,8 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = 0; i < 128; ++i) sum[i] = 0.f;
 #pragma unroll 1
       for (int kb = 0; kb < nk; ++kb) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&tail->sfull[slot8], sph, tmo, abort_flag) &&
-                                         mbar_wait(&tail->tfull[2 * half + acc], aph, tmo, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&tail->tfull[2 * half + acc], aph, tmo, abort_flag))) {
           ok = false;
           break;
         }
@@ -305,10 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_ld_32x32b_x32(tb + 32, v[1]);
         const float as = tail->a_s[slot8][row_in_tile];
         const float s0 = as * tail->b_s[slot8][SW ? 0 : half], s1 = SW ? as * tail->b_s[slot8][1] : s0;
-        if (++slot8 == 8) {
-          slot8 = 0;
-          sph ^= 1;
-        }
+        slot8 = (slot8 + 1) % 8;
         tc_wait_ld();
         add(0, s0);
         tc_ld_32x32b_x32(tb + 64, v[0]);
@@ -429,7 +424,7 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const F8GemmA
                    cudaStream_t stream) {
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(gemm_f8_kernel<EPI>), SMEM);
   if (e != cudaSuccess) return e;
-  return launch_dependent(gemm_f8_kernel<EPI>, grid, THREADS, SMEM, stream, tmA, tmB, args);
+  return launch_dependent(gemm_f8_kernel<EPI>, grid, THREADS, SMEM, stream, 1, tmA, tmB, args);
 }
 
 }  // namespace

@@ -68,17 +68,6 @@ static_assert(sizeof(Tail) <= TAIL_BYTES, "barrier block");
 
 __device__ uint32_t g_status;
 
-// 32 lanes x 16 columns, as the 32-column form.
-__device__ __forceinline__ void tc_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
 // The two halves of cluster_sync_all, for threads that diverge in between.
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -298,12 +287,12 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * C::COLS + half * MINE;
       uint32_t v[MINE / 16 > 1 ? 2 : 1][16];
-      tc_ld_x16(tb, v[0]);
+      tc_ld_32x32b_x16(tb, v[0]);
 #pragma unroll
       for (int c = 0; c < MINE / 16; ++c) {
         tc_wait_ld();
         if (c + 1 < MINE / 16) {
-          tc_ld_x16(tb + 16 * (c + 1), v[(c + 1) & 1]);
+          tc_ld_32x32b_x16(tb + 16 * (c + 1), v[(c + 1) & 1]);
         } else {
           tc_fence_before();
           if (lane == 0) mbar_arrive(&tail->tempty[acc]);
