@@ -39,7 +39,7 @@ struct Cfg {
   static constexpr int HALVES = COLS > 64 ? 2 : 1;      // summing warps: 4 a half
   static constexpr int MINE = COLS / HALVES;            // columns of a thread
   static constexpr int THREADS = 64 + 128 * HALVES;
-  static constexpr int ACCS = COLS <= 32 ? 4 : 2;       // accumulators, in turn
+  static constexpr int ACCS = 4;                         // accumulators, in turn
   static constexpr int TMEM = ACCS * COLS < 32 ? 32 : ACCS * COLS;
   static constexpr int STAGE = NA * WM * BK + TOK * BK;
   static constexpr int SCALES = 4 * HALVES * 2 * MINE * 4;
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const int row = quarter * 32 + lane;  // feature of the tile
     float* sc = scales + (warp - 2) * 2 * MINE;
-    f32x2 sum[MINE / 2];
+    float sum[MINE];
 #pragma unroll
-    for (int i = 0; i < MINE / 2; ++i) sum[i] = 0;
+    for (int i = 0; i < MINE; ++i) sum[i] = 0.f;
     // Column half * MINE + lane + 32 i of the accumulator: its row of A, its operand of B.
     constexpr int CI = (MINE + 31) / 32, AHEAD = 4;
     const float* bs = args.b_s + (static_cast<size_t>(e) * NA * nb + wt) * nk;
@@ -295,13 +295,18 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
           tc_ld_32x32b_x16(tb + 16 * (c + 1), v[(c + 1) & 1]);
         } else {
           tc_fence_before();
-          if (lane == 0) mbar_arrive(&tail->tempty[acc]);
+          __syncwarp();
+          mbar_arrive_if(&tail->tempty[acc], lane == 0);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float4 s = *reinterpret_cast<const float4*>(p + 16 * c + 4 * j);
-          fma_f32x2(sum[8 * c + 2 * j], pack_b32x2(v[c & 1][4 * j], v[c & 1][4 * j + 1]), pack_f32x2(s.x, s.y));
-          fma_f32x2(sum[8 * c + 2 * j + 1], pack_b32x2(v[c & 1][4 * j + 2], v[c & 1][4 * j + 3]), pack_f32x2(s.z, s.w));
+          float* d = sum + 16 * c + 4 * j;
+          const uint32_t* a = v[c & 1] + 4 * j;
+          fma_loaded(d[0], a[0], s.x);
+          fma_loaded(d[1], a[1], s.y);
+          fma_loaded(d[2], a[2], s.z);
+          fma_loaded(d[3], a[3], s.w);
         }
       }
       if (++acc == ACCS) {
@@ -324,12 +329,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     // After a failure the ring may still be written: nothing is stored.
     if (ok) {
 #pragma unroll
-      for (int j = 0; j < MINE / 2; ++j) {
-        float a, b;
-        unpack_f32x2(sum[j], a, b);
-        xbuf[(half * MINE + 2 * j) * WM + row] = a;
-        xbuf[(half * MINE + 2 * j + 1) * WM + row] = b;
-      }
+      for (int j = 0; j < MINE; ++j) xbuf[(half * MINE + j) * WM + row] = sum[j];
     }
     cluster_wait();  // every peer's barriers exist
     asm volatile("bar.sync 1, %0;" ::"n"(128 * C::HALVES) : "memory");
