@@ -45,6 +45,19 @@ nf_status check_rows(int32_t rows, int32_t cols, const char* what) {
   return NF_OK;
 }
 
+// Whether a product goes to the kernel of few rows of A.  Measured, few rows against
+// tiles of 128 rows, us: 4096 x 14336, 1 row 15.6 / 33, 128 rows 20.5 / 34, 256 32.5 / 35;
+// 6144 x 4096, 128 rows 13.9 / 16, 256 20.4 / 16.4.  SwiGLU's two matrices make wide
+// tiles (128 features of both) enough for the GPU sooner: 14336 x 4096, 1 row 24 / 33, 16
+// rows 25.7 / 31, 32 rows 28.2 / 25.1.  Groups, by their mean: 8 of 14336 x 4096 SwiGLU, 8
+// rows 142 / 147, 16 rows 149 / 149, 32 rows 174 / 151; 8 of 4096 x 14336, 16 rows 75 / 77,
+// 32 rows 78 / 78, 48 rows 104 / 78.  A capped product takes the tiles, which loop.
+bool few_rows(int M, int N, int groups, bool two, int sms) {
+  const int rows = (M + groups - 1) / groups;
+  if (groups > 1 || (two && (N + 127) / 128 * 3 >= 2 * sms)) return rows <= 16;
+  return rows <= 128;
+}
+
 // The product's checks, for one matrix (group_off NULL, groups 1) or by groups.
 nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s,
                 const int32_t* group_off, int32_t groups, void* C, float* c_s, const void* R,
@@ -71,8 +84,7 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
   const int sms = sm_count();
   if (sms <= 0) return fail8(NF_ERR_CUDA, "no CUDA device");
   const bool capped = max_sms > 0 && max_sms < sms;
-  const int rows = (M + groups - 1) / groups;
-  const bool few = !capped && rows <= (groups > 1 ? 32 : 128);
+  const bool few = !capped && few_rows(M, N, groups, two, sms);
   nf::F8RowsChoice c{};
   if (few) c = nf::gemm_f8_wrows_choice(epilogue, M, N, K, groups);
   CUtensorMap ta, tb;

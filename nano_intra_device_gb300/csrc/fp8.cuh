@@ -34,6 +34,21 @@ __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[1
       : "r"(taddr)
       : "memory");
 }
+// 16 bytes of a CTA of the cluster, by shared::cluster address.
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// A tile into L2 alone.  Allowed ahead of pdl_wait(): L2 is where writes of the kernel
+// ahead meet later reads, so a line taken early does not get stale.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
 // One lane of a converged warp.  Products are issued under it rather than under
 // `lane == 0`: their operands, computed by the whole warp, then stay in uniform registers.
 __device__ __forceinline__ bool elect_one() {

@@ -12,6 +12,9 @@
 //    registers.  While they do, the tensor core fills the other accumulators.
 //  * Warp 0 loads tiles by TMA, warps 1 and 2 issue the products of a half each, warp 3
 //    copies the scales beside the tiles, warps 4 to 11 sum and run the epilogue.  Persistent CTAs, one an SM.
+//  * A product with tiles for less than half of the SMs is cut along K between the two
+//    CTAs of a cluster (SPLIT): each finishes a half of the tile's columns, with the
+//    other's sums from its shared memory.
 //  * Every wait is bounded; one that gives up flags the status word, and the kernel
 //    drains what it has in flight (bounded) and frees tensor memory.
 #include "fp8.cuh"
@@ -38,6 +41,7 @@ struct Tail {
   uint64_t tempty[4];
   uint64_t pair[4];    // the two warps of 32 rows (SWIGLU8: the block's largest value)
   uint64_t drain[2];
+  uint64_t ready;      // SPLIT: the peer's sums are in its shared memory
   uint32_t tmem_base;
   int abort;
   int tile0[F8_MAX_GROUPS + 1];  // first tile of each group
@@ -55,7 +59,8 @@ struct Tile {
   int m0, m_lim, tn, e;
 };
 
-template <int EPI>
+// SPLIT: the two CTAs of a cluster take a half of K each of one tile (see the header).
+template <int EPI, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_f8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const F8GemmArgs args) {
@@ -71,6 +76,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int nk = (args.K + BK - 1) / BK, n_tiles = (args.N + TN - 1) / TN;
   const int nb = (args.N + F8_BLOCK - 1) / F8_BLOCK;
   const bool grouped = args.group_off != nullptr;
+  const int rank = SPLIT ? static_cast<int>(cluster_rank()) : 0;
+  const int first = SPLIT ? blockIdx.x / 2 : blockIdx.x, stride = SPLIT ? gridDim.x / 2 : gridDim.x;
+  const int k0 = SPLIT ? rank * nk / 2 : 0, k1 = SPLIT ? (rank + 1) * nk / 2 : nk;
   const uint64_t tmo = args.timeout_ns;
 
   pdl_trigger();
@@ -84,6 +92,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&tail->tempty[a], 4);
     }
     for (int a = 0; a < 2; ++a) mbar_init(&tail->drain[a], 1);
+    mbar_init(&tail->ready, 1);
     for (int a = 0; a < 4; ++a) mbar_init(&tail->pair[a], 2);
     tail->abort = 0;
     fence_mbar_init();
@@ -128,6 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (SPLIT) cluster_sync_all();  // the peer's barriers exist before anything arrives on them
   const uint32_t tmem_base = tail->tmem_base;
   volatile int* abort_flag = &tail->abort;
   const int total = grouped ? tail->tile0[args.groups] : (args.M + BM - 1) / BM * n_tiles;
@@ -160,11 +170,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0 && lane == 0) {
       uint32_t st = 0, ph = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+      for (int u = first; u < total && ok; u += stride) {
         const Tile x = decode(u);
         const int b0 = x.e * (SW ? 2 : 1) * args.N + x.tn * TN;
         const int b1 = SW ? b0 + args.N : b0 + 128;
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int kb = k0; kb < k1; ++kb) {
           if (!mbar_wait(&tail->empty[st], ph ^ 1, tmo, abort_flag)) {
             ok = false;
             break;
@@ -199,9 +209,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool one = elect_one();
       uint32_t st = 0, ph = 0, acc = 0, aph = 0;
       bool ok = true, any = false;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+      for (int u = first; u < total && ok; u += stride) {
 #pragma unroll 1
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int kb = k0; kb < k1; ++kb) {
           // (the stage is there long before the accumulator is free)
           const uint32_t sa = smem_u32(smem + st * STAGE_BYTES), d = tmem_base + (2 * h + acc) * (BN / 2);
           const uint64_t ad = desc_sw128_kmajor(sa), bd = desc_sw128_kmajor(sa + A_BYTES + h * (B_BYTES / 2));
@@ -242,14 +252,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       // the stage's products of 4 blocks before are done, so the sums of 2 further before.
       uint32_t st = 0, ph = 0, slot = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+      for (int u = first; u < total && ok; u += stride) {
         const Tile x = decode(u);
         const int b0 = SW ? x.tn : min(2 * x.tn, nb - 1), b1 = SW ? nb + x.tn : min(2 * x.tn + 1, nb - 1);
-        const float* as = args.a_s + x.m0 + lane;
+        const float* as = args.a_s + static_cast<size_t>(k0) * args.M + x.m0 + lane;
         const float* bs = args.b_s + (static_cast<size_t>(x.e) * (SW ? 2 : 1) * nb + (lane ? b1 : b0)) * nk;
         const int rows = x.m_lim - x.m0 - lane;  // row 32 i of this lane's is there below it
 #pragma unroll 1
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int kb = k0; kb < k1; ++kb) {
           ok = __all_sync(0xffffffffu, mbar_wait(&tail->empty[st], ph ^ 1, tmo, abort_flag)) != 0;
           if (!ok) break;
 #pragma unroll
@@ -280,14 +290,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto slot = [&](int r, int j) { return reinterpret_cast<uint4*>(mine + r * 64 + ((j ^ (r >> 1 & 3)) << 4)); };
     uint32_t acc = 0, aph = 0, parity = 0, slot8 = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+    for (int u = first; u < total && ok; u += stride) {
       // This thread's sums: 128 columns of its half (SwiGLU: 64 features' gate columns,
       // then their up columns).
       float sum[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.f;
 #pragma unroll 1
-      for (int kb = 0; kb < nk; ++kb) {
+      for (int kb = k0; kb < k1; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(&tail->tfull[2 * half + acc], aph, tmo, abort_flag))) {
           ok = false;
           break;
@@ -318,6 +328,39 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (++acc == 2) {
           acc = 0;
           aph ^= 1;
+        }
+      }
+      if (SPLIT) {
+        // Both halves' products have read the ring, which now takes the sums that the peer
+        // finishes: four columns of a row together, rows next to one another.
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        float4* ring = reinterpret_cast<float4*>(smem);
+        if (half != rank) {
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              ring[i * BM + row_in_tile] = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
+          }
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (quarter == 0 && lane == 0) {
+            fence_acq_rel_cluster();
+            mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), rank ^ 1));
+          }
+          break;  // (one tile a cluster; !ok is reported below)
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo)) && ok;
+        if (!ok) break;
+        const uint32_t peer = cluster_map(smem_u32(ring + row_in_tile), rank ^ 1);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {  // (a load takes about a microsecond: many at once)
+          float4 w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = ld_cluster_f4(peer + (b * 16 + i) * (BM * 16));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float* d = sum + (b * 16 + i) * 4;
+            d[0] += w[i].x; d[1] += w[i].y; d[2] += w[i].z; d[3] += w[i].w;
+          }
         }
       }
       if (!ok) break;
@@ -414,17 +457,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
+  if (SPLIT) cluster_sync_all();  // no CTA leaves while the peer may read its sums
 }
 
 __device__ uint32_t g_taken;
 __global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0u); }
 
-template <int EPI>
+template <int EPI, bool SPLIT>
 cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const F8GemmArgs& args, int grid,
                    cudaStream_t stream) {
-  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(gemm_f8_kernel<EPI>), SMEM);
+  const auto kernel = gemm_f8_kernel<EPI, SPLIT>;
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), SMEM);
   if (e != cudaSuccess) return e;
-  return launch_dependent(gemm_f8_kernel<EPI>, grid, THREADS, SMEM, stream, 1, tmA, tmB, args);
+  return launch_dependent(kernel, grid, THREADS, SMEM, stream, SPLIT ? 2 : 1, tmA, tmB, args);
 }
 
 }  // namespace
@@ -432,16 +477,23 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const F8GemmA
 cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& tmB,
                            const F8GemmArgs& args, int sms, cudaStream_t stream) {
   const int tn = epi >= F8_SWIGLU ? BN / 2 : BN;
-  const long long most = ((args.M + BM - 1) / BM + (args.group_off ? args.groups : 0)) *
-                         static_cast<long long>((args.N + tn - 1) / tn);
+  const long long most = ((static_cast<long long>(args.M) + BM - 1) / BM + (args.group_off ? args.groups : 0)) *
+                         ((args.N + tn - 1) / tn);
   if (most > 0x7fffffffLL || args.groups > F8_MAX_GROUPS) return cudaErrorInvalidValue;
   if (most <= 0) return cudaSuccess;
+  // Tiles for less than half of the SMs, and four blocks of K at least for each of two CTAs
+  if (!args.group_off && 2 * most <= sms && (args.K + BK - 1) / BK >= 8) {
+    const int grid = static_cast<int>(2 * most);
+    if (epi == F8_STORE) return launch<F8_STORE, true>(tmA, tmB, args, grid, stream);
+    if (epi == F8_RESID) return launch<F8_RESID, true>(tmA, tmB, args, grid, stream);
+    if (epi == F8_SWIGLU) return launch<F8_SWIGLU, true>(tmA, tmB, args, grid, stream);
+  }
   const int grid = static_cast<int>(most < sms ? most : sms);
   switch (epi) {
-    case F8_STORE: return launch<F8_STORE>(tmA, tmB, args, grid, stream);
-    case F8_RESID: return launch<F8_RESID>(tmA, tmB, args, grid, stream);
-    case F8_SWIGLU: return launch<F8_SWIGLU>(tmA, tmB, args, grid, stream);
-    case F8_SWIGLU8: return launch<F8_SWIGLU8>(tmA, tmB, args, grid, stream);
+    case F8_STORE: return launch<F8_STORE, false>(tmA, tmB, args, grid, stream);
+    case F8_RESID: return launch<F8_RESID, false>(tmA, tmB, args, grid, stream);
+    case F8_SWIGLU: return launch<F8_SWIGLU, false>(tmA, tmB, args, grid, stream);
+    case F8_SWIGLU8: return launch<F8_SWIGLU8, false>(tmA, tmB, args, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }

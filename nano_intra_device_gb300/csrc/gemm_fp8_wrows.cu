@@ -75,15 +75,6 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 template <int EPI, int TOK>
 __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     gemm_f8_wrows_kernel(const __grid_constant__ CUtensorMap tmW,
@@ -125,7 +116,17 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     tmem_alloc(&tail->tmem_base, C::TMEM);
     tmem_relinquish();
   }
-  pdl_wait();  // nothing before this reads or writes global memory
+  if (threadIdx.x == 0 && !args.group_off) {
+    // the first blocks of B are on their way from memory while the kernel ahead ends
+    const int w = unit / ((args.M + TOK - 1) / TOK), a = rank * nk / S, n = (rank + 1) * nk / S - a;
+    const int turn = static_cast<int>(static_cast<long long>(w) * n / nb) % n;
+    for (int i = 0; i < min(STAGES, n); ++i) {
+      const int kx = (a + (i + turn >= n ? i + turn - n : i + turn)) * BK;
+      tma_prefetch_2d(&tmW, kx, w * WM);
+      if (NA == 2) tma_prefetch_2d(&tmW, kx, w * WM + args.N);
+    }
+  }
+  pdl_wait();  // nothing before this reads or writes global memory but into L2
   if (warp == 2) {
     if (!args.group_off) {
       if (lane == 0) {
