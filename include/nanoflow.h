@@ -600,7 +600,7 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
  * all in fp32 (the squares' sum must stay within its range); y becomes q and s.
  * x, r, h: device bf16 [rows, hidden]; r NULL: h = x.  h (the residual of the
  * next addition, rounded to bf16) may be NULL, must be without r, and may be x
- * or r itself.  g: device bf16 [hidden].  q: device e4m3 [rows, hidden], s:
+ * or r itself; q overlaps none of them.  g: device bf16 [hidden].  q: device e4m3 [rows, hidden], s:
  * device fp32 [ceil(hidden / 128)][rows].  hidden: a multiple of 16, <= 32768. */
 nf_status nf_rmsnorm_fp8(const void* x, const void* r, const void* g, void* h, void* q, float* s,
                          int32_t rows, int32_t hidden, float eps, void* stream);
@@ -652,9 +652,12 @@ nf_status nf_gemm_fp8_grouped(const void* A, const float* a_s, const void* B, co
 
 /* Waits for `stream`, then reports and clears what the products of this section
  * have flagged on the current device since the last poll: NF_OK, or
- * NF_ERR_TIMEOUT if a bounded wait gave up (2 s; outputs since then are
- * undefined). */
+ * NF_ERR_TIMEOUT if a bounded wait gave up (outputs since then are undefined,
+ * later calls are not affected). */
 nf_status nf_fp8_poll(void* stream);
+/* Limit of every device-side wait of the products that this process calls (or
+ * captures) from now on, in [1, 1e10] (2e9 at first). */
+nf_status nf_fp8_set_timeout(int64_t timeout_ns);
 
 /* Copy one of the plan's device buffers (written by the last step or
  * metadata call on the plan's device) to dst (host or device), synchronously.

@@ -134,6 +134,7 @@ _SIGS = {
     "nf_gemm_fp8_grouped": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
                                     c_int32, c_int32, c_int32, c_int32, c_void_p]),
     "nf_fp8_poll": (c_int, [c_void_p]),
+    "nf_fp8_set_timeout": (c_int, [c_int64]),
     "nf_kv4_pool_bytes": (c_int, [POINTER(nf_model_shape), c_int32, POINTER(c_size_t)]),
     "nf_block_tables": (c_int, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_int32, c_void_p,
                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p]),
@@ -579,6 +580,11 @@ def gemm_fp8_grouped(a, a_s, b, b_s, group_off, c, c_s=None, epilogue=NF_EPI_STO
 def fp8_poll(stream=None):
     """nf_fp8_poll: wait for the stream, then report and clear what the 8-bit products flagged."""
     check(lib().nf_fp8_poll(stream_handle(stream)))
+
+
+def fp8_set_timeout(timeout_ns):
+    """nf_fp8_set_timeout: the limit of the device-side waits of later 8-bit products."""
+    check(lib().nf_fp8_set_timeout(int(timeout_ns)))
 
 
 # ------------------------------------------------------ the 4-bit KV cache

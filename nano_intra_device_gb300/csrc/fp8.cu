@@ -1,4 +1,5 @@
 // C ABI of the 8-bit operators: argument checks, tensor maps, launches.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 
@@ -9,7 +10,7 @@
 
 namespace {
 
-constexpr unsigned long long kTimeoutNs = 2000000000ULL;
+std::atomic<int64_t> g_timeout_ns{2000000000};  // nf_fp8_set_timeout
 
 nf_status fail8(nf_status s, const char* fmt, ...) {
   char buf[512];
@@ -104,7 +105,7 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
   g.R = static_cast<const __nv_bfloat16*>(R);
   g.q = eight ? static_cast<uint8_t*>(C) : nullptr;
   g.c_s = c_s;
-  g.timeout_ns = kTimeoutNs;
+  g.timeout_ns = static_cast<unsigned long long>(g_timeout_ns.load(std::memory_order_relaxed));
   if (few) {
     g.splits = c.splits;
     NF_CUDA8(nf::launch_gemm_f8_wrows(epilogue, c.tok, tb, ta, g, c.units, static_cast<cudaStream_t>(stream)));
@@ -194,6 +195,13 @@ nf_status nf_gemm_fp8_grouped(const void* A, const float* a_s, const void* B, co
   if (epilogue == NF_EPI_RESID) return fail8(NF_ERR_INVALID_ARG, "the grouped product has no residual epilogue");
   if (M > 0 && !group_off) return fail8(NF_ERR_INVALID_ARG, "NULL argument");
   return gemm8(A, a_s, B, b_s, group_off, groups, C, c_s, nullptr, M, N, K, epilogue, max_sms, stream);
+}
+
+nf_status nf_fp8_set_timeout(int64_t timeout_ns) {
+  if (timeout_ns < 1 || timeout_ns > 10000000000LL)
+    return fail8(NF_ERR_INVALID_ARG, "timeout_ns must lie in [1, 1e10]");
+  g_timeout_ns.store(timeout_ns, std::memory_order_relaxed);
+  return NF_OK;
 }
 
 nf_status nf_fp8_poll(void* stream) {

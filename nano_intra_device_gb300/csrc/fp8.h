@@ -9,6 +9,9 @@ namespace nf {
 
 constexpr int F8_BLOCK = 128;        // columns (and, for weights, rows) of a scale's block
 constexpr int F8_MAX_GROUPS = 128;   // groups of rows of one product
+// After a wait gave up: the limit of the waits for what is in flight already (loads,
+// products), which takes microseconds, whatever the call's own limit is.
+constexpr unsigned long long F8_DRAIN_NS = 20000000ULL;
 constexpr int F8_MAX_COLS = 32768;   // columns of a row that one CTA norms or quantises
 
 enum { F8_STORE = 0, F8_RESID = 1, F8_SWIGLU = 2, F8_SWIGLU8 = 3 };

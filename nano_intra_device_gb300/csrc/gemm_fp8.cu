@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   uint32_t issued = 0, phases = 0;  // thread 0: the ring's stages and the phase of their last load
+  bool issuer = false;              // this thread has issued products
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FEW));
     if (warp == 0 && lane == 0) {
@@ -241,11 +242,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok && one) {
         raise_status(&g_status, ST_TIMEOUT);
         *abort_flag = 1;
-        if (any) {  // the products already issued end before tensor memory goes away
-          tc_commit(&tail->drain[h]);
-          mbar_wait(&tail->drain[h], 0, tmo);
-        }
       }
+      issuer = one && any;
     }
     if (warp == 3) {
       // Scales, copied beside the tiles: a slot is filled again 8 blocks of K later, when
@@ -450,9 +448,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag)  // loads in flight land before shared memory goes away
-    for (int s = 0; s < STAGES; ++s)
-      if (issued & (1u << s)) mbar_wait(&tail->full[s], phases >> s & 1, tmo);
+  if (*abort_flag) {
+    // Whoever gave up: products in flight end before tensor memory goes away, loads land
+    // before shared memory does.
+    if (issuer) {
+      tc_commit(&tail->drain[warp - 1]);
+      mbar_wait(&tail->drain[warp - 1], 0, F8_DRAIN_NS);
+    }
+    if (threadIdx.x == 0)
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) mbar_wait(&tail->full[s], phases >> s & 1, F8_DRAIN_NS);
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);

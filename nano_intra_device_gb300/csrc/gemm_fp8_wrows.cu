@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
   auto kb_at = [&](int i) { return kb0 + (i + rot >= klen ? i + rot - klen : i + rot); };
 
   uint32_t issued = 0, phases = 0;  // thread 0: the ring's stages and the phase of their last load
+  bool issuer = false;              // this thread has issued products
   if (warp == 0) {
     if (lane == 0) {
       const int w0 = e * NA * args.N + wt * WM;
@@ -220,10 +221,6 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
             !mbar_wait(&tail->full[st], ph, tmo, abort_flag)) {
           raise_status(&g_status, ST_TIMEOUT);
           *abort_flag = 1;
-          if (i) {  // the products already issued end before tensor memory goes away
-            tc_commit(&tail->drain);
-            mbar_wait(&tail->drain, 0, tmo);
-          }
           break;
         }
         tc_fence_after();
@@ -235,6 +232,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
           tc_mma_e4m3(d, w0 + 2 * k, xd + 2 * k, IDESC, k != 0);
           if (NA == 2) tc_mma_e4m3(d + TOK, w1 + 2 * k, xd + 2 * k, IDESC, k != 0);
         }
+        issuer = true;
         tc_commit(&tail->empty[st]);
         tc_commit(&tail->tfull[acc]);
         if (++st == STAGES) {
@@ -396,9 +394,18 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag)  // loads in flight land before shared memory goes away
-    for (int s = 0; s < STAGES; ++s)
-      if (issued & (1u << s)) mbar_wait(&tail->full[s], phases >> s & 1, tmo);
+  if (*abort_flag) {
+    // Whoever gave up: products in flight end before tensor memory goes away, loads land
+    // before shared memory does.
+    if (issuer) {
+      tc_commit(&tail->drain);
+      mbar_wait(&tail->drain, 0, F8_DRAIN_NS);
+    }
+    if (threadIdx.x == 0)
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) mbar_wait(&tail->full[s], phases >> s & 1, F8_DRAIN_NS);
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM);

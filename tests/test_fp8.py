@@ -134,6 +134,12 @@ def test_gemm_refusals(L, grouped):
     assert call(m=0) == _lib.NF_OK
 
 
+def test_timeout_refusals(L):
+    for bad in (0, -1, 10 ** 10 + 1):
+        assert "timeout_ns" in _refused(L.nf_fp8_set_timeout(bad))
+    assert L.nf_fp8_set_timeout(2 * 10 ** 9) == _lib.NF_OK
+
+
 def test_the_bf16_product_refuses_the_8_bit_epilogue(L):
     _refused(L.nf_gemm(P16, P16, P16, None, 8, 16, 16, _lib.NF_EPI_SWIGLU_FP8, 0, None))
 

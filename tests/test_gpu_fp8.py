@@ -324,6 +324,19 @@ def test_gemm_grid_limits_change_nothing(m, max_sms):
     assert torch.equal(p.c, want)
 
 
+@pytest.mark.parametrize("epi", [STORE, RESID, SWIGLU, SWIGLU8])
+@pytest.mark.parametrize("m,n,k", [(700, 1040, 400), (129, 4112, 144), (1030, 528, 1040)])
+def test_many_tiles_a_cta(m, n, k, epi):
+    """Few CTAs walk many tiles: rings, accumulators and the exchange of the largest values go on across tiles."""
+    p = Product(m, n, k, epi)
+    p.run(max_sms=3)
+    _lib.fp8_poll()
+    p.check()
+    want = p.c.float().clone()
+    p.run(max_sms=2)
+    assert torch.equal(p.c.float(), want)
+
+
 def offsets(counts, first=0):
     return torch.tensor(np.concatenate([[first], first + np.cumsum(counts)]), dtype=I32, device=DEV)
 
@@ -348,6 +361,18 @@ def test_grouped(counts, n, k, epi):
     for rows in (slice(0, first), slice(m - tail, m)):
         assert (p.c[rows].float() == 5).all()
         assert p.c_s is None or (p.c_s[:, rows] == 3).all()
+
+
+@pytest.mark.parametrize("epi", [STORE, SWIGLU8])
+def test_grouped_many_tiles_a_cta(epi):
+    counts = [130, 0, 257, 3, 128, 40]
+    p = Product(sum(counts), 528, 656, epi, groups=len(counts))
+    p.run(offsets(counts), max_sms=3)
+    at = 0
+    for e, c in enumerate(counts):
+        if c:
+            p.check(at, at + c, e)
+        at += c
 
 
 @pytest.mark.parametrize("m", [40, 500])
@@ -468,6 +493,61 @@ def test_binding_refuses_tensors_of_another_place():
     with pytest.raises(ValueError, match="cpu"):
         p.b = p.b.cpu()
         p.run()
+
+
+@pytest.mark.parametrize("limit", [1, 500, 2000, 20000])
+@pytest.mark.parametrize("m,n,epi,groups", [(5, 1024, STORE, 0), (64, 512, SWIGLU8, 0), (300, 512, RESID, 0), (700, 5200, SWIGLU8, 0), (900, 528, STORE, 3), (12, 528, SWIGLU, 3)])
+def test_limits_shorter_than_the_waits(m, n, epi, groups, limit):
+    """A wait that gives up is reported once, or nothing gave up and the result is right; the next call is as ever."""
+    p = Product(m, n, 2064, epi, groups=groups)
+    off = offsets([m // 3] * 3) if groups else None
+    rows = m // 3 * 3 if groups else m
+    want = p.run(off)[0].float().clone()
+    _lib.fp8_poll()
+    try:
+        _lib.fp8_set_timeout(limit)
+        p.run(off)
+        try:
+            _lib.fp8_poll()
+            assert torch.equal(p.c.float()[:rows], want[:rows])
+        except _lib.NanoflowError as e:
+            assert e.code == _lib.NF_ERR_TIMEOUT
+    finally:
+        _lib.fp8_set_timeout(2_000_000_000)
+    _lib.fp8_poll()
+    p.run(off)
+    _lib.fp8_poll()
+    assert torch.equal(p.c.float()[:rows], want[:rows])
+
+
+def test_first_call_of_a_process_in_a_capture():
+    """Nothing is allocated or looked up that a capture forbids."""
+    code = """
+import torch
+from nano_intra_device_gb300 import _lib
+e = torch.float8_e4m3fn
+x = torch.randn(200, 256, device="cuda").bfloat16()
+q, s, c = torch.zeros(200, 256, device="cuda").to(e), torch.zeros(2, 200, device="cuda"), torch.zeros(200, 128, device="cuda").bfloat16()
+w, ws, d = torch.zeros(128, 256, device="cuda").to(e), torch.ones(1, 2, device="cuda"), torch.ones(3, 128, device="cuda").bfloat16()
+w.view(torch.uint8).fill_(0x38)  # ones
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    _lib.quant_fp8(x, q, s)
+    _lib.gemm_fp8(q, s, w, ws, c)
+    _lib.gemm_fp8(q[:3], s[:, :3].contiguous(), w, ws, d)
+g.replay()
+torch.cuda.synchronize()
+_lib.fp8_poll()
+want = x.float().sum(1, keepdim=True)
+assert (c.float() - want).abs().max() < 4, (c.float() - want).abs().max()
+print("captured")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 # ------------------------------------------------------------------ together
