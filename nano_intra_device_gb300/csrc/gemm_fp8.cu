@@ -12,6 +12,16 @@
 //    registers.  While they do, the tensor core fills the other accumulators.
 //  * Warp 0 loads tiles by TMA, warps 1 and 2 issue the products of a half each, warp 3
 //    copies the scales beside the tiles, warps 4 to 11 sum and run the epilogue.  Persistent CTAs, one an SM.
+//  * What bounds it: the hand-over between products and sums.  A block of K is 528 cycles
+//    of products (two halves of four instructions), but a half's accumulator goes issue,
+//    completion, sums' loads, release, issue, some 1500 cycles for two blocks; about 800
+//    cycles a block are reached, 57 % of the tensor pipe.  In long runs the power limit
+//    counts as well: 4096 x 8192 x 28672 takes 700 us (2.7 PFLOP/s) for the first dozens of
+//    calls and 795 us (1590 MHz, 1360 W) after seconds.  Measured and not kept, on that
+//    product at 711: one issuing warp for both halves 946, one for each accumulator 748,
+//    sixteen summing warps of 64 columns 718, the next block's loads ahead of this one's
+//    last sums 890, packed pairs of sums 893 (moves), one hand-over for all 256 columns
+//    884, B multicast to two CTAs 703 (shorter products 4 to 7 % slower).
 //  * A product with tiles for less than half of the SMs is cut along K between the two
 //    CTAs of a cluster (SPLIT): each finishes a half of the tile's columns, with the
 //    other's sums from its shared memory.
@@ -488,7 +498,9 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
                          ((args.N + tn - 1) / tn);
   if (most > 0x7fffffffLL || args.groups > F8_MAX_GROUPS) return cudaErrorInvalidValue;
   if (most <= 0) return cudaSuccess;
-  // Tiles for less than half of the SMs, and four blocks of K at least for each of two CTAs
+  // Tiles for less than half of the SMs, and four blocks of K at least for each of two
+  // CTAs.  Whole / cut: 333 x 6144 x 4096 18.2 / 16.7 us, 333 x 4096 x 14336 51.5 / 34.9,
+  // 256 x 8192 x 28672 99 / 62.6; 8 blocks of K, 512 x 2048 x 2048, 12 either way.
   if (!args.group_off && 2 * most <= sms && (args.K + BK - 1) / BK >= 8) {
     const int grid = static_cast<int>(2 * most);
     if (epi == F8_STORE) return launch<F8_STORE, true>(tmA, tmB, args, grid, stream);
