@@ -625,8 +625,9 @@ nf_status nf_quant_fp8_weights(const void* w, void* q, float* s, int32_t mats, i
  *   device bf16 [M, N].  SwiGLU: B holds 2 N rows, gate rows then up rows, each
  *   a matrix of its own scales: b_s [2][ceil(N / 128)][ceil(K / 128)].
  *   NF_EPI_SWIGLU_FP8: the SwiGLU's fp32 values to 8-bit rows without a rounding
- *   between, C device e4m3 [M, N], c_s [ceil(N / 128)][M]; c_s is not used by
- *   the others.
+ *   between (y / s as a product with 1 / s: off the nearest code where it lies
+ *   within 2^-22 of a border), C device e4m3 [M, N], c_s [ceil(N / 128)][M]; c_s
+ *   is not used by the others.
  * K a multiple of 16, N of 8 (NF_EPI_SWIGLU_FP8: of 16); M = 0 does nothing.
  * C must not overlap A or B; C = R is allowed.  The product of a row's and a
  * column's scale has to stay within fp32's range.  A NaN scale makes NaN of its

@@ -2,6 +2,7 @@
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 
 #include "../../include/nanoflow.h"
 #include "fp8.h"
@@ -205,6 +206,9 @@ nf_status nf_fp8_set_timeout(int64_t timeout_ns) {
 }
 
 nf_status nf_fp8_poll(void* stream) {
+  // one poll at a time: they share the words that the status is taken into
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
   uint32_t bits = 0, more = 0;
   NF_CUDA8(nf::take_gemm_f8_status(&bits, static_cast<cudaStream_t>(stream)));
   NF_CUDA8(nf::take_gemm_f8_wrows_status(&more, static_cast<cudaStream_t>(stream)));

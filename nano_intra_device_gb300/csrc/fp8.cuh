@@ -1,5 +1,5 @@
-// Device-side helpers of the 8-bit operators: e4m3 products on tcgen05, packed
-// fp32 arithmetic, the scale of a block and its codes.
+// Device-side helpers of the 8-bit operators: e4m3 products on tcgen05, copies and
+// arrivals, the scale of a block and its codes, SwiGLU, launches.
 #pragma once
 #include <cuda_fp8.h>
 
@@ -34,6 +34,14 @@ __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[1
       : "r"(taddr)
       : "memory");
 }
+// The cluster barrier in two halves, for threads that diverge in between.  Relaxed: it
+// orders execution alone (barriers made before it are published by fence_mbar_init).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 // 16 bytes of a CTA of the cluster, by shared::cluster address.
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
@@ -57,25 +65,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Two fp32 values a register pair: one instruction for both.  Volatile: an
-// accumulator read from tensor memory must not be used ahead of the wait for it.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack_f32x2(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 pack_b32x2(uint32_t a, uint32_t b) {
-  f32x2 r;
-  asm volatile("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack_f32x2(f32x2 v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ void fma_f32x2(f32x2& d, f32x2 a, f32x2 b) {
-  asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
 // One arrival of the lanes for which `yes` holds, without a branch.
 __device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool yes) {
   asm volatile(
@@ -94,7 +83,8 @@ __device__ __forceinline__ void copy4(float* dst, const float* src, bool there) 
 __device__ __forceinline__ void mbar_arrive_copied(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// d += a b, a a value read from tensor memory.
+// d += a b, a a value read from tensor memory.  Volatile: it must not be used ahead of
+// the wait for its load.
 __device__ __forceinline__ void fma_loaded(float& d, uint32_t a, float b) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "f"(__uint_as_float(a)), "f"(b));
 }
@@ -114,8 +104,8 @@ __device__ __forceinline__ float f8_scale(float top) {
 // gives the rounded quotient (P. Markstein, "Computation of elementary functions on the
 // IBM RISC System/6000 processor", 1990); where s < 2^-100 the remainder may underflow
 // and the quotient be an ulp off.  A block's values are often exact ties of codes (a
-// ratio of two 8-bit significands times 448), so the product alone would settle 1 code
-// in 500 of a bf16 tensor otherwise.
+// ratio of two 8-bit significands times 448): the product alone settles one code in 2000
+// of normal bf16 values otherwise.
 __device__ __forceinline__ float f8_quotient(float y, float s, float inv) {
   const float q = y * inv;
   return fmaf(fmaf(-q, s, y), inv, q);

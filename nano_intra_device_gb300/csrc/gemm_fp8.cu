@@ -147,7 +147,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (SPLIT) cluster_sync_all();  // the peer's barriers exist before anything arrives on them
+  if (SPLIT) {  // the peer's barriers exist before anything arrives on them
+    cluster_arrive();
+    cluster_wait();
+  }
   const uint32_t tmem_base = tail->tmem_base;
   volatile int* abort_flag = &tail->abort;
   const int total = grouped ? tail->tile0[args.groups] : (args.M + BM - 1) / BM * n_tiles;
@@ -350,10 +353,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               ring[i * BM + row_in_tile] = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
           }
           asm volatile("bar.sync 2, 128;" ::: "memory");
-          if (quarter == 0 && lane == 0) {
-            fence_acq_rel_cluster();
-            mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), rank ^ 1));
-          }
+          // (a release at cluster scope, behind the barrier that the group's writes precede)
+          if (quarter == 0 && lane == 0) mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), rank ^ 1));
           break;  // (one tile a cluster; !ok is reported below)
         }
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo)) && ok;
@@ -474,7 +475,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
-  if (SPLIT) cluster_sync_all();  // no CTA leaves while the peer may read its sums
+  if (SPLIT) {  // no CTA leaves while the peer may read its sums
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 __device__ uint32_t g_taken;

@@ -69,13 +69,6 @@ static_assert(sizeof(Tail) <= TAIL_BYTES, "barrier block");
 
 __device__ uint32_t g_status;
 
-// The two halves of cluster_sync_all, for threads that diverge in between.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
 template <int EPI, int TOK>
 __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     gemm_f8_wrows_kernel(const __grid_constant__ CUtensorMap tmW,
@@ -333,11 +326,8 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     }
     cluster_wait();  // every peer's barriers exist
     asm volatile("bar.sync 1, %0;" ::"n"(128 * C::HALVES) : "memory");
-    if (warp == 2 && lane == 0) {
-      fence_acq_rel_cluster();
-      const uint32_t at = smem_u32(&tail->ready);
-      for (int j = 0; j < S; ++j) mbar_arrive_remote(cluster_map(at, j));
-    }
+    // (a release at cluster scope, behind the barrier that all of the CTA's writes precede)
+    if (warp == 2 && lane < S) mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), lane));
     if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo))) {
       raise_status(&g_status, ST_TIMEOUT);
       *abort_flag = 1;
