@@ -91,7 +91,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int k0 = SPLIT ? rank * nk / 2 : 0, k1 = SPLIT ? (rank + 1) * nk / 2 : nk;
   const uint64_t tmo = args.timeout_ns;
 
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&tail->full[s], 1 + 32);  // the tiles, the scales' 32 lanes
@@ -109,11 +108,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
   }
+  pdl_wait();  // nothing before this reads or writes global memory
+  // Tensor memory is taken once the kernel ahead is complete, and the kernel behind let
+  // start once it is taken: neither can wait for columns that the other holds.
   if (warp == 1) {
     tmem_alloc(&tail->tmem_base, TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_wait();  // nothing before this reads or writes global memory
   if (warp == 2 && grouped) {
     // Rows and tiles of the groups.  Offsets are held within [0, M], and one below
     // the one before it counts as that one, so no offset leads out of a tensor.
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();
   if (SPLIT) {  // the peer's barriers exist before anything arrives on them
     cluster_arrive();
     cluster_wait();

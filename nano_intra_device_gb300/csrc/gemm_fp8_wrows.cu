@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
   const int nk = (args.K + BK - 1) / BK, nb = (args.N + F8_BLOCK - 1) / F8_BLOCK;
   const uint64_t tmo = args.timeout_ns;
 
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&tail->full[s], 1);
@@ -106,10 +105,6 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     prefetch_tensormap(&tmW);
     prefetch_tensormap(&tmX);
   }
-  if (warp == 1) {
-    tmem_alloc(&tail->tmem_base, C::TMEM);
-    tmem_relinquish();
-  }
   if (threadIdx.x == 0 && !args.group_off) {
     // the first blocks of B are on their way from memory while the kernel ahead ends
     const int w = unit / ((args.M + TOK - 1) / TOK), a = rank * nk / S, n = (rank + 1) * nk / S - a;
@@ -121,6 +116,12 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     }
   }
   pdl_wait();  // nothing before this reads or writes global memory but into L2
+  // Tensor memory is taken once the kernel ahead is complete, and the kernel behind let
+  // start once it is taken: neither can wait for columns that the other holds.
+  if (warp == 1) {
+    tmem_alloc(&tail->tmem_base, C::TMEM);
+    tmem_relinquish();
+  }
   if (warp == 2) {
     if (!args.group_off) {
       if (lane == 0) {
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();
   cluster_arrive();  // this CTA's barriers exist; each thread waits for the peers' further down
   const uint32_t tmem_base = tail->tmem_base;
   volatile int* abort_flag = &tail->abort;
@@ -419,7 +421,7 @@ void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, int clusters, i
   at[0].val.clusterDim.x = static_cast<unsigned>(splits);
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
-  // its barriers and tensor memory are made while the kernel ahead ends
+  // its barriers are made while the kernel ahead ends
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg->attrs = at;
