@@ -37,9 +37,13 @@ constexpr int BM = 128, BN = 256, BK = F8_BLOCK;
 constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int THREADS = 384;
-// Registers: 384 threads start with 168 each (64,512); the first warpgroup keeps 72,
-// the summing warps take 208: 4 * 32 * 72 + 8 * 32 * 208 = 62,464.
-constexpr int REGS_FEW = 72, REGS_SUM = 208;
+// Registers: 384 threads start with 168 each (64,512); the first warpgroup keeps 40 (SPLIT:
+// 72), the summing warps take 224 (208): 4 * 32 * 40 + 8 * 32 * 224 = 62,464, and as many
+// with 72 and 208.  40 / 224 against 72 / 208: 2048 x 14336 x 4096 to 8 bits 180 / 189 us,
+// 4096 x 8192 x 28672 704 / 706; 333 x 6144 x 4096 cut along K 17.6 / 16.4.  With 56 / 216 or
+// 64 / 208 the compiler moves sums about: 4096 x 8192 x 28672 836 and 760.
+constexpr int regs_few(bool split) { return split ? 72 : 40; }
+constexpr int regs_sum(bool split) { return split ? 208 : 224; }
 constexpr int TMEM_COLS = 512;
 constexpr int STORE_BYTES = 2048;  // of a summing warp: 32 rows x 64 bytes of output
 constexpr int TAIL_BYTES = 8192;
@@ -54,6 +58,10 @@ struct Tail {
   uint64_t ready;      // SPLIT: the peer's sums are in its shared memory
   uint32_t tmem_base;
   int abort;
+  // for a drain after a wait gave up: the ring's stages and the phase of their last load,
+  // the lanes that issue products (32: none issued)
+  uint32_t issued, phases;
+  int issuer[2];
   int tile0[F8_MAX_GROUPS + 1];  // first tile of each group
   int row0[F8_MAX_GROUPS + 1];   // first row of each group
   float a_s[8][BM];       // scales of the next blocks of K: of A's rows,
@@ -179,12 +187,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     return x;
   };
 
-  uint32_t issued = 0, phases = 0;  // thread 0: the ring's stages and the phase of their last load
-  bool issuer = false;              // this thread has issued products
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FEW));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(regs_few(SPLIT)));
     if (warp == 0 && lane == 0) {
-      uint32_t st = 0, ph = 0;
+      uint32_t st = 0, ph = 0, issued = 0, phases = 0;  // the stages, and the phase of their last load
       bool ok = true;
       for (int u = first; u < total && ok; u += stride) {
         const Tile x = decode(u);
@@ -215,6 +221,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
+      tail->issued = issued;
+      tail->phases = phases;
       if (!ok) {
         raise_status(&g_status, ST_TIMEOUT);
         *abort_flag = 1;
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         raise_status(&g_status, ST_TIMEOUT);
         *abort_flag = 1;
       }
-      issuer = one && any;
+      if (one) tail->issuer[h] = any ? lane : 32;
     }
     if (warp == 3) {
       // Scales, copied beside the tiles: a slot is filled again 8 blocks of K later, when
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SUM));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(regs_sum(SPLIT)));
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int row_in_tile = quarter * 32 + lane;
     uint8_t* mine = smem + STAGES * STAGE_BYTES + (warp - 4) * STORE_BYTES;
@@ -464,13 +472,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (*abort_flag) {
     // Whoever gave up: products in flight end before tensor memory goes away, loads land
     // before shared memory does.
-    if (issuer) {
+    if ((warp == 1 || warp == 2) && lane == tail->issuer[warp - 1]) {
       tc_commit(&tail->drain[warp - 1]);
       mbar_wait(&tail->drain[warp - 1], 0, F8_DRAIN_NS);
     }
     if (threadIdx.x == 0)
       for (int s = 0; s < STAGES; ++s)
-        if (issued & (1u << s)) mbar_wait(&tail->full[s], phases >> s & 1, F8_DRAIN_NS);
+        if (tail->issued & (1u << s)) mbar_wait(&tail->full[s], tail->phases >> s & 1, F8_DRAIN_NS);
     __syncthreads();
   }
   if (warp == 1) {
