@@ -453,6 +453,33 @@ def test_two_streams_at_once_and_a_graph(m, groups):
         assert torch.equal(c[:m // 3 * 2].view(torch.uint8), p.c[:m // 3 * 2].view(torch.uint8))
 
 
+def test_two_threads_at_once():
+    """Calls from two host threads, each on a stream of its own."""
+    import threading
+    ps = [Product(9, 528, 1040, SWIGLU8, seed=3), Product(300, 520, 2064, STORE, seed=4)]
+    want = [p.run()[0].float().clone() for p in ps]
+    outs, errors = [[], []], []
+
+    def work(i):
+        try:
+            st, p = torch.cuda.Stream(), ps[i]
+            for _ in range(30):
+                c = torch.zeros_like(p.c.float()).to(p.c.dtype)
+                st.wait_stream(torch.cuda.current_stream())
+                outs[i].append(p.run(None, c, None if p.c_s is None else torch.zeros_like(p.c_s), stream=st)[0])
+            st.synchronize()
+        except Exception as e:  # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert not errors
+    for i in range(2):
+        assert len(outs[i]) == 30 and all(torch.equal(c.float(), want[i]) for c in outs[i])
+
+
 def test_results_repeat_bit_for_bit():
     for m, k in ((1, 14336), (40, 8192), (700, 1024)):
         p = Product(m, 1024, k, STORE)
