@@ -465,7 +465,8 @@ cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const F8GemmA
   return cudaLaunchKernelEx(&cfg, gemm_f8_wrows_kernel<EPI, TOK>, tmW, tmX, args);
 }
 
-// Clusters of `splits` CTAs that the device holds at once; asked once a process.
+// Clusters of `splits` CTAs that the device holds at once, one CTA an SM (more is not
+// reported for kernels with tensor memory); asked once a process.
 template <int EPI, int TOK>
 int most_clusters(int splits) {
   static std::atomic<int> cache[MAX_CLUSTER + 1];
@@ -519,12 +520,18 @@ F8RowsChoice gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups) {
   c.tok = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 || most == 64 ? 64 : 128;
   const long long wt = (N + WM - 1) / WM;
   c.units = groups > 1 ? wt * (M / c.tok + (M < groups ? M : groups)) : wt * ((M + c.tok - 1) / c.tok);
-  // As many CTAs as the device holds at once, but four blocks of K each at least.
+  // As many CTAs as the device holds at once, but four blocks of K each at least.  Where an
+  // SM holds two, for one / both: 1 row of 4096 x 14336 15.3 / 14.3 us, of 10240 x 4096
+  // 14.7 / 10.0, of 10240 x 14336 40.6 / 26.5, 64 rows of 14336 x 4096 18.3 / 15.1, 16 rows of
+  // 14336 x 4096 SwiGLU 24.8 / 22.9.
   const long long busy = wt * (groups > 1 ? (M < groups ? M : groups) : (M + c.tok - 1) / c.tok);
   const int nk = (K + BK - 1) / BK;
   c.splits = 1;
   for (int s = 2; s <= MAX_CLUSTER && 4 * s <= nk; ++s)
-    if (busy <= dispatch(epi, c.tok, [&](auto e, auto k) { return most_clusters<decltype(e)::value, decltype(k)::value>(s); }))
+    if (busy <= dispatch(epi, c.tok, [&](auto e, auto k) {
+          constexpr int EPI = decltype(e)::value, TOK = decltype(k)::value;
+          return Cfg<EPI, TOK>::PER_SM * most_clusters<EPI, TOK>(s);
+        }))
       c.splits = s;
   return c;
 }
