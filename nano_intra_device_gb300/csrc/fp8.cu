@@ -47,17 +47,30 @@ nf_status check_rows(int32_t rows, int32_t cols, const char* what) {
   return NF_OK;
 }
 
-// Whether a product goes to the kernel of few rows of A.  Measured, few rows against
-// tiles of 128 rows, us: 4096 x 14336, 1 row 15.6 / 33, 128 rows 20.5 / 34, 256 32.5 / 35;
-// 6144 x 4096, 128 rows 13.9 / 16, 256 20.4 / 16.4.  SwiGLU's two matrices make wide
-// tiles (128 features of both) enough for the GPU sooner: 14336 x 4096, 1 row 24 / 33, 16
-// rows 25.7 / 31, 32 rows 28.2 / 25.1.  Groups, by their mean: 8 of 14336 x 4096 SwiGLU, 8
-// rows 142 / 147, 16 rows 149 / 149, 32 rows 174 / 151; 8 of 4096 x 14336, 16 rows 75 / 77,
-// 32 rows 78 / 78, 48 rows 104 / 78.  A capped product takes the tiles, which loop.
-bool few_rows(int M, int N, int groups, bool two, int sms) {
+// Whether a product goes to the kernel of few rows of A, which fills the GPU by cutting K
+// (the fewer tiles of weights, the more rows), or to tiles of 128 rows x 256, which read the
+// weights once for all rows.  Few rows / tiles, us, K 4096, by tiles of 128 weight rows:
+//   64 (8192): 64 rows 10.7 / 15.7, 128 rows 13.1 / 16.2; 256 rows of 6144 15.7 / 15.7;
+//   112 (14336): 64 rows 14.9 / 17.4, 128 rows 19.4 / 17.9;
+//   224 (28672): 16 rows 23.2 / 30.2, 32 rows 23.5 / 23.5, 64 rows 25.1 / 24.1;
+//   224 (SwiGLU, 14336): 32 rows 23.5 / 24.0, 64 rows 26.0 / 24.0;
+//   1002 (128256): 16 rows 88 / 101, 32 rows 97 / 88.
+// By groups, with the rows' mean (a tile has room for twice as many, of SwiGLU for 64):
+//   8 of 1024 x 4096 (64): 64 rows 13.4 / 19.0; SwiGLU, 8 of 512 (64): 32 rows 12.4 / 19.3, 64
+//   rows 22.0 / 19.5; 8 of 2048 (128): 32 rows 16.4 / 19.9, 64 rows 20.0 / 20.4;
+//   8 of 14336 x 4096 SwiGLU: 1 row 75 / 94, 8 rows 142 / 143, 32 rows 170 / 146;
+//   64 of 2048 x 2048: 0.5 rows 26.6 / 27.4, 1 row 40 / 36, 8 rows 58 / 49 (a CTA a tile: short
+//   ones do not pay); 64 of 768 x 2048: 1 row 15.7 / 16.0, 2 rows 25.8 / 24.3.
+// A capped product takes the tiles, which loop.
+bool few_rows(int M, int N, int K, int groups, bool two, int sms) {
   const int rows = (M + groups - 1) / groups;
-  if (groups > 1 || (two && (N + 127) / 128 * 3 >= 2 * sms)) return rows <= 16;
-  return rows <= 128;
+  const int64_t ops = two ? 2 : 1;
+  const int64_t tiles = (N + 127LL) / 128 * ops * (M < groups ? M : groups);
+  if (groups > 1) {
+    if (tiles > sms) return rows <= 16 && (M <= groups || K * ops >= 8192);
+    return rows <= (tiles <= sms / 2 && !two ? 64 : 32);
+  }
+  return rows <= (tiles <= sms / 2 ? 128 : tiles <= sms ? 64 : tiles <= 2 * sms ? 32 : 16);
 }
 
 // The product's checks, for one matrix (group_off NULL, groups 1) or by groups.
@@ -86,7 +99,7 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
   const int sms = sm_count();
   if (sms <= 0) return fail8(NF_ERR_CUDA, "no CUDA device");
   const bool capped = max_sms > 0 && max_sms < sms;
-  const bool few = !capped && few_rows(M, N, groups, two, sms);
+  const bool few = !capped && few_rows(M, N, K, groups, two, sms);
   nf::F8RowsChoice c{};
   if (few) c = nf::gemm_f8_wrows_choice(epilogue, M, N, K, groups);
   CUtensorMap ta, tb;

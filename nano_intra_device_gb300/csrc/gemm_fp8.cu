@@ -512,10 +512,10 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
                          ((args.N + tn - 1) / tn);
   if (most > 0x7fffffffLL || args.groups > F8_MAX_GROUPS) return cudaErrorInvalidValue;
   if (most <= 0) return cudaSuccess;
-  // Tiles for less than half of the SMs, and four blocks of K at least for each of two
-  // CTAs.  Whole / cut: 333 x 6144 x 4096 18.2 / 16.7 us, 333 x 4096 x 14336 51.5 / 34.9,
-  // 256 x 8192 x 28672 99 / 62.6; 8 blocks of K, 512 x 2048 x 2048, 12 either way.
-  if (!args.group_off && 2 * most <= sms && (args.K + BK - 1) / BK >= 8) {
+  // Tiles for less than half of the SMs, and eight blocks of K at least for each of two
+  // CTAs.  Whole / cut: 333 x 6144 x 4096 18.4 / 16.5 us, 333 x 4096 x 14336 49 / 32,
+  // 256 x 8192 x 28672 95 / 60; 512 x 2048 x 2048 11.5 either way, x 1024 8.4 / 9.5.
+  if (!args.group_off && 2 * most <= sms && (args.K + BK - 1) / BK >= 16) {
     const int grid = static_cast<int>(2 * most);
     if (epi == F8_STORE) return launch<F8_STORE, true>(tmA, tmB, args, grid, stream);
     if (epi == F8_RESID) return launch<F8_RESID, true>(tmA, tmB, args, grid, stream);

@@ -270,6 +270,29 @@ def test_gemm(m, n, k, epi):
     p.check()
 
 
+@pytest.mark.parametrize("epi", [STORE, RESID, SWIGLU8])
+@pytest.mark.parametrize("m,n,k", [(1, 10256, 1040), (40, 12304, 528), (65, 12304, 528), (20, 24592, 400), (33, 24592, 144), (17, 40016, 80)])
+def test_gemm_few_rows_many_columns(m, n, k, epi):
+    """Around the bounds of the kernel for few rows: two CTAs an SM, and more tiles than the GPU holds at once."""
+    p = Product(m, n, k, epi)
+    p.run()
+    _lib.fp8_poll()
+    p.check()
+
+
+@pytest.mark.parametrize("epi", [STORE, SWIGLU8])
+@pytest.mark.parametrize("counts,n,k", [([70, 0, 64, 33, 90], 272, 2064), ([40, 20, 33], 528, 1040), ([1, 130, 2], 144, 1040), ([16] * 16 + [0] * 4, 2064, 528)])
+def test_grouped_rows_between(counts, n, k, epi):
+    p = Product(sum(counts), n, k, epi, groups=len(counts))
+    p.run(offsets(counts))
+    _lib.fp8_poll()
+    at = 0
+    for e, c in enumerate(counts):
+        if c:
+            p.check(at, at + c, e)
+        at += c
+
+
 @pytest.mark.parametrize("epi", [STORE, SWIGLU8])
 @pytest.mark.parametrize("m", [5, 300])
 def test_gemm_of_every_code(m, epi):
