@@ -50,7 +50,7 @@ nf_status check_rows(int32_t rows, int32_t cols, const char* what) {
 // Whether a product goes to the kernel of few rows of A, which fills the GPU by cutting K
 // (the fewer tiles of weights, the more rows), or to tiles of 128 rows x 256, which read the
 // weights once for all rows.  Few rows / tiles, us, K 4096, by tiles of 128 weight rows:
-//   64 (8192): 64 rows 10.7 / 15.7, 128 rows 13.1 / 16.2; 256 rows of 6144 15.7 / 15.7;
+//   64 (8192): 64 rows 10.7 / 15.7, 128 rows 13.1 / 16.2; 256 rows of 6144 18.8 / 15.0;
 //   112 (14336): 64 rows 14.9 / 17.4, 128 rows 19.4 / 17.9;
 //   224 (28672): 16 rows 23.2 / 30.2, 32 rows 23.5 / 23.5, 64 rows 25.1 / 24.1;
 //   224 (SwiGLU, 14336): 32 rows 23.5 / 24.0, 64 rows 26.0 / 24.0;

@@ -22,9 +22,9 @@
 //    sixteen summing warps of 64 columns 718, the next block's loads ahead of this one's
 //    last sums 890, packed pairs of sums 893 (moves), one hand-over for all 256 columns
 //    884, B multicast to two CTAs 703 (shorter products 4 to 7 % slower).
-//  * A product with tiles for less than half of the SMs is cut along K between the two
-//    CTAs of a cluster (SPLIT): each finishes a half of the tile's columns, with the
-//    other's sums from its shared memory.
+//  * A product with tiles for less than a half (a quarter) of the SMs is cut along K between
+//    the two (four) CTAs of a cluster (SPLIT): each finishes its part of the tile's columns,
+//    with the others' sums from their shared memory.
 //  * Every wait is bounded; one that gives up flags the status word, and the kernel
 //    drains what it has in flight (bounded) and frees tensor memory.
 #include "fp8.cuh"
@@ -40,8 +40,9 @@ constexpr int THREADS = 384;
 // Registers: 384 threads start with 168 each (64,512); the first warpgroup keeps 40 (SPLIT:
 // 72), the summing warps take 224 (208): 4 * 32 * 40 + 8 * 32 * 224 = 62,464, and as many
 // with 72 and 208.  40 / 224 against 72 / 208: 2048 x 14336 x 4096 to 8 bits 180 / 189 us,
-// 4096 x 8192 x 28672 704 / 706; 333 x 6144 x 4096 cut along K 17.6 / 16.4.  With 56 / 216 or
-// 64 / 208 the compiler moves sums about: 4096 x 8192 x 28672 836 and 760.
+// 4096 x 8192 x 28672 704 / 706; 333 x 6144 x 4096 cut along K 16.9 / 15.6, 333 x 4096 x 14336
+// 36.9 / 30.4.  With 56 / 216 or 64 / 208 the compiler moves sums about: 4096 x 8192 x 28672
+// 836 and 760, 333 x 4096 x 14336 38.6 with 56 / 216.
 constexpr int regs_few(bool split) { return split ? 72 : 40; }
 constexpr int regs_sum(bool split) { return split ? 208 : 224; }
 constexpr int TMEM_COLS = 512;
@@ -55,7 +56,7 @@ struct Tail {
   uint64_t tempty[4];
   uint64_t pair[4];    // the two warps of 32 rows (SWIGLU8: the block's largest value)
   uint64_t drain[2];
-  uint64_t ready;      // SPLIT: the peer's sums are in its shared memory
+  uint64_t ready;      // SPLIT: all CTAs' sums are in their shared memory
   uint32_t tmem_base;
   int abort;
   // for a drain after a wait gave up: the ring's stages and the phase of their last load,
@@ -77,8 +78,8 @@ struct Tile {
   int m0, m_lim, tn, e;
 };
 
-// SPLIT: the two CTAs of a cluster take a half of K each of one tile (see the header).
-template <int EPI, bool SPLIT>
+// SPLIT: CTAs of a cluster that take a part of K each of one tile (see the header).
+template <int EPI, int SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_f8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const F8GemmArgs args) {
@@ -94,9 +95,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int nk = (args.K + BK - 1) / BK, n_tiles = (args.N + TN - 1) / TN;
   const int nb = (args.N + F8_BLOCK - 1) / F8_BLOCK;
   const bool grouped = args.group_off != nullptr;
-  const int rank = SPLIT ? static_cast<int>(cluster_rank()) : 0;
-  const int first = SPLIT ? blockIdx.x / 2 : blockIdx.x, stride = SPLIT ? gridDim.x / 2 : gridDim.x;
-  const int k0 = SPLIT ? rank * nk / 2 : 0, k1 = SPLIT ? (rank + 1) * nk / 2 : nk;
+  const int rank = SPLIT > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int first = blockIdx.x / SPLIT, stride = gridDim.x / SPLIT;
+  const int k0 = rank * nk / SPLIT, k1 = (rank + 1) * nk / SPLIT;
   const uint64_t tmo = args.timeout_ns;
 
   if (threadIdx.x == 0) {
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&tail->tempty[a], 4);
     }
     for (int a = 0; a < 2; ++a) mbar_init(&tail->drain[a], 1);
-    mbar_init(&tail->ready, 1);
+    mbar_init(&tail->ready, SPLIT);
     for (int a = 0; a < 4; ++a) mbar_init(&tail->pair[a], 2);
     tail->abort = 0;
     fence_mbar_init();
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
-  if (SPLIT) {  // the peer's barriers exist before anything arrives on them
+  if (SPLIT > 1) {  // the peers' barriers exist before anything arrives on them
     cluster_arrive();
     cluster_wait();
   }
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(regs_few(SPLIT)));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(regs_few(SPLIT > 1)));
     if (warp == 0 && lane == 0) {
       uint32_t st = 0, ph = 0, issued = 0, phases = 0;  // the stages, and the phase of their last load
       bool ok = true;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(regs_sum(SPLIT)));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(regs_sum(SPLIT > 1)));
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int row_in_tile = quarter * 32 + lane;
     uint8_t* mine = smem + STAGES * STAGE_BYTES + (warp - 4) * STORE_BYTES;
@@ -351,35 +352,45 @@ __global__ void __launch_bounds__(THREADS, 1)
           aph ^= 1;
         }
       }
-      if (SPLIT) {
-        // Both halves' products have read the ring, which now takes the sums that the peer
-        // finishes: four columns of a row together, rows next to one another.
+      if (SPLIT > 1) {
+        // Both halves' products have read the ring, which now takes the sums, four columns of
+        // a row together, rows next to one another.  A CTA finishes its part of each half's
+        // columns, with all CTAs' sums in their order (a load takes about a microsecond: all
+        // 32 at once).
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        float4* ring = reinterpret_cast<float4*>(smem);
-        if (half != rank) {
-          if (ok) {
+        float4* ring = reinterpret_cast<float4*>(smem) + half * 32 * BM + row_in_tile;
+        if (ok) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              ring[i * BM + row_in_tile] = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
-          }
-          asm volatile("bar.sync 2, 128;" ::: "memory");
-          // (a release at cluster scope, behind the barrier that the group's writes precede)
-          if (quarter == 0 && lane == 0) mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), rank ^ 1));
-          break;  // (one tile a cluster; !ok is reported below)
+          for (int i = 0; i < 32; ++i)
+            ring[i * BM] = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
         }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        // (a release at cluster scope, behind the barrier that all of the CTA's writes precede)
+        if (warp == 4 && lane < SPLIT) mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), lane));
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo)) && ok;
         if (!ok) break;
-        const uint32_t peer = cluster_map(smem_u32(ring + row_in_tile), rank ^ 1);
+        constexpr int OPS = SW ? 2 : 1, PART = 32 / OPS / SPLIT;  // of a row's float4s, of each operand
+        float4 w[SPLIT][OPS * PART];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {  // (a load takes about a microsecond: many at once)
-          float4 w[16];
+        for (int r = 0; r < SPLIT; ++r) {
+          const uint32_t at = cluster_map(smem_u32(ring + rank * PART * BM), r);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = ld_cluster_f4(peer + (b * 16 + i) * (BM * 16));
+          for (int i = 0; i < OPS * PART; ++i)
+            w[r][i] = ld_cluster_f4(at + (i / PART * (32 / OPS) + i % PART) * (BM * 16));
+        }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float* d = sum + (b * 16 + i) * 4;
-            d[0] += w[i].x; d[1] += w[i].y; d[2] += w[i].z; d[3] += w[i].w;
+        for (int i = 0; i < OPS * PART; ++i)
+#pragma unroll
+          for (int r = 1; r < SPLIT; ++r) {
+            w[0][i].x += w[r][i].x; w[0][i].y += w[r][i].y; w[0][i].z += w[r][i].z; w[0][i].w += w[r][i].w;
           }
+#pragma unroll
+        for (int i = 0; i < PART; ++i) {
+          const float4 a = w[0][i], b = w[0][SW ? PART + i : i];
+          sum[4 * i] = SW ? silu_mul(a.x, b.x) : a.x;
+          sum[4 * i + 1] = SW ? silu_mul(a.y, b.y) : a.y;
+          sum[4 * i + 2] = SW ? silu_mul(a.z, b.z) : a.z;
+          sum[4 * i + 3] = SW ? silu_mul(a.w, b.w) : a.w;
         }
       }
       if (!ok) break;
@@ -421,9 +432,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       } else {
+        constexpr int WIDE = SW && SPLIT == 4 ? 16 : 32, CHUNKS = TN / 2 / SPLIT / WIDE;
 #pragma unroll
-        for (int h = 0; h < (SW ? 2 : 4); ++h) {
-          const int n0 = x.tn * TN + half * (TN / 2) + h * 32;
+        for (int h = 0; h < CHUNKS; ++h) {
+          const int n0 = x.tn * TN + half * (TN / 2) + (rank * CHUNKS + h) * WIDE;
           if (EPI == F8_RESID) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -436,12 +448,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < WIDE / 8; ++j) {
             float w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               w[i] = sum[h * 32 + j * 8 + i];
-              if (SW) w[i] = silu_mul(w[i], sum[64 + h * 32 + j * 8 + i]);
+              if (SW && SPLIT == 1) w[i] = silu_mul(w[i], sum[64 + h * 32 + j * 8 + i]);
             }
             if (EPI == F8_RESID) {
               const uint4 r = *slot(lane, j);
@@ -454,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = i * 8 + lane / 4, j = lane % 4, n = n0 + 8 * j;
-            if (mw + r < x.m_lim && n < args.N)
+            if (mw + r < x.m_lim && n < args.N && 8 * j < WIDE)
               *reinterpret_cast<uint4*>(args.C + static_cast<size_t>(mw + r) * args.N + n) = *slot(r, j);
           }
           __syncwarp();
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
-  if (SPLIT) {  // no CTA leaves while the peer may read its sums
+  if (SPLIT > 1) {  // no CTA leaves while a peer may read its sums
     cluster_arrive();
     cluster_wait();
   }
@@ -494,13 +506,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 __device__ uint32_t g_taken;
 __global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0u); }
 
-template <int EPI, bool SPLIT>
+template <int EPI, int SPLIT>
 cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const F8GemmArgs& args, int grid,
                    cudaStream_t stream) {
   const auto kernel = gemm_f8_kernel<EPI, SPLIT>;
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), SMEM);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, grid, THREADS, SMEM, stream, SPLIT ? 2 : 1, tmA, tmB, args);
+  return launch_dependent(kernel, grid, THREADS, SMEM, stream, SPLIT, tmA, tmB, args);
 }
 
 }  // namespace
@@ -513,20 +525,27 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
   if (most > 0x7fffffffLL || args.groups > F8_MAX_GROUPS) return cudaErrorInvalidValue;
   if (most <= 0) return cudaSuccess;
   // Tiles for less than half of the SMs, and eight blocks of K at least for each of two
-  // CTAs.  Whole / cut: 333 x 6144 x 4096 18.4 / 16.5 us, 333 x 4096 x 14336 49 / 32,
-  // 256 x 8192 x 28672 95 / 60; 512 x 2048 x 2048 11.5 either way, x 1024 8.4 / 9.5.
+  // CTAs.  Whole / cut: 333 x 6144 x 4096 18.4 / 15.8 us, 333 x 4096 x 14336 49 / 31,
+  // 256 x 8192 x 28672 95 / 60; 512 x 2048 x 2048 11.5 either way, x 1024 8.4 / 9.5.  For less
+  // than a quarter of the SMs four; two / four: 256 x 4096 x 14336 35 / 24, 256 x 4096 x 4096
+  // 14.4 either way, x 2048 11.4 / 12.5, 256 x 2048 x 4096 SwiGLU 15.5 / 13.6.
   if (!args.group_off && 2 * most <= sms && (args.K + BK - 1) / BK >= 16) {
     const int grid = static_cast<int>(2 * most);
-    if (epi == F8_STORE) return launch<F8_STORE, true>(tmA, tmB, args, grid, stream);
-    if (epi == F8_RESID) return launch<F8_RESID, true>(tmA, tmB, args, grid, stream);
-    if (epi == F8_SWIGLU) return launch<F8_SWIGLU, true>(tmA, tmB, args, grid, stream);
+    if (4 * most <= sms && (args.K + BK - 1) / BK >= 32) {
+      if (epi == F8_STORE) return launch<F8_STORE, 4>(tmA, tmB, args, 2 * grid, stream);
+      if (epi == F8_RESID) return launch<F8_RESID, 4>(tmA, tmB, args, 2 * grid, stream);
+      if (epi == F8_SWIGLU) return launch<F8_SWIGLU, 4>(tmA, tmB, args, 2 * grid, stream);
+    }
+    if (epi == F8_STORE) return launch<F8_STORE, 2>(tmA, tmB, args, grid, stream);
+    if (epi == F8_RESID) return launch<F8_RESID, 2>(tmA, tmB, args, grid, stream);
+    if (epi == F8_SWIGLU) return launch<F8_SWIGLU, 2>(tmA, tmB, args, grid, stream);
   }
   const int grid = static_cast<int>(most < sms ? most : sms);
   switch (epi) {
-    case F8_STORE: return launch<F8_STORE, false>(tmA, tmB, args, grid, stream);
-    case F8_RESID: return launch<F8_RESID, false>(tmA, tmB, args, grid, stream);
-    case F8_SWIGLU: return launch<F8_SWIGLU, false>(tmA, tmB, args, grid, stream);
-    case F8_SWIGLU8: return launch<F8_SWIGLU8, false>(tmA, tmB, args, grid, stream);
+    case F8_STORE: return launch<F8_STORE, 1>(tmA, tmB, args, grid, stream);
+    case F8_RESID: return launch<F8_RESID, 1>(tmA, tmB, args, grid, stream);
+    case F8_SWIGLU: return launch<F8_SWIGLU, 1>(tmA, tmB, args, grid, stream);
+    case F8_SWIGLU8: return launch<F8_SWIGLU8, 1>(tmA, tmB, args, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -270,6 +270,20 @@ def test_gemm(m, n, k, epi):
     p.check()
 
 
+@pytest.mark.parametrize("epi", [STORE, RESID, SWIGLU])
+@pytest.mark.parametrize("m,n,k", [(129, 24, 2048), (129, 520, 2064), (300, 1400, 4080), (129, 520, 4112), (260, 1040, 4096), (400, 264, 14336)])
+def test_gemm_cut_along_k(m, n, k, epi):
+    """Tiles for a part of the GPU: two and four CTAs a tile, in place as well."""
+    p = Product(m, n, k, epi)
+    p.run()
+    _lib.fp8_poll()
+    p.check()
+    if epi == RESID:
+        c = p.r.clone()
+        _lib.gemm_fp8(p.a, p.a_s, p.b.view(-1, p.k), p.b_s.squeeze(0), c, r=c, epilogue=RESID)
+        assert torch.equal(c, p.c)
+
+
 @pytest.mark.parametrize("epi", [STORE, RESID, SWIGLU8])
 @pytest.mark.parametrize("m,n,k", [(1, 10256, 1040), (40, 12304, 528), (65, 12304, 528), (20, 24592, 400), (33, 24592, 144), (17, 40016, 80)])
 def test_gemm_few_rows_many_columns(m, n, k, epi):
@@ -550,8 +564,16 @@ def test_binding_refuses_tensors_of_another_place():
 def test_limits_shorter_than_the_waits(m, n, epi, groups, limit):
     """A wait that gives up is reported once, or nothing gave up and the result is right; the next call is as ever."""
     p = Product(m, n, 2064, epi, groups=groups)
-    off = offsets([m // 3] * 3) if groups else None
-    rows = m // 3 * 3 if groups else m
+    short_limit(p, limit, offsets([m // 3] * 3) if groups else None, m // 3 * 3 if groups else m)
+
+
+@pytest.mark.parametrize("limit", [1, 500, 2000, 20000])
+@pytest.mark.parametrize("epi", [RESID, SWIGLU])
+def test_limits_shorter_than_the_waits_of_four_ctas(epi, limit):
+    short_limit(Product(300, 528, 4112, epi), limit, None, 300)
+
+
+def short_limit(p, limit, off, rows):
     want = p.run(off)[0].float().clone()
     _lib.fp8_poll()
     try:
