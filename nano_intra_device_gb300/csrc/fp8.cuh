@@ -138,7 +138,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 
 // A launch as a programmatic dependent of the stream's kernel ahead, in clusters of
 // `cluster` CTAs: the kernel may start while that one ends, and calls pdl_wait() before
-// it touches global memory.
+// it touches global memory.  What kernels ahead may have written is not read through the
+// read-only path, whose lines may be as old as the kernel's start.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
                              int cluster, const A&... args) {

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(512) f8_norm_kernel(const F8RowsArgs a) {
     float top = 0.f;
     if (i < nvec) {
       float g[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(a.g) + i), g);
+      unpack8(reinterpret_cast<const uint4*>(a.g)[i], g);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         v[j][k] = v[j][k] * scale * g[k];
@@ -125,14 +125,14 @@ __global__ void __launch_bounds__(256) f8_quant_kernel(const F8RowsArgs a, int c
   const int sub = threadIdx.x & 15, nvec = a.cols / 8;
   const int group = blockIdx.x / col_groups, row = group * 16 + (threadIdx.x >> 4);
   const int vec = (blockIdx.x - group * col_groups) * (V * 16) + sub;
-  const int from = row < a.rows ? a.index ? __ldg(a.index + row) : row : -1;
+  const int from = row < a.rows ? a.index ? a.index[row] : row : -1;
   const bool there = from >= 0 && from < a.src_rows;
   const uint4* x = reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(there ? from : 0) * a.cols);
   uint4 u[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     u[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (there && vec + 16 * j < nvec) u[j] = __ldg(x + vec + 16 * j);
+    if (there && vec + 16 * j < nvec) u[j] = x[vec + 16 * j];
   }
   const int end = row < a.rows ? nvec : 0;
 #pragma unroll
@@ -155,7 +155,7 @@ cudaError_t launch_quant(const F8RowsArgs& a, cudaStream_t stream) {
 
 // One CTA a 128 x 128 block: thread t has vector t % 16 of the rows t / 16 + 16 i.
 __global__ void __launch_bounds__(256)
-    f8_weights_kernel(const __nv_bfloat16* __restrict__ w, uint8_t* __restrict__ q, float* __restrict__ s,
+    f8_weights_kernel(const __nv_bfloat16* w, uint8_t* q, float* s,
                       int rows, int cols, int row_blocks, int col_blocks) {
   pdl_trigger();
   pdl_wait();
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(256)
   for (int i = 0; i < 8; ++i) {
     u[i] = make_uint4(0u, 0u, 0u, 0u);
     if (c < cols && r0 + 16 * i < rows)
-      u[i] = __ldg(reinterpret_cast<const uint4*>(w + base + static_cast<size_t>(r0 + 16 * i) * cols));
+      u[i] = *reinterpret_cast<const uint4*>(w + base + static_cast<size_t>(r0 + 16 * i) * cols);
   }
   float top = 0.f;
 #pragma unroll

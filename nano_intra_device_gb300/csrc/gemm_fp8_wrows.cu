@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       __syncwarp();
       for (int b = 0; b <= args.groups; b += 32) {
         const int i = b + lane;
-        int o = i <= args.groups ? min(max(__ldg(args.group_off + i), 0), args.M) : 0;
+        int o = i <= args.groups ? min(max(args.group_off[i], 0), args.M) : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, o, d);
@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
         const int c = half * MINE + lane + 32 * j, t = m0 + c % TOK;
         const bool on = i < klen && c < C::COLS && t < m_lim;
         const int kb = i < klen ? kb_at(i) : 0;
-        px[at][j] = on ? __ldg(args.a_s + static_cast<size_t>(kb) * args.M + t) : 0.f;
-        pw[at][j] = on ? __ldg(bs + (c / TOK) * static_cast<size_t>(nb) * nk + kb) : 0.f;
+        px[at][j] = on ? args.a_s[static_cast<size_t>(kb) * args.M + t] : 0.f;
+        pw[at][j] = on ? bs[(c / TOK) * static_cast<size_t>(nb) * nk + kb] : 0.f;
       }
     };
 #pragma unroll

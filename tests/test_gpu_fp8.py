@@ -490,6 +490,50 @@ def test_two_streams_at_once_and_a_graph(m, groups):
         assert torch.equal(c[:m // 3 * 2].view(torch.uint8), p.c[:m // 3 * 2].view(torch.uint8))
 
 
+@pytest.mark.parametrize("m", [1, 40, 200, 700])
+def test_a_chain_over_the_same_buffers(m):
+    """Each call reads what the one ahead wrote to buffers that were read before: one after the other without a wait, captured, and with a wait after each call."""
+    n, f = 1024, 528
+    up, down = Product(m, f, n, SWIGLU8, seed=5), Product(m, n, f, RESID, seed=6)
+    up.b_s.mul_(0.05), down.b_s.mul_(0.05)
+    x0 = torch.randn(m, n, device=DEV).bfloat16()
+    g = torch.ones(n, device=DEV, dtype=BF16)
+    x, h = x0.clone(), torch.zeros_like(x0)
+    q, s = torch.zeros(m, n, device=DEV).to(E4M3), torch.zeros(n // 128, m, device=DEV)
+    c, c_s = torch.zeros(m, f, device=DEV).to(E4M3), torch.zeros((f + 127) // 128, m, device=DEV)
+
+    def pair(out, res):
+        return [lambda: _lib.gemm_fp8(q, s, up.b.view(-1, n), up.b_s.squeeze(0), c, c_s=c_s, epilogue=SWIGLU8),
+                lambda: _lib.gemm_fp8(c, c_s, down.b.view(-1, f), down.b_s.squeeze(0), out, r=res, epilogue=RESID)]
+
+    calls = [lambda: _lib.rmsnorm_fp8(x, g, q, s, 1e-5, r=x0, h=h), *pair(h, h), lambda: _lib.quant_fp8(h, q, s), *pair(x, x0)] * 8
+
+    def layers(wait):
+        for call in calls:
+            call()
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return x.clone(), h.clone()
+
+    want = layers(True)
+    assert torch.isfinite(want[0]).all() and not torch.equal(want[0], x0)
+    for _ in range(5):
+        x.copy_(x0)
+        assert all(torch.equal(a, b) for a, b in zip(layers(False), want))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        x.copy_(x0)
+        for call in calls:
+            call()
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x, want[0]) and torch.equal(h, want[1])
+    _lib.fp8_poll()
+
+
 def test_two_threads_at_once():
     """Calls from two host threads, each on a stream of its own."""
     import threading
