@@ -19,6 +19,7 @@
 // Launched as a programmatic dependent of the kernel ahead.
 // Every wait is bounded.  After one gave up the CTAs of a cluster still meet at the
 // same exchange and the barrier before exit.
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -521,16 +522,20 @@ F8RowsChoice gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups) {
   const long long wt = (N + WM - 1) / WM;
   c.units = groups > 1 ? wt * (M / c.tok + (M < groups ? M : groups)) : wt * ((M + c.tok - 1) / c.tok);
   // As many CTAs as the device holds at once, but four blocks of K each at least.  Where an
-  // SM holds two, for one / both: 1 row of 4096 x 14336 15.3 / 14.3 us, of 10240 x 4096
+  // SM holds two, for one / both: 1 row of 4096 x 14336 15.3 / 13.2 us, of 10240 x 4096
   // 14.7 / 10.0, of 10240 x 14336 40.6 / 26.5, 64 rows of 14336 x 4096 18.3 / 15.1, 16 rows of
-  // 14336 x 4096 SwiGLU 24.8 / 22.9.
+  // 14336 x 4096 SwiGLU 24.8 / 22.9.  A group of SMs that holds n clusters of s CTAs, one an
+  // SM, holds 2 n of them two an SM, or n of 2 s.  One part more than fits is a second wave:
+  // 1 row of 8192 x 4096 in 4 parts 8.5, in 5 13.9.
   const long long busy = wt * (groups > 1 ? (M < groups ? M : groups) : (M + c.tok - 1) / c.tok);
   const int nk = (K + BK - 1) / BK;
   c.splits = 1;
   for (int s = 2; s <= MAX_CLUSTER && 4 * s <= nk; ++s)
     if (busy <= dispatch(epi, c.tok, [&](auto e, auto k) {
           constexpr int EPI = decltype(e)::value, TOK = decltype(k)::value;
-          return Cfg<EPI, TOK>::PER_SM * most_clusters<EPI, TOK>(s);
+          const int one = most_clusters<EPI, TOK>(s);
+          if (Cfg<EPI, TOK>::PER_SM == 1) return one;
+          return s > 2 ? std::max(2 * one, most_clusters<EPI, TOK>((s + 1) / 2)) : 2 * one;
         }))
       c.splits = s;
   return c;
