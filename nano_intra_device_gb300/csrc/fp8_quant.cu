@@ -9,17 +9,18 @@
 //
 // Bound by memory: one pass, 16-byte loads, a row of the norm in the registers of its
 // CTA between the sum of squares and the codes.  Reached (of 6.68 TB/s copied): norm with
-// residual, 4096 rows of 8192, 39 us = 6.0 TB/s; quantisation, 4096 rows of 14336, 31 us =
-// 5.7 TB/s, by an index 4094 rows of 4096 11 us; two matrices of 14336 x 4096, 56 us =
+// residual, 4096 rows of 8192, 39 us = 6.0 TB/s; quantisation, 4096 rows of 14336, 28 us =
+// 6.3 TB/s, by an index 4094 rows of 4096 9.5 us; two matrices of 14336 x 4096, 56 us =
 // 6.3 TB/s.  Few rows: launch and latency, 1.4 to 2 us in a graph.
 #include "fp8.cuh"
 
 namespace nf {
 namespace {
 
-// Column blocks a thread quantises: as many loads are under way at once.  Measured with 1,
-// 2, 4 and 8: 4096 rows of 14336 42 / 35 / 31 / 32 us, 4096 rows of 4096 13.7 / 11.9 / 11.0 /
-// 12.2; where there are at most FEW_BLOCKS blocks an SM, one, which gives every SM work.
+// Column blocks a thread quantises: as many loads are under way at once.  Where there are at
+// most FEW_BLOCKS blocks an SM, or two blocks a row, one, which gives every SM work; one / four:
+// 512 rows of 4096 (16384 blocks) 2.8 / 3.3 us, 1024 rows 4.5 / 4.1, 512 rows of 14336 6.7 /
+// 5.6; 65536 rows of 256 13.0 / 13.3, of 384 18.9 / 15.2.
 constexpr int FEW_BLOCKS = 128, QV = 4;
 // Rows an SM up to which the norm takes one vector a thread: 1 / 2 vectors, rows of 4096,
 // 1 row 1.96 / 2.26 us, 512 rows 5.2 / 6.2, 2048 rows 14.3 / 12.6.
@@ -116,15 +117,19 @@ cudaError_t launch_norm(const F8RowsArgs& a, int threads, cudaStream_t stream) {
   return launch_dependent(f8_norm_kernel<VPT, false, WARP>, grid, threads, 0, stream, 1, a);
 }
 
-// Given values: a CTA takes 16 rows x V column blocks, 16 threads a block of 128, so that
-// the scales of neighbouring rows, next to one another in memory, are written together.
+// Given values: a CTA takes 16 rows (8 where a thread has several blocks: a shorter last
+// wave, 4096 rows of 14336 28.0 us, by 16 rows 29.9, by 4 30.9) x V column blocks, 16 threads
+// a block of 128, so that the scales of neighbouring rows, next to one another in memory, are
+// written together.
+constexpr int rows_of(int v) { return v == 1 ? 16 : 8; }
 template <int V>
-__global__ void __launch_bounds__(256) f8_quant_kernel(const F8RowsArgs a, int col_groups) {
+__global__ void __launch_bounds__(rows_of(V) * 16) f8_quant_kernel(const F8RowsArgs a, int col_groups) {
   pdl_trigger();
   pdl_wait();
   const int sub = threadIdx.x & 15, nvec = a.cols / 8;
-  const int group = blockIdx.x / col_groups, row = group * 16 + (threadIdx.x >> 4);
+  const int group = blockIdx.x / col_groups, row = group * rows_of(V) + (threadIdx.x >> 4);
   const int vec = (blockIdx.x - group * col_groups) * (V * 16) + sub;
+  static_assert(V == 1 || V == 4, "column blocks");
   const int from = row < a.rows ? a.index ? a.index[row] : row : -1;
   const bool there = from >= 0 && from < a.src_rows;
   const uint4* x = reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(there ? from : 0) * a.cols);
@@ -135,22 +140,52 @@ __global__ void __launch_bounds__(256) f8_quant_kernel(const F8RowsArgs a, int c
     if (there && vec + 16 * j < nvec) u[j] = x[vec + 16 * j];
   }
   const int end = row < a.rows ? nvec : 0;
+  if constexpr (V == 4) {
+    // The four blocks' largest magnitudes at once: a lane hands on the two blocks, then the
+    // one, that it does not keep, and ends with block sub % 4, whose scale and reciprocal it
+    // takes for all (a division is a dozen instructions; made for each block by every lane,
+    // 4096 rows of 14336 take 30.7 us, so 29.5).
+    float t[4];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < 4; ++j) {
+      float v[8];
+      unpack8(u[j], v);
+      t[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[j] = absmax_nan(t[j], v[k]);
+    }
+    auto over = [](float kept, float given, int lanes) { return absmax_nan(kept, __shfl_xor_sync(0xffffffffu, given, lanes)); };
+    const bool odd = sub & 1, high = sub & 2;
+    const float t0 = over(odd ? t[1] : t[0], odd ? t[0] : t[1], 1), t2 = over(odd ? t[3] : t[2], odd ? t[2] : t[3], 1);
+    float top = over(high ? t2 : t0, high ? t0 : t2, 2);
+    top = over(top, top, 4);
+    top = over(top, top, 8);
+    const float s = f8_scale(top), inv = 1.f / s;
+    if (sub < 4 && vec + 15 * sub < end) a.s[static_cast<size_t>((vec - sub) / 16 + sub) * a.rows + row] = s;
+    uint2* q = reinterpret_cast<uint2*>(a.q + static_cast<size_t>(row) * a.cols);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float sj = __shfl_sync(0xffffffffu, s, j, 16), ij = __shfl_sync(0xffffffffu, inv, j, 16);
+      float v[8];
+      unpack8(u[j], v);
+      if (vec + 16 * j < end)
+        q[vec + 16 * j] = make_uint2(f8_codes4(v[0], v[1], v[2], v[3], sj, ij), f8_codes4(v[4], v[5], v[6], v[7], sj, ij));
+    }
+  } else {
     float v[8], top = 0.f;
-    unpack8(u[j], v);
+    unpack8(u[0], v);
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = absmax_nan(top, v[k]);
-    store_block(a, row, vec + 16 * j, end, v, top);
+    store_block(a, row, vec, end, v, top);
   }
 }
 
 template <int V>
 cudaError_t launch_quant(const F8RowsArgs& a, cudaStream_t stream) {
   const int col_groups = (a.cols + V * F8_BLOCK - 1) / (V * F8_BLOCK);
-  const long long grid = (static_cast<long long>(a.rows) + 15) / 16 * col_groups;
+  const long long grid = (static_cast<long long>(a.rows) + rows_of(V) - 1) / rows_of(V) * col_groups;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_dependent(f8_quant_kernel<V>, static_cast<unsigned>(grid), 256, 0, stream, 1, a, col_groups);
+  return launch_dependent(f8_quant_kernel<V>, static_cast<unsigned>(grid), rows_of(V) * 16, 0, stream, 1, a, col_groups);
 }
 
 // One CTA a 128 x 128 block: thread t has vector t % 16 of the rows t / 16 + 16 i.
@@ -207,7 +242,7 @@ cudaError_t launch_f8_rows(const F8RowsArgs& a, int sms, cudaStream_t stream) {
   const int nvec = a.cols / 8;
   if (!a.g) {
     const long long blocks = static_cast<long long>(a.rows) * ((nvec + 15) / 16);
-    return blocks <= FEW_BLOCKS * sms ? launch_quant<1>(a, stream) : launch_quant<QV>(a, stream);
+    return blocks <= FEW_BLOCKS * sms || nvec <= 32 ? launch_quant<1>(a, stream) : launch_quant<QV>(a, stream);
   }
   auto threads = [&](int vpt) { return (nvec + 32 * vpt - 1) / (32 * vpt) * 32; };
   // rows of at most 512 columns a warp each: 4096 rows of 256 3.6 us, by CTAs 4.5

@@ -90,6 +90,27 @@ def test_quant_special_values():
     same(f64(q), want[0])
 
 
+@pytest.mark.parametrize("rows,cols", [(6601, 272), (5003, 400), (5001, 512), (3509, 688), (2301, 1040), (613, 4240), (70001, 144)])
+def test_quant_many_rows(rows, cols):
+    """Enough blocks for several a thread: special values in every block's place, rows by an index with some outside."""
+    x = (torch.randn(1009, cols, generator=torch.Generator().manual_seed(cols)) * 3).to(BF16)
+    sp = special()
+    for i in range(0, 1009 - 9, 27):
+        at = (i // 27 * 128) % (cols - 16)
+        n = min(272, cols - at)
+        x[i:i + 9, at:at + n] = sp[:, :n]
+    index = torch.randint(-20, 1029, (rows,), generator=torch.Generator().manual_seed(rows), dtype=I32)
+    q, s = quant(x.to(DEV), index.to(DEV))
+    want_q, want_s = orc.quantise_rows(x.float().numpy())
+    inside = (index >= 0) & (index < 1009)
+    pick = index.clamp(0, 1008).long().numpy()
+    zero_q, zero_s = orc.quantise_rows(np.zeros((1, cols), np.float32))
+    same(f64(q), np.where(inside.numpy()[:, None], want_q[pick], zero_q))
+    same(f64(s), np.where(inside.numpy()[None], want_s[:, pick], zero_s))
+    q2, s2 = quant(x[pick].to(DEV))
+    same(f64(q2), want_q[pick]), same(f64(s2), want_s[:, pick])
+
+
 def test_quotients_are_cudas():
     """All pairs of 8-bit significands as value and largest of a block: codes as of the fp32 quotient."""
     top = torch.arange(128, 256, device=DEV).float()
