@@ -50,17 +50,17 @@ nf_status check_rows(int32_t rows, int32_t cols, const char* what) {
 // Whether a product goes to the kernel of few rows of A, which fills the GPU by cutting K
 // (the fewer tiles of weights, the more rows), or to tiles of 128 rows x 256, which read the
 // weights once for all rows.  Few rows / tiles, us, K 4096, by tiles of 128 weight rows:
-//   64 (8192): 64 rows 10.7 / 15.7, 128 rows 13.1 / 16.2; 256 rows of 6144 18.8 / 15.0;
-//   112 (14336): 64 rows 14.9 / 17.4, 128 rows 19.4 / 17.9;
-//   224 (28672): 16 rows 23.2 / 30.2, 32 rows 23.5 / 23.5, 64 rows 25.1 / 24.1;
-//   224 (SwiGLU, 14336): 32 rows 23.5 / 24.0, 64 rows 26.0 / 24.0;
-//   1002 (128256): 16 rows 88 / 101, 32 rows 97 / 88.
+//   64 (8192): 64 rows 10.8 / 15.6, 128 rows 13.2 / 15.8; 256 rows of 6144 19.1 / 15.6;
+//   112 (14336): 64 rows 14.8 / 16.9, 128 rows 19.5 / 17.4;
+//   224 (28672): 16 rows 23.2 / 30.5, 32 rows 23.5 / 23.4, 64 rows 25.1 / 23.8;
+//   224 (SwiGLU, 14336): 32 rows 23.6 / 24.1, 64 rows 25.8 / 24.2;
+//   1002 (128256): 16 rows 89 / 96, 32 rows 97 / 89.
 // By groups, with the rows' mean (a tile has room for twice as many, of SwiGLU for 64):
-//   8 of 1024 x 4096 (64): 64 rows 13.4 / 19.0; SwiGLU, 8 of 512 (64): 32 rows 12.4 / 19.3, 64
-//   rows 22.0 / 19.5; 8 of 2048 (128): 32 rows 16.4 / 19.9, 64 rows 20.0 / 20.4;
-//   8 of 14336 x 4096 SwiGLU: 1 row 75 / 94, 8 rows 142 / 143, 32 rows 170 / 146;
-//   64 of 2048 x 2048: 0.5 rows 26.6 / 27.4, 1 row 40 / 36, 8 rows 58 / 49 (a CTA a tile: short
-//   ones do not pay); 64 of 768 x 2048: 1 row 15.7 / 16.0, 2 rows 25.8 / 24.3.
+//   8 of 1024 x 4096 (64): 64 rows 13.5 / 19.0; SwiGLU, 8 of 512 (64): 32 rows 12.5 / 19.4, 64
+//   rows 21.9 / 19.5; 8 of 2048 (128): 32 rows 16.4 / 20.0, 64 rows 19.9 / 20.6;
+//   8 of 14336 x 4096 SwiGLU: 1 row 73 / 102, 8 rows 139 / 140, 32 rows 165 / 142;
+//   64 of 2048 x 2048: 0.5 rows 26.1 / 28.0, 1 row 40 / 36, 8 rows 58 / 48 (a CTA a tile: short
+//   ones do not pay); 64 of 768 x 2048: 1 row 15.4 / 15.4, 2 rows 25.5 / 24.0.
 // A capped product takes the tiles, which loop.
 bool few_rows(int M, int N, int K, int groups, bool two, int sms) {
   const int rows = (M + groups - 1) / groups;

@@ -16,8 +16,8 @@
 //    of products (two halves of four instructions), but a half's accumulator goes issue,
 //    completion, sums' loads, release, issue, some 1500 cycles for two blocks; about 800
 //    cycles a block are reached, 57 % of the tensor pipe.  In long runs the power limit
-//    counts as well: 4096 x 8192 x 28672 takes 700 us (2.7 PFLOP/s) for the first dozens of
-//    calls and 795 us (1590 MHz, 1360 W) after seconds.  Measured and not kept, on that
+//    counts as well: 4096 x 8192 x 28672 takes 685 to 705 us (2.8 PFLOP/s) for the first dozens
+//    of calls and 800 us (1590 MHz, 1360 W) after seconds.  Measured and not kept, on that
 //    product at 711: one issuing warp for both halves 946, one for each accumulator 748,
 //    sixteen summing warps of 64 columns 718, the next block's loads ahead of this one's
 //    last sums 890, packed pairs of sums 893 (moves), one hand-over for all 256 columns
