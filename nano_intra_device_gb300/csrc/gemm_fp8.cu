@@ -27,6 +27,9 @@
 //    with the others' sums from their shared memory.
 //  * Every wait is bounded; one that gives up flags the status word, and the kernel
 //    drains what it has in flight (bounded) and frees tensor memory.
+#include <atomic>
+#include <type_traits>
+
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -506,6 +509,33 @@ __global__ void __launch_bounds__(THREADS, 1)
 __device__ uint32_t g_taken;
 __global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0u); }
 
+// Clusters of SPLIT CTAs that the device holds at once; asked once a process.
+template <int EPI, int SPLIT>
+int most_clusters() {
+  static std::atomic<int> cache;
+  int n = cache.load(std::memory_order_relaxed);
+  if (n == 0) {
+    const auto kernel = gemm_f8_kernel<EPI, SPLIT>;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = SPLIT;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(SPLIT, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (set_smem_limit(reinterpret_cast<const void*>(kernel), SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;
+    }
+    cache.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 template <int EPI, int SPLIT>
 cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const F8GemmArgs& args, int grid,
                    cudaStream_t stream) {
@@ -529,16 +559,24 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
   // 256 x 8192 x 28672 95 / 60; 512 x 2048 x 2048 11.5 either way, x 1024 8.4 / 9.5.  For less
   // than a quarter of the SMs four; two / four: 256 x 4096 x 14336 35 / 24, 256 x 4096 x 4096
   // 14.4 either way, x 2048 11.4 / 12.5, 256 x 2048 x 4096 SwiGLU 15.5 / 13.6.
-  if (!args.group_off && 2 * most <= sms && (args.K + BK - 1) / BK >= 16) {
-    const int grid = static_cast<int>(2 * most);
-    if (4 * most <= sms && (args.K + BK - 1) / BK >= 32) {
-      if (epi == F8_STORE) return launch<F8_STORE, 4>(tmA, tmB, args, 2 * grid, stream);
-      if (epi == F8_RESID) return launch<F8_RESID, 4>(tmA, tmB, args, 2 * grid, stream);
-      if (epi == F8_SWIGLU) return launch<F8_SWIGLU, 4>(tmA, tmB, args, 2 * grid, stream);
-    }
-    if (epi == F8_STORE) return launch<F8_STORE, 2>(tmA, tmB, args, grid, stream);
-    if (epi == F8_RESID) return launch<F8_RESID, 2>(tmA, tmB, args, grid, stream);
-    if (epi == F8_SWIGLU) return launch<F8_SWIGLU, 2>(tmA, tmB, args, grid, stream);
+  // A tile more than clusters fit is a second wave: 38 tiles of 256 x 4864 x 4096 in two parts
+  // 14.8, in four (152 SMs, in groups that hold 36 clusters of four) 25.1.
+  const int nk = (args.K + BK - 1) / BK;
+  if (!args.group_off && epi != F8_SWIGLU8) {
+    cudaError_t e = cudaSuccess;
+    auto cut = [&](auto epilogue, auto split) {
+      constexpr int EPI = decltype(epilogue)::value, SPLIT = decltype(split)::value;
+      if (nk < 8 * SPLIT || SPLIT * most > sms || most > most_clusters<EPI, SPLIT>()) return false;
+      e = launch<EPI, SPLIT>(tmA, tmB, args, static_cast<int>(SPLIT * most), stream);
+      return true;
+    };
+    auto either = [&](auto epilogue) {
+      return cut(epilogue, std::integral_constant<int, 4>{}) || cut(epilogue, std::integral_constant<int, 2>{});
+    };
+    if (epi == F8_STORE ? either(std::integral_constant<int, F8_STORE>{})
+        : epi == F8_RESID ? either(std::integral_constant<int, F8_RESID>{})
+                          : epi == F8_SWIGLU && either(std::integral_constant<int, F8_SWIGLU>{}))
+      return e;
   }
   const int grid = static_cast<int>(most < sms ? most : sms);
   switch (epi) {
