@@ -371,6 +371,65 @@ __global__ void __launch_bounds__(THREADS, 1)
         // (a release at cluster scope, behind the barrier that all of the CTA's writes precede)
         if (warp == 4 && lane < SPLIT) mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), lane));
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo)) && ok;
+        if constexpr (EPI == F8_SWIGLU8) {
+          // An 8-bit block is a row's 128 features, so a CTA finishes rows: a warp 32 of them,
+          // FEAT features each.
+          constexpr int ROW_WARPS = BM / SPLIT / 32, FEAT = 16 * ROW_WARPS, PART = FEAT / 4;
+          const int w8 = warp - 4, chunk = w8 / ROW_WARPS;
+          const int row = (rank * ROW_WARPS + w8 % ROW_WARPS) * 32 + lane;
+          const int c4 = chunk / (64 / FEAT) * 32 + chunk % (64 / FEAT) * PART;  // first gate columns, in fours
+          const Tile x = decode(u);
+          const int n0 = x.tn * TN + chunk * FEAT;
+          float o[FEAT], top = 0.f;
+          if (ok) {
+            const uint32_t mine8 = smem_u32(reinterpret_cast<float4*>(smem) + c4 * BM + row);
+            float4 w[SPLIT][2 * PART];
+#pragma unroll
+            for (int r = 0; r < SPLIT; ++r) {
+              const uint32_t at = cluster_map(mine8, r);
+#pragma unroll
+              for (int i = 0; i < 2 * PART; ++i) w[r][i] = ld_cluster_f4(at + (i / PART * 16 + i % PART) * (BM * 16));
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * PART; ++i)
+#pragma unroll
+              for (int r = 1; r < SPLIT; ++r) {
+                w[0][i].x += w[r][i].x; w[0][i].y += w[r][i].y; w[0][i].z += w[r][i].z; w[0][i].w += w[r][i].w;
+              }
+#pragma unroll
+            for (int i = 0; i < PART; ++i) {
+              const float4 a = w[0][i], b = w[0][PART + i];
+              o[4 * i] = silu_mul(a.x, b.x);
+              o[4 * i + 1] = silu_mul(a.y, b.y);
+              o[4 * i + 2] = silu_mul(a.z, b.z);
+              o[4 * i + 3] = silu_mul(a.w, b.w);
+            }
+#pragma unroll
+            for (int i = 0; i < FEAT; ++i) {
+              if (n0 + i >= args.N) o[i] = 0.f;
+              top = absmax_nan(top, o[i]);
+            }
+          }
+          tail->top[0][w8][lane] = top;
+          asm volatile("bar.sync 1, 256;" ::: "memory");  // (also after a failure)
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 8 / ROW_WARPS; ++j) top = absmax_nan(top, tail->top[0][w8 % ROW_WARPS + j * ROW_WARPS][lane]);
+          const float s = f8_scale(top), inv = 1.f / s;
+          const int m = x.m0 + row;
+          if (m < x.m_lim) {
+            if (chunk == 0) args.c_s[static_cast<size_t>(x.tn) * args.M + m] = s;
+#pragma unroll
+            for (int j = 0; j < FEAT / 16; ++j) {
+              const float* v = o + 16 * j;
+              if (n0 + 16 * j < args.N)
+                *reinterpret_cast<uint4*>(args.q + static_cast<size_t>(m) * args.N + n0 + 16 * j) =
+                    make_uint4(f8_codes4_near(v[0], v[1], v[2], v[3], inv), f8_codes4_near(v[4], v[5], v[6], v[7], inv),
+                               f8_codes4_near(v[8], v[9], v[10], v[11], inv), f8_codes4_near(v[12], v[13], v[14], v[15], inv));
+            }
+          }
+          break;  // one tile a cluster
+        }
         if (!ok) break;
         constexpr int OPS = SW ? 2 : 1, PART = 32 / OPS / SPLIT;  // of a row's float4s, of each operand
         float4 w[SPLIT][OPS * PART];
@@ -562,7 +621,7 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
   // A tile more than clusters fit is a second wave: 38 tiles of 256 x 4864 x 4096 in two parts
   // 14.8, in four (152 SMs, in groups that hold 36 clusters of four) 25.1.
   const int nk = (args.K + BK - 1) / BK;
-  if (!args.group_off && epi != F8_SWIGLU8) {
+  if (!args.group_off) {
     cudaError_t e = cudaSuccess;
     auto cut = [&](auto epilogue, auto split) {
       constexpr int EPI = decltype(epilogue)::value, SPLIT = decltype(split)::value;
@@ -574,8 +633,9 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
       return cut(epilogue, std::integral_constant<int, 4>{}) || cut(epilogue, std::integral_constant<int, 2>{});
     };
     if (epi == F8_STORE ? either(std::integral_constant<int, F8_STORE>{})
-        : epi == F8_RESID ? either(std::integral_constant<int, F8_RESID>{})
-                          : epi == F8_SWIGLU && either(std::integral_constant<int, F8_SWIGLU>{}))
+        : epi == F8_RESID  ? either(std::integral_constant<int, F8_RESID>{})
+        : epi == F8_SWIGLU ? either(std::integral_constant<int, F8_SWIGLU>{})
+                           : epi == F8_SWIGLU8 && either(std::integral_constant<int, F8_SWIGLU8>{}))
       return e;
   }
   const int grid = static_cast<int>(most < sms ? most : sms);
