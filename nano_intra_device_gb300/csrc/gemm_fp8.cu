@@ -371,9 +371,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         // (a release at cluster scope, behind the barrier that all of the CTA's writes precede)
         if (warp == 4 && lane < SPLIT) mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), lane));
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo)) && ok;
-        if constexpr (EPI == F8_SWIGLU8) {
-          // An 8-bit block is a row's 128 features, so a CTA finishes rows: a warp 32 of them,
-          // FEAT features each.
+        if constexpr (SW) {
+          // A feature's gate and up columns meet here, and an 8-bit block is a row's 128
+          // features, so a CTA finishes rows: a warp 32 of them, FEAT features each.
           constexpr int ROW_WARPS = BM / SPLIT / 32, FEAT = 16 * ROW_WARPS, PART = FEAT / 4;
           const int w8 = warp - 4, chunk = w8 / ROW_WARPS;
           const int row = (rank * ROW_WARPS + w8 % ROW_WARPS) * 32 + lane;
@@ -410,13 +410,25 @@ __global__ void __launch_bounds__(THREADS, 1)
               top = absmax_nan(top, o[i]);
             }
           }
+          const int m = x.m0 + row;
+          if constexpr (EPI == F8_SWIGLU) {
+            if (ok && m < x.m_lim) {
+#pragma unroll
+              for (int j = 0; j < FEAT / 8; ++j) {
+                const float* v = o + 8 * j;
+                if (n0 + 8 * j < args.N)
+                  *reinterpret_cast<uint4*>(args.C + static_cast<size_t>(m) * args.N + n0 + 8 * j) =
+                      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+              }
+            }
+            break;  // one tile a cluster
+          }
           tail->top[0][w8][lane] = top;
           asm volatile("bar.sync 1, 256;" ::: "memory");  // (also after a failure)
           if (!ok) break;
 #pragma unroll
           for (int j = 0; j < 8 / ROW_WARPS; ++j) top = absmax_nan(top, tail->top[0][w8 % ROW_WARPS + j * ROW_WARPS][lane]);
           const float s = f8_scale(top), inv = 1.f / s;
-          const int m = x.m0 + row;
           if (m < x.m_lim) {
             if (chunk == 0) args.c_s[static_cast<size_t>(x.tn) * args.M + m] = s;
 #pragma unroll
@@ -428,31 +440,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                                f8_codes4_near(v[8], v[9], v[10], v[11], inv), f8_codes4_near(v[12], v[13], v[14], v[15], inv));
             }
           }
-          break;  // one tile a cluster
+          break;
         }
         if (!ok) break;
-        constexpr int OPS = SW ? 2 : 1, PART = 32 / OPS / SPLIT;  // of a row's float4s, of each operand
-        float4 w[SPLIT][OPS * PART];
+        constexpr int PART = 32 / SPLIT;  // of a row's fours of columns
+        float4 w[SPLIT][PART];
 #pragma unroll
         for (int r = 0; r < SPLIT; ++r) {
           const uint32_t at = cluster_map(smem_u32(ring + rank * PART * BM), r);
 #pragma unroll
-          for (int i = 0; i < OPS * PART; ++i)
-            w[r][i] = ld_cluster_f4(at + (i / PART * (32 / OPS) + i % PART) * (BM * 16));
+          for (int i = 0; i < PART; ++i) w[r][i] = ld_cluster_f4(at + i * (BM * 16));
         }
 #pragma unroll
-        for (int i = 0; i < OPS * PART; ++i)
+        for (int i = 0; i < PART; ++i) {
+          float4 t = w[0][i];
 #pragma unroll
           for (int r = 1; r < SPLIT; ++r) {
-            w[0][i].x += w[r][i].x; w[0][i].y += w[r][i].y; w[0][i].z += w[r][i].z; w[0][i].w += w[r][i].w;
+            t.x += w[r][i].x; t.y += w[r][i].y; t.z += w[r][i].z; t.w += w[r][i].w;
           }
-#pragma unroll
-        for (int i = 0; i < PART; ++i) {
-          const float4 a = w[0][i], b = w[0][SW ? PART + i : i];
-          sum[4 * i] = SW ? silu_mul(a.x, b.x) : a.x;
-          sum[4 * i + 1] = SW ? silu_mul(a.y, b.y) : a.y;
-          sum[4 * i + 2] = SW ? silu_mul(a.z, b.z) : a.z;
-          sum[4 * i + 3] = SW ? silu_mul(a.w, b.w) : a.w;
+          sum[4 * i] = t.x; sum[4 * i + 1] = t.y; sum[4 * i + 2] = t.z; sum[4 * i + 3] = t.w;
         }
       }
       if (!ok) break;
@@ -494,10 +500,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       } else {
-        constexpr int WIDE = SW && SPLIT == 4 ? 16 : 32, CHUNKS = TN / 2 / SPLIT / WIDE;
+        constexpr int CHUNKS = SW ? 2 : 4 / SPLIT;  // (SwiGLU: not cut)
 #pragma unroll
         for (int h = 0; h < CHUNKS; ++h) {
-          const int n0 = x.tn * TN + half * (TN / 2) + (rank * CHUNKS + h) * WIDE;
+          const int n0 = x.tn * TN + half * (TN / 2) + (rank * CHUNKS + h) * 32;
           if (EPI == F8_RESID) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -510,12 +516,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
           }
 #pragma unroll
-          for (int j = 0; j < WIDE / 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             float w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               w[i] = sum[h * 32 + j * 8 + i];
-              if (SW && SPLIT == 1) w[i] = silu_mul(w[i], sum[64 + h * 32 + j * 8 + i]);
+              if (SW) w[i] = silu_mul(w[i], sum[64 + h * 32 + j * 8 + i]);
             }
             if (EPI == F8_RESID) {
               const uint4 r = *slot(lane, j);
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = i * 8 + lane / 4, j = lane % 4, n = n0 + 8 * j;
-            if (mw + r < x.m_lim && n < args.N && 8 * j < WIDE)
+            if (mw + r < x.m_lim && n < args.N)
               *reinterpret_cast<uint4*>(args.C + static_cast<size_t>(mw + r) * args.N + n) = *slot(r, j);
           }
           __syncwarp();
