@@ -51,6 +51,7 @@ nf_status check_rows(int32_t rows, int32_t cols, const char* what) {
 // (the fewer tiles of weights, the more rows), or to tiles of 128 rows x 256, which read the
 // weights once for all rows.  Few rows / tiles, us, K 4096, by tiles of 128 weight rows:
 //   64 (8192): 64 rows 10.8 / 15.6, 128 rows 13.2 / 15.8; 256 rows of 6144 19.1 / 15.6;
+//   SwiGLU, 32 (2048): 128 rows 11.3 / 12.7; 64 (4096): 64 rows 12.0 / 14.5, 128 rows 15.4 / 14.6;
 //   112 (14336): 64 rows 14.8 / 16.9, 128 rows 19.5 / 17.4;
 //   224 (28672): 16 rows 23.2 / 30.5, 32 rows 23.5 / 23.4, 64 rows 25.1 / 23.8;
 //   224 (SwiGLU, 14336): 32 rows 23.6 / 24.1, 64 rows 25.8 / 24.2;
@@ -70,7 +71,7 @@ bool few_rows(int M, int N, int K, int groups, bool two, int sms) {
     if (tiles > sms) return rows <= 16 && (M <= groups || K * ops >= 8192);
     return rows <= (tiles <= sms / 2 && !two ? 64 : 32);
   }
-  return rows <= (tiles <= sms / 2 ? 128 : tiles <= sms ? 64 : tiles <= 2 * sms ? 32 : 16);
+  return rows <= (tiles <= sms / (two ? 4 : 2) ? 128 : tiles <= sms ? 64 : tiles <= 2 * sms ? 32 : 16);
 }
 
 // The product's checks, for one matrix (group_off NULL, groups 1) or by groups.

@@ -23,8 +23,8 @@
 //    last sums 890, packed pairs of sums 893 (moves), one hand-over for all 256 columns
 //    884, B multicast to two CTAs 703 (shorter products 4 to 7 % slower).
 //  * A product with tiles for less than a half (a quarter) of the SMs is cut along K between
-//    the two (four) CTAs of a cluster (SPLIT): each finishes its part of the tile's columns,
-//    with the others' sums from their shared memory.
+//    the two (four) CTAs of a cluster (SPLIT): each finishes its part of the tile's columns
+//    (SwiGLU: of its rows), with the others' sums from their shared memory.
 //  * Every wait is bounded; one that gives up flags the status word, and the kernel
 //    drains what it has in flight (bounded) and frees tensor memory.
 #include <atomic>
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (SPLIT > 1) {
         // Both halves' products have read the ring, which now takes the sums, four columns of
         // a row together, rows next to one another.  A CTA finishes its part of each half's
-        // columns, with all CTAs' sums in their order (a load takes about a microsecond: all
-        // 32 at once).
+        // columns (SwiGLU: of the rows), with all CTAs' sums in their order (a load takes about
+        // a microsecond: all 32 at once).
         asm volatile("bar.sync 1, 256;" ::: "memory");
         float4* ring = reinterpret_cast<float4*>(smem) + half * 32 * BM + row_in_tile;
         if (ok) {
@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo)) && ok;
         if constexpr (SW) {
           // A feature's gate and up columns meet here, and an 8-bit block is a row's 128
-          // features, so a CTA finishes rows: a warp 32 of them, FEAT features each.
+          // features, so a CTA finishes rows: a warp 32 of them, FEAT features each (bf16
+          // output by columns as below: 256 x 4096 x 14336 39 us, so 35).
           constexpr int ROW_WARPS = BM / SPLIT / 32, FEAT = 16 * ROW_WARPS, PART = FEAT / 4;
           const int w8 = warp - 4, chunk = w8 / ROW_WARPS;
           const int row = (rank * ROW_WARPS + w8 % ROW_WARPS) * 32 + lane;
@@ -623,7 +624,7 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
   // CTAs.  Whole / cut: 333 x 6144 x 4096 18.4 / 15.8 us, 333 x 4096 x 14336 49 / 31,
   // 256 x 8192 x 28672 95 / 60; 512 x 2048 x 2048 11.5 either way, x 1024 8.4 / 9.5.  For less
   // than a quarter of the SMs four; two / four: 256 x 4096 x 14336 35 / 24, 256 x 4096 x 4096
-  // 14.4 either way, x 2048 11.4 / 12.5, 256 x 2048 x 4096 SwiGLU 15.5 / 13.6.
+  // 14.4 either way, x 2048 11.4 / 12.5, 256 x 2048 x 4096 SwiGLU 15.5 / 13.0.
   // A tile more than clusters fit is a second wave: 38 tiles of 256 x 4864 x 4096 in two parts
   // 14.8, in four (152 SMs, in groups that hold 36 clusters of four) 25.1.
   const int nk = (args.K + BK - 1) / BK;
