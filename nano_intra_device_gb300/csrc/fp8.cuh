@@ -42,6 +42,14 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
+// The barrier before exit: no CTA leaves, and with it its shared memory, while a peer may
+// still read there.  Released: the loads from peers that are before it in a thread's
+// program are done when it arrives, whether or not their values were used (rows behind the
+// last one are read and not stored, so the compiler may leave their loads in flight).
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  cluster_wait();
+}
 // 16 bytes of a CTA of the cluster, by shared::cluster address.
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;

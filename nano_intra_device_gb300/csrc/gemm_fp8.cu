@@ -566,10 +566,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
-  if (SPLIT > 1) {  // no CTA leaves while a peer may read its sums
-    cluster_arrive();
-    cluster_wait();
-  }
+  if (SPLIT > 1) cluster_leave();
 }
 
 __device__ uint32_t g_taken;

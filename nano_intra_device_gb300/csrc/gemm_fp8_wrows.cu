@@ -425,8 +425,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM);
   }
-  cluster_arrive();
-  cluster_wait();  // no CTA leaves while a peer may still read its sums
+  cluster_leave();
 }
 
 __device__ uint32_t g_taken;

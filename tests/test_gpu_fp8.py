@@ -555,6 +555,24 @@ def test_a_chain_over_the_same_buffers(m):
     _lib.fp8_poll()
 
 
+@pytest.mark.parametrize("m,n,k,epi", [(129, 528, 4112, SWIGLU), (129, 528, 4112, SWIGLU8), (257, 528, 2064, SWIGLU8), (130, 520, 4112, RESID), (1, 528, 14336, SWIGLU), (3, 1040, 8192, STORE)])
+def test_clusters_whose_rows_end_early_beside_others(m, n, k, epi):
+    """CTAs of a cluster that store little end while peers still read their sums, on two streams that fill each other's SMs: the same bits at each call."""
+    ps = [Product(m, n, k, epi, seed=i) for i in (7, 8)]
+    want = [p.run()[0].float().clone() for p in ps]
+    ps[0].check(), ps[1].check()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[(torch.zeros_like(p.c.float()).to(p.c.dtype), None if p.c_s is None else torch.zeros_like(p.c_s)) for _ in range(40)] for p in ps]
+    torch.cuda.synchronize()
+    for i in range(40):
+        for p, o, st in zip(ps, outs, streams):
+            p.run(None, *o[i], stream=st)
+    torch.cuda.synchronize()
+    _lib.fp8_poll()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(c.float(), w) for c, _ in o)
+
+
 def test_two_threads_at_once():
     """Calls from two host threads, each on a stream of its own."""
     import threading
