@@ -651,10 +651,13 @@ nf_status nf_gemm_fp8_grouped(const void* A, const float* a_s, const void* B, co
                               int32_t M, int32_t N, int32_t K, int32_t epilogue, int32_t max_sms,
                               void* stream);
 
-/* Waits for `stream`, then reports and clears what the products of this section
- * have flagged on the current device since the last poll: NF_OK, or
- * NF_ERR_TIMEOUT if a bounded wait gave up (outputs since then are undefined,
- * later calls are not affected). */
+/* Waits for `stream`, then tells the calling thread whether a bounded wait of the
+ * products of this section has given up on the current device, on whatever
+ * stream and whoever called them, since the thread's last poll: NF_OK, or
+ * NF_ERR_TIMEOUT (outputs of products since that poll are undefined, later calls
+ * are not affected).  Each thread is told once, so polls of several threads take
+ * nothing from one another; a thread's first poll counts from its first product
+ * or, where it has called none (it replays a graph), from the process's start. */
 nf_status nf_fp8_poll(void* stream);
 /* Limit of every device-side wait of the products that this process calls (or
  * captures) from now on, in [1, 1e10] (2e9 at first). */

@@ -578,7 +578,7 @@ def gemm_fp8_grouped(a, a_s, b, b_s, group_off, c, c_s=None, epilogue=NF_EPI_STO
 
 
 def fp8_poll(stream=None):
-    """nf_fp8_poll: wait for the stream, then report and clear what the 8-bit products flagged."""
+    """nf_fp8_poll: wait for the stream; raises where an 8-bit product gave up since this thread's last poll."""
     check(lib().nf_fp8_poll(stream_handle(stream)))
 
 

@@ -1,4 +1,5 @@
 // C ABI of the 8-bit operators: argument checks, tensor maps, launches.
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -30,6 +31,32 @@ nf_status fail8(nf_status s, const char* fmt, ...) {
   } while (0)
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// What nf_fp8_poll goes by.  The kernels count, for a device, the waits that gave up, and the
+// counts only grow; a host thread is told when they differ from what it saw last, so no
+// thread's poll takes a report away from another's.  A thread that begins with a product
+// starts from the highest counts that any poll has read by then: its own timeouts come later.
+struct GaveUp {
+  uint64_t tiles = 0, rows = 0;  // by the two product kernels
+  bool begun = false;            // (of a thread) holds what the thread starts from
+};
+constexpr int MAX_DEVICES = 64;
+std::mutex g_mu;
+GaveUp g_read[MAX_DEVICES];               // under g_mu: the highest counts read by a poll
+thread_local GaveUp t_seen[MAX_DEVICES];  // what this thread was told of
+
+void begin_products(int dev) {
+  if (t_seen[dev].begun) return;
+  std::lock_guard<std::mutex> lk(g_mu);
+  t_seen[dev] = g_read[dev];
+  t_seen[dev].begun = true;
+}
+
+// The current device, for a section that keeps something by device.
+nf_status device_number(int* dev) {
+  NF_CUDA8(cudaGetDevice(dev));
+  return *dev < MAX_DEVICES ? NF_OK : fail8(NF_ERR_UNSUPPORTED, "device %d: %d are counted", *dev, MAX_DEVICES);
+}
 
 // SM count of the current device (a cached attribute query).
 int sm_count() {
@@ -99,6 +126,9 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
     return fail8(NF_ERR_INVALID_ARG, "scales and offsets must be 4-byte aligned");
   const int sms = sm_count();
   if (sms <= 0) return fail8(NF_ERR_CUDA, "no CUDA device");
+  int dev = 0;
+  if (nf_status e = device_number(&dev)) return e;
+  begin_products(dev);
   const bool capped = max_sms > 0 && max_sms < sms;
   const bool few = !capped && few_rows(M, N, K, groups, two, sms);
   nf::F8RowsChoice c{};
@@ -220,15 +250,25 @@ nf_status nf_fp8_set_timeout(int64_t timeout_ns) {
 }
 
 nf_status nf_fp8_poll(void* stream) {
-  // one poll at a time: they share the words that the status is taken into
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lk(mu);
-  uint32_t bits = 0, more = 0;
-  NF_CUDA8(nf::take_gemm_f8_status(&bits, static_cast<cudaStream_t>(stream)));
-  NF_CUDA8(nf::take_gemm_f8_wrows_status(&more, static_cast<cudaStream_t>(stream)));
-  bits |= more;
-  if (!bits) return NF_OK;
-  return fail8(NF_ERR_TIMEOUT, "nf_gemm_fp8: a device-side wait timed out (status 0x%x)", bits);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int dev = 0;
+  if (nf_status e = device_number(&dev)) return e;
+  GaveUp now;
+  NF_CUDA8(nf::read_gemm_f8_gave_up(&now.tiles, st));
+  NF_CUDA8(nf::read_gemm_f8_wrows_gave_up(&now.rows, st));
+  NF_CUDA8(cudaStreamSynchronize(st));
+  GaveUp& seen = t_seen[dev];
+  const bool more = now.tiles != seen.tiles || now.rows != seen.rows;
+  seen = now;
+  seen.begun = true;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    GaveUp& all = g_read[dev];
+    all.tiles = std::max(all.tiles, now.tiles);
+    all.rows = std::max(all.rows, now.rows);
+  }
+  if (!more) return NF_OK;
+  return fail8(NF_ERR_TIMEOUT, "nf_gemm_fp8: a device-side wait timed out");
 }
 
 }  // extern "C"

@@ -51,10 +51,9 @@ struct F8GemmArgs {
 // (SwiGLU: 64) rows, x 128 columns.
 cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& tmB,
                            const F8GemmArgs& args, int sms, cudaStream_t stream);
-// The bits that the kernels of launch_gemm_f8 raised on the current device, and zeros
-// in their place; waits for the stream.
-cudaError_t take_gemm_f8_status(uint32_t* bits, cudaStream_t stream);
-
+// How often waits of the kernels of launch_gemm_f8 gave up on the current device since the
+// process began, copied to *count in the stream's order.
+cudaError_t read_gemm_f8_gave_up(uint64_t* count, cudaStream_t stream);
 
 // The same for few rows: tiles of 128 features x tok rows of A (tmX: the rows of A in
 // boxes of tok rows; tok 16, 32, 64 and, but for SwiGLU, 128), `units` clusters of
@@ -66,6 +65,6 @@ struct F8RowsChoice {
 F8RowsChoice gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups);
 cudaError_t launch_gemm_f8_wrows(int epi, int tok, const CUtensorMap& tmW, const CUtensorMap& tmX,
                                  const F8GemmArgs& args, long long units, cudaStream_t stream);
-cudaError_t take_gemm_f8_wrows_status(uint32_t* bits, cudaStream_t stream);
+cudaError_t read_gemm_f8_wrows_gave_up(uint64_t* count, cudaStream_t stream);
 
 }  // namespace nf

@@ -25,7 +25,7 @@
 //  * A product with tiles for less than a half (a quarter) of the SMs is cut along K between
 //    the two (four) CTAs of a cluster (SPLIT): each finishes its part of the tile's columns
 //    (SwiGLU: of its rows), with the others' sums from their shared memory.
-//  * Every wait is bounded; one that gives up flags the status word, and the kernel
+//  * Every wait is bounded; one that gives up is counted, and the kernel
 //    drains what it has in flight (bounded) and frees tensor memory.
 #include <atomic>
 #include <type_traits>
@@ -75,7 +75,9 @@ struct Tail {
 constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 8 * STORE_BYTES + TAIL_BYTES;
 static_assert(sizeof(Tail) <= TAIL_BYTES && SMEM <= 232448, "shared memory");
 
-__device__ uint32_t g_status;
+// Times that a wait of this file's kernels gave up on the device.  It only grows: callers
+// compare it with what they last saw.
+__device__ unsigned long long g_gave_up;
 
 struct Tile {
   int m0, m_lim, tn, e;
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tail->issued = issued;
       tail->phases = phases;
       if (!ok) {
-        raise_status(&g_status, ST_TIMEOUT);
+        atomicAdd(&g_gave_up, 1ULL);
         *abort_flag = 1;
       }
     }
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok && one) {
-        raise_status(&g_status, ST_TIMEOUT);
+        atomicAdd(&g_gave_up, 1ULL);
         *abort_flag = 1;
       }
       if (one) tail->issuer[h] = any ? lane : 32;
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) {
-        raise_status(&g_status, ST_TIMEOUT);
+        atomicAdd(&g_gave_up, 1ULL);
         *abort_flag = 1;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     if (!ok) {
-      raise_status(&g_status, ST_TIMEOUT);
+      atomicAdd(&g_gave_up, 1ULL);
       *abort_flag = 1;
     }
   }
@@ -568,9 +570,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (SPLIT > 1) cluster_leave();
 }
-
-__device__ uint32_t g_taken;
-__global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0u); }
 
 // Clusters of SPLIT CTAs that the device holds at once; asked once a process.
 template <int EPI, int SPLIT>
@@ -652,14 +651,8 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
   }
 }
 
-cudaError_t take_gemm_f8_status(uint32_t* bits, cudaStream_t stream) {
-  void* at = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(&at, g_taken);
-  if (e != cudaSuccess) return e;
-  take_status_kernel<<<1, 1, 0, stream>>>();
-  e = cudaGetLastError();
-  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, at, 4, cudaMemcpyDeviceToHost, stream);
-  return e == cudaSuccess ? cudaStreamSynchronize(stream) : e;
+cudaError_t read_gemm_f8_gave_up(uint64_t* count, cudaStream_t stream) {
+  return cudaMemcpyFromSymbolAsync(count, g_gave_up, sizeof(*count), 0, cudaMemcpyDeviceToHost, stream);
 }
 
 }  // namespace nf

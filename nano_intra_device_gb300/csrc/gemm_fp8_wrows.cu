@@ -68,7 +68,7 @@ struct Tail {
 };
 static_assert(sizeof(Tail) <= TAIL_BYTES, "barrier block");
 
-__device__ uint32_t g_status;
+__device__ unsigned long long g_gave_up;  // as in gemm_fp8.cu
 
 template <int EPI, int TOK>
 __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       uint32_t st = 0, ph = 0;
       for (int i = 0; i < klen; ++i) {
         if (!mbar_wait(&tail->empty[st], ph ^ 1, tmo, abort_flag)) {
-          raise_status(&g_status, ST_TIMEOUT);
+          atomicAdd(&g_gave_up, 1ULL);
           *abort_flag = 1;
           break;
         }
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       for (int i = 0; i < klen; ++i) {
         if (!mbar_wait(&tail->tempty[acc], aph ^ 1, tmo, abort_flag) ||
             !mbar_wait(&tail->full[st], ph, tmo, abort_flag)) {
-          raise_status(&g_status, ST_TIMEOUT);
+          atomicAdd(&g_gave_up, 1ULL);
           *abort_flag = 1;
           break;
         }
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       for (int j = 0; j < AHEAD; ++j)
         if (ok && i + j < klen) ok = block(i + j, j);
     if (!ok) {
-      raise_status(&g_status, ST_TIMEOUT);
+      atomicAdd(&g_gave_up, 1ULL);
       *abort_flag = 1;
     }
     // The exchange: this CTA's sums to its shared memory (every product that read the
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     // (a release at cluster scope, behind the barrier that all of the CTA's writes precede)
     if (warp == 2 && lane < S) mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), lane));
     if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo))) {
-      raise_status(&g_status, ST_TIMEOUT);
+      atomicAdd(&g_gave_up, 1ULL);
       *abort_flag = 1;
     } else {
       const int nv = min(TOK, m_lim - m0);
@@ -427,9 +427,6 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
   }
   cluster_leave();
 }
-
-__device__ uint32_t g_taken;
-__global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0u); }
 
 template <int EPI, int TOK>
 void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, int clusters, int splits, cudaStream_t stream) {
@@ -551,14 +548,8 @@ cudaError_t launch_gemm_f8_wrows(int epi, int tok, const CUtensorMap& tmW, const
   return e < 0 ? cudaErrorInvalidValue : static_cast<cudaError_t>(e);
 }
 
-cudaError_t take_gemm_f8_wrows_status(uint32_t* bits, cudaStream_t stream) {
-  void* at = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(&at, g_taken);
-  if (e != cudaSuccess) return e;
-  take_status_kernel<<<1, 1, 0, stream>>>();
-  e = cudaGetLastError();
-  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, at, 4, cudaMemcpyDeviceToHost, stream);
-  return e == cudaSuccess ? cudaStreamSynchronize(stream) : e;
+cudaError_t read_gemm_f8_wrows_gave_up(uint64_t* count, cudaStream_t stream) {
+  return cudaMemcpyFromSymbolAsync(count, g_gave_up, sizeof(*count), 0, cudaMemcpyDeviceToHost, stream);
 }
 
 }  // namespace nf

@@ -675,6 +675,54 @@ def short_limit(p, limit, off, rows):
     assert torch.equal(p.c.float()[:rows], want[:rows])
 
 
+def _told():
+    try:
+        _lib.fp8_poll()
+        return False
+    except _lib.NanoflowError as e:
+        assert e.code == _lib.NF_ERR_TIMEOUT
+        return True
+
+
+def _in_a_thread(f):
+    import threading
+    out = []
+    t = threading.Thread(target=lambda: out.append(f()))
+    t.start()
+    t.join()
+    return out[0]
+
+
+@pytest.mark.parametrize("m,n,k", [(900, 5200, 2064), (64, 4096, 14336)])
+def test_polls_of_several_threads_take_no_report_from_one_another(m, n, k):
+    """A product that gave up is reported to its caller although another thread's poll came first, to each thread once."""
+    p = Product(m, n, k, STORE)
+    p.run()
+    _told()
+    for _ in range(20):
+        try:
+            _lib.fp8_set_timeout(1)
+            p.run()
+        finally:
+            _lib.fp8_set_timeout(2_000_000_000)
+        assert not _in_a_thread(lambda: (_told(), _told()))[1]
+        mine = _told()
+        if mine:
+            break
+    assert mine  # a limit of a nanosecond: some wait of 20 calls ran out
+    assert not _told()
+
+    def product_then_poll():  # a thread that begins with a product is not told of what was reported before
+        c = torch.zeros_like(p.c)
+        _lib.gemm_fp8(p.a, p.a_s, p.b.view(-1, p.k), p.b_s.squeeze(0), c)
+        return _told()
+
+    assert not _in_a_thread(product_then_poll)
+    p.run()
+    assert not _told()
+    p.check()
+
+
 def test_first_call_of_a_process_in_a_capture():
     """Nothing is allocated or looked up that a capture forbids."""
     code = """
