@@ -657,7 +657,8 @@ nf_status nf_gemm_fp8_grouped(const void* A, const float* a_s, const void* B, co
  * NF_ERR_TIMEOUT (outputs of products since that poll are undefined, later calls
  * are not affected).  Each thread is told once, so polls of several threads take
  * nothing from one another; a thread's first poll counts from its first product
- * or, where it has called none (it replays a graph), from the process's start. */
+ * or, where it has called none (it replays a graph), from the process's start.
+ * A stream that is being captured is refused. */
 nf_status nf_fp8_poll(void* stream);
 /* Limit of every device-side wait of the products that this process calls (or
  * captures) from now on, in [1, 1e10] (2e9 at first). */

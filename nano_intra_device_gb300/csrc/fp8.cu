@@ -253,6 +253,10 @@ nf_status nf_fp8_poll(void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int dev = 0;
   if (nf_status e = device_number(&dev)) return e;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  NF_CUDA8(cudaStreamIsCapturing(st, &capture));
+  if (capture != cudaStreamCaptureStatusNone)
+    return fail8(NF_ERR_INVALID_ARG, "the stream is being captured: a poll waits for it");
   GaveUp now;
   NF_CUDA8(nf::read_gemm_f8_gave_up(&now.tiles, st));
   NF_CUDA8(nf::read_gemm_f8_wrows_gave_up(&now.rows, st));

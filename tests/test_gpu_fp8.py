@@ -723,6 +723,22 @@ def test_polls_of_several_threads_take_no_report_from_one_another(m, n, k):
     p.check()
 
 
+def test_a_poll_inside_a_capture_is_refused_and_the_capture_goes_on():
+    p = Product(5, 528, 1040, STORE)
+    want = p.run()[0].clone()
+    _told()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(_lib.NanoflowError, match="captured") as e:
+            _lib.fp8_poll()
+        p.run()
+    assert e.value.code == _lib.NF_ERR_INVALID_ARG
+    p.c.zero_()
+    graph.replay()
+    _lib.fp8_poll()
+    assert torch.equal(p.c, want)
+
+
 def test_first_call_of_a_process_in_a_capture():
     """Nothing is allocated or looked up that a capture forbids."""
     code = """
