@@ -513,14 +513,22 @@ def _blocks(n):
     return (n + 127) // 128
 
 
+def _rows(name, t, dtype, outer, last, dev):
+    """_arg for a matrix, or several as one, of `outer` rows of `last` elements: a transposed one has as many (row
+    scales by row instead of by column block, weights [K, N])."""
+    if t.dtype is not dtype or not t.is_contiguous() or \
+            (t.shape != (outer, last) and (t.numel() != outer * last or (outer > 1 and last > 1 and t.shape[-1] != last))):
+        raise ValueError(f"{name}: need {outer} contiguous rows of {last} elements of {dtype}, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr() if t.get_device() == dev else _on(name, t, dev)
+
+
 def rmsnorm_fp8(x, g, q, s, eps, r=None, h=None, stream=None):
     """nf_rmsnorm_fp8: RMSNorm of x (+ r, kept in h) to 8-bit rows q [rows, hidden] e4m3 and
     s [ceil(hidden / 128), rows] fp32."""
     (e4m3, bf16, f32, _), (rows, n), dev = _types(), x.shape, x.get_device()
-    size = rows * n
-    check(lib().nf_rmsnorm_fp8(_arg("x", x, bf16, size, dev), None if r is None else _arg("r", r, bf16, size, dev),
-                               _arg("g", g, bf16, n, dev), None if h is None else _arg("h", h, bf16, size, dev),
-                               _arg("q", q, e4m3, size, dev), _arg("s", s, f32, _blocks(n) * rows, dev), rows, n, eps,
+    check(lib().nf_rmsnorm_fp8(_arg("x", x, bf16, rows * n, dev), None if r is None else _rows("r", r, bf16, rows, n, dev),
+                               _arg("g", g, bf16, n, dev), None if h is None else _rows("h", h, bf16, rows, n, dev),
+                               _rows("q", q, e4m3, rows, n, dev), _rows("s", s, f32, _blocks(n), rows, dev), rows, n, eps,
                                _call_stream(dev, stream)))
 
 
@@ -530,7 +538,7 @@ def quant_fp8(x, q, s, index=None, stream=None):
     (e4m3, bf16, f32, i32), (src, n), dev = _types(), x.shape, x.get_device()
     rows = src if index is None else index.numel()
     check(lib().nf_quant_fp8(_arg("x", x, bf16, src * n, dev), src, None if index is None else _arg("index", index, i32, rows, dev),
-                             _arg("q", q, e4m3, rows * n, dev), _arg("s", s, f32, _blocks(n) * rows, dev), rows, n,
+                             _rows("q", q, e4m3, rows, n, dev), _rows("s", s, f32, _blocks(n), rows, dev), rows, n,
                              _call_stream(dev, stream)))
 
 
@@ -539,8 +547,8 @@ def quant_fp8_weights(w, q, s, stream=None):
     s [..., ceil(rows / 128), ceil(cols / 128)] fp32."""
     (e4m3, bf16, f32, _), (rows, n), dev, size = _types(), w.shape[-2:], w.get_device(), w.numel()
     mats = size // (rows * n) if size else 0
-    check(lib().nf_quant_fp8_weights(_arg("w", w, bf16, size, dev), _arg("q", q, e4m3, size, dev),
-                                     _arg("s", s, f32, mats * _blocks(rows) * _blocks(n), dev), mats, rows, n,
+    check(lib().nf_quant_fp8_weights(_arg("w", w, bf16, size, dev), _rows("q", q, e4m3, mats * rows, n, dev),
+                                     _rows("s", s, f32, mats * _blocks(rows), _blocks(n), dev), mats, rows, n,
                                      _call_stream(dev, stream)))
 
 
@@ -553,9 +561,9 @@ def _product(a, a_s, b, b_s, groups, c, c_s, epilogue, dev):
     eight = epilogue == NF_EPI_SWIGLU_FP8
     if eight and c_s is None:
         raise ValueError("c_s: an 8-bit output needs its scales")
-    return ((_arg("a", a, e4m3, m * k, dev), _arg("a_s", a_s, f32, kb * m, dev),
-             _arg("b", b, e4m3, groups * two * n * k, dev), _arg("b_s", b_s, f32, groups * two * nb * kb, dev)),
-            (_arg("c", c, e4m3 if eight else bf16, m * n, dev), _arg("c_s", c_s, f32, nb * m, dev) if eight else None),
+    return ((_arg("a", a, e4m3, m * k, dev), _rows("a_s", a_s, f32, kb, m, dev),
+             _rows("b", b, e4m3, groups * two * n, k, dev), _rows("b_s", b_s, f32, groups * two * nb, kb, dev)),
+            (_rows("c", c, e4m3 if eight else bf16, m, n, dev), _rows("c_s", c_s, f32, nb, m, dev) if eight else None),
             (m, n, k))
 
 
@@ -564,7 +572,7 @@ def gemm_fp8(a, a_s, b, b_s, c, c_s=None, r=None, epilogue=NF_EPI_STORE, max_sms
     [2 N, K].  NF_EPI_SWIGLU_FP8: c e4m3 with scales c_s, else bf16."""
     dev = a.get_device()
     ins, outs, size = _product(a, a_s, b, b_s, 1, c, c_s, epilogue, dev)
-    check(lib().nf_gemm_fp8(*ins, *outs, None if r is None else _arg("r", r, c.dtype, size[0] * size[1], dev), *size,
+    check(lib().nf_gemm_fp8(*ins, *outs, None if r is None else _rows("r", r, c.dtype, size[0], size[1], dev), *size,
                             epilogue, max_sms, _call_stream(dev, stream)))
 
 

@@ -182,3 +182,34 @@ def test_binding_wants_the_scales_of_an_8_bit_output():
     call, good = CALLS["swiglu8"]
     with pytest.raises(ValueError, match="c_s"):
         call(**(good | dict(c_s=None)))
+
+
+def _other_way_round(t):
+    """Contiguous, with as many elements, rows and columns of the last two dimensions exchanged."""
+    return t.view(t.shape[:-2] + (t.shape[-1], t.shape[-2]))
+
+
+@pytest.mark.parametrize("name,k", [(n, k) for n, (_, good) in CALLS.items() for k, t in good.items() if isinstance(t, torch.Tensor) and t.dim() > 1])
+def test_binding_refuses_the_other_way_round(name, k):
+    """Scales [rows, blocks], weights [K, N] and the like have the right count and would give wrong results."""
+    call, good = CALLS[name]
+    big = dict(good)
+    if name in ("gemm", "swiglu8", "grouped"):  # (three rows and three blocks of K would be the same either way)
+        big |= dict(a=z(4, 272, t=E), a_s=z(3, 4, t=F), c=z(4, good["c"].shape[1], t=good["c"].dtype))
+        big |= dict(r=z(4, 136)) if name == "gemm" else dict(c_s=z(2, 4, t=F)) if name == "swiglu8" else {}
+    if name == "norm":
+        big |= {n: z(4, 272, t=good[n].dtype) for n in ("x", "q", "r", "h")} | dict(s=z(3, 4, t=F))
+    with pytest.raises(ValueError, match="CUDA device"):
+        call(**big)
+    with pytest.raises(ValueError) as e:
+        call(**(big | {k: _other_way_round(big[k])}))
+    assert "CUDA device" not in str(e.value)
+
+
+def test_binding_takes_every_naming_of_the_same_rows():
+    """One row's scales in either order and matrices stacked as one are the same memory."""
+    call, good = CALLS["swiglu8"]
+    one = good | dict(a=z(1, 272, t=E), a_s=z(1, 3, t=F), c=z(1, 144, t=E), c_s=z(2, t=F))
+    for more in ({}, dict(b=z(2, 144, 272, t=E)), dict(b_s=z(4, 3, t=F))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(**(one | more))
