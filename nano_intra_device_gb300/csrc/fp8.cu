@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "../../include/nanoflow.h"
+#include "by_device.h"
 #include "fp8.h"
 #include "internal.h"
 #include "kernels.h"
@@ -40,10 +41,9 @@ struct GaveUp {
   uint64_t tiles = 0, rows = 0;  // by the two product kernels
   bool begun = false;            // (of a thread) holds what the thread starts from
 };
-constexpr int MAX_DEVICES = 64;
 std::mutex g_mu;
-GaveUp g_read[MAX_DEVICES];               // under g_mu: the highest counts read by a poll
-thread_local GaveUp t_seen[MAX_DEVICES];  // what this thread was told of
+GaveUp g_read[nf::MAX_DEVICES];               // under g_mu: the highest counts read by a poll
+thread_local GaveUp t_seen[nf::MAX_DEVICES];  // what this thread was told of
 
 void begin_products(int dev) {
   if (t_seen[dev].begun) return;
@@ -55,7 +55,7 @@ void begin_products(int dev) {
 // The current device, for a section that keeps something by device.
 nf_status device_number(int* dev) {
   NF_CUDA8(cudaGetDevice(dev));
-  return *dev < MAX_DEVICES ? NF_OK : fail8(NF_ERR_UNSUPPORTED, "device %d: %d are counted", *dev, MAX_DEVICES);
+  return *dev < nf::MAX_DEVICES ? NF_OK : fail8(NF_ERR_UNSUPPORTED, "device %d: %d are counted", *dev, nf::MAX_DEVICES);
 }
 
 // SM count of the current device (a cached attribute query).
@@ -132,7 +132,7 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
   const bool capped = max_sms > 0 && max_sms < sms;
   const bool few = !capped && few_rows(M, N, K, groups, two, sms);
   nf::F8RowsChoice c{};
-  if (few) c = nf::gemm_f8_wrows_choice(epilogue, M, N, K, groups);
+  if (few) NF_CUDA8(nf::gemm_f8_wrows_choice(epilogue, M, N, K, groups, &c));
   CUtensorMap ta, tb;
   if (!nf::make_tmap_8bit(&ta, A, M, K, few ? c.tok : 128) ||
       !nf::make_tmap_8bit(&tb, B, static_cast<uint64_t>(groups) * N * (two ? 2 : 1), K,

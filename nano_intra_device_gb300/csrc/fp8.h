@@ -62,7 +62,7 @@ struct F8RowsChoice {
   int tok, splits;
   long long units;
 };
-F8RowsChoice gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups);
+cudaError_t gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups, F8RowsChoice* choice);
 cudaError_t launch_gemm_f8_wrows(int epi, int tok, const CUtensorMap& tmW, const CUtensorMap& tmX,
                                  const F8GemmArgs& args, long long units, cudaStream_t stream);
 cudaError_t read_gemm_f8_wrows_gave_up(uint64_t* count, cudaStream_t stream);

@@ -27,9 +27,9 @@
 //    (SwiGLU: of its rows), with the others' sums from their shared memory.
 //  * Every wait is bounded; one that gives up is counted, and the kernel
 //    drains what it has in flight (bounded) and frees tensor memory.
-#include <atomic>
 #include <type_traits>
 
+#include "by_device.h"
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -571,12 +571,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (SPLIT > 1) cluster_leave();
 }
 
-// Clusters of SPLIT CTAs that the device holds at once; asked once a process.
+// Clusters of SPLIT CTAs that the current device holds at once; asked once a device.
 template <int EPI, int SPLIT>
-int most_clusters() {
-  static std::atomic<int> cache;
-  int n = cache.load(std::memory_order_relaxed);
-  if (n == 0) {
+cudaError_t most_clusters(int* most) {
+  static ByDevice<1> kept;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return kept.get(dev, 0, most, [](int* n) {
     const auto kernel = gemm_f8_kernel<EPI, SPLIT>;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -588,14 +590,9 @@ int most_clusters() {
     cfg.dynamicSmemBytes = SMEM;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    if (set_smem_limit(reinterpret_cast<const void*>(kernel), SMEM) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = -1;
-    }
-    cache.store(n, std::memory_order_relaxed);
-  }
-  return n;
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), SMEM);
+    return e == cudaSuccess ? cudaOccupancyMaxActiveClusters(n, kernel, &cfg) : e;
+  });
 }
 
 template <int EPI, int SPLIT>
@@ -628,8 +625,11 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
     cudaError_t e = cudaSuccess;
     auto cut = [&](auto epilogue, auto split) {
       constexpr int EPI = decltype(epilogue)::value, SPLIT = decltype(split)::value;
-      if (nk < 8 * SPLIT || SPLIT * most > sms || most > most_clusters<EPI, SPLIT>()) return false;
-      e = launch<EPI, SPLIT>(tmA, tmB, args, static_cast<int>(SPLIT * most), stream);
+      if (nk < 8 * SPLIT || SPLIT * most > sms) return false;
+      int fit = 0;
+      e = most_clusters<EPI, SPLIT>(&fit);
+      if (e == cudaSuccess && most > fit) return false;
+      if (e == cudaSuccess) e = launch<EPI, SPLIT>(tmA, tmB, args, static_cast<int>(SPLIT * most), stream);
       return true;
     };
     auto either = [&](auto epilogue) {

@@ -20,9 +20,9 @@
 // Every wait is bounded.  After one gave up the CTAs of a cluster still meet at the
 // same exchange and the barrier before exit.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
+#include "by_device.h"
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -462,25 +462,22 @@ cudaError_t launch(const CUtensorMap& tmW, const CUtensorMap& tmX, const F8GemmA
   return cudaLaunchKernelEx(&cfg, gemm_f8_wrows_kernel<EPI, TOK>, tmW, tmX, args);
 }
 
-// Clusters of `splits` CTAs that the device holds at once, one CTA an SM (more is not
-// reported for kernels with tensor memory); asked once a process.
+// Clusters of `splits` CTAs that the current device holds at once, one CTA an SM (more is
+// not reported for kernels with tensor memory); asked once a device.
 template <int EPI, int TOK>
-int most_clusters(int splits) {
-  static std::atomic<int> cache[MAX_CLUSTER + 1];
-  int n = cache[splits].load(std::memory_order_relaxed);
-  if (n == 0) {
+cudaError_t most_clusters(int splits, int* most) {
+  static ByDevice<MAX_CLUSTER + 1> kept;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return kept.get(dev, splits, most, [splits](int* n) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[2];
     configure<EPI, TOK>(&cfg, at, 1, splits, nullptr);
     cfg.numAttrs = 1;
-    if (prepare<EPI, TOK>() != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, gemm_f8_wrows_kernel<EPI, TOK>, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = -1;
-    }
-    cache[splits].store(n, std::memory_order_relaxed);
-  }
-  return n > 0 ? n : 0;
+    const cudaError_t e = prepare<EPI, TOK>();
+    return e == cudaSuccess ? cudaOccupancyMaxActiveClusters(n, gemm_f8_wrows_kernel<EPI, TOK>, &cfg) : e;
+  });
 }
 
 // f(epilogue, rows of A of a tile) with both as compile-time constants; -1 for others.
@@ -508,8 +505,8 @@ int dispatch(int epi, int tok, F f) {
 
 }  // namespace
 
-F8RowsChoice gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups) {
-  F8RowsChoice c{};
+cudaError_t gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups, F8RowsChoice* choice) {
+  F8RowsChoice& c = *choice;
   const int rows = (M + groups - 1) / groups;  // of a group, were they even
   const int most = epi >= F8_SWIGLU ? 64 : 128;
   // by groups: room for twice the mean, as B is read again for each further tile
@@ -526,15 +523,22 @@ F8RowsChoice gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups) {
   const long long busy = wt * (groups > 1 ? (M < groups ? M : groups) : (M + c.tok - 1) / c.tok);
   const int nk = (K + BK - 1) / BK;
   c.splits = 1;
-  for (int s = 2; s <= MAX_CLUSTER && 4 * s <= nk; ++s)
-    if (busy <= dispatch(epi, c.tok, [&](auto e, auto k) {
-          constexpr int EPI = decltype(e)::value, TOK = decltype(k)::value;
-          const int one = most_clusters<EPI, TOK>(s);
-          if (Cfg<EPI, TOK>::PER_SM == 1) return one;
-          return s > 2 ? std::max(2 * one, most_clusters<EPI, TOK>((s + 1) / 2)) : 2 * one;
-        }))
-      c.splits = s;
-  return c;
+  for (int s = 2; s <= MAX_CLUSTER && 4 * s <= nk; ++s) {
+    int fit = 0;
+    const int e = dispatch(epi, c.tok, [&](auto epilogue, auto tok) {
+      constexpr int EPI = decltype(epilogue)::value, TOK = decltype(tok)::value;
+      int half = 0;
+      cudaError_t e = most_clusters<EPI, TOK>(s, &fit);
+      if (Cfg<EPI, TOK>::PER_SM == 1) return static_cast<int>(e);
+      fit *= 2;
+      if (e == cudaSuccess && s > 2) e = most_clusters<EPI, TOK>((s + 1) / 2, &half);
+      fit = std::max(fit, half);
+      return static_cast<int>(e);
+    });
+    if (e) return e < 0 ? cudaErrorInvalidValue : static_cast<cudaError_t>(e);
+    if (busy <= fit) c.splits = s;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_gemm_f8_wrows(int epi, int tok, const CUtensorMap& tmW, const CUtensorMap& tmX,

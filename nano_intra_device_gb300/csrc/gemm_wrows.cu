@@ -29,8 +29,7 @@
 //    exchange rounds, also after an error (with zeros in place of the
 //    accumulator), and meet at a cluster barrier before they exit, so no CTA
 //    leaves while a peer may still address its shared memory.
-#include <atomic>
-
+#include "by_device.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -637,22 +636,21 @@ cudaError_t wr_launch(const CUtensorMap& tmW, const CUtensorMap& tmW2, const CUt
 // Both variants take one SM per CTA, so one query serves them.
 template <int EPI, int TOK>
 int wr_max_clusters(int S) {
-  static std::atomic<int> cache[WR_MAX_CLUSTER + 1];  // 0: not asked yet
-  if (cache[S].load(std::memory_order_relaxed) == 0) {
-    int n = 0;
+  static ByDevice<WR_MAX_CLUSTER + 1> kept;
+  int dev = 0, most = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const cudaError_t e = kept.get(dev, S, &most, [S](int* n) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[1];
     wr_config<EPI, TOK, false>(&cfg, at, 1, S, nullptr);
-    if (wr_prepare<EPI, TOK, false>() != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, gemm_wrows_kernel<EPI, TOK, false>, &cfg) !=
-            cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
-    }
-    cache[S].store(n > 0 ? n : -1, std::memory_order_relaxed);
-  }
-  const int c = cache[S].load(std::memory_order_relaxed);
-  return c > 0 ? c : 0;
+    const cudaError_t e = wr_prepare<EPI, TOK, false>();
+    return e == cudaSuccess
+               ? cudaOccupancyMaxActiveClusters(n, gemm_wrows_kernel<EPI, TOK, false>, &cfg)
+               : e;
+  });
+  if (e == cudaSuccess) return most;
+  cudaGetLastError();
+  return 0;
 }
 
 template <int EPI, int TOK>

@@ -213,3 +213,48 @@ def test_binding_takes_every_naming_of_the_same_rows():
     for more in ({}, dict(b=z(2, 144, 272, t=E)), dict(b_s=z(4, 3, t=F))):
         with pytest.raises(ValueError, match="CUDA device"):
             call(**(one | more))
+
+
+# ------------------------------------------------------------------ host code
+
+def run_host_code(tmp_path, code):
+    """Compile a program against csrc/ with the host compiler and return what it prints."""
+    import os
+    import subprocess
+    src, exe = tmp_path / "main.cpp", tmp_path / "main"
+    src.write_text(code)
+    csrc = os.path.join(os.path.dirname(_lib.__file__), "csrc")
+    r = subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    return subprocess.run([str(exe)], capture_output=True, text=True, check=True, timeout=60).stdout
+
+
+def test_answers_are_kept_by_device_and_failures_are_not(tmp_path):
+    out = run_host_code(tmp_path, """
+#include "by_device.h"
+#include <cstdio>
+int asked = 0;
+int main() {
+  static nf::ByDevice<9> kept;
+  auto get = [](int dev, int which, int says, int code) {
+    int n = -1;
+    const int e = kept.get(dev, which, &n, [&](int* a) { ++asked; *a = says; return code; });
+    std::printf("%d:%d:%d ", e, e ? -1 : n, asked);
+  };
+  get(0, 2, 36, 0), get(0, 2, 99, 0);  // asked once
+  get(1, 2, 33, 0), get(0, 2, 99, 0), get(1, 2, 99, 0);  // another device has its own
+  get(0, 4, 18, 700), get(0, 4, 17, 0), get(0, 4, 99, 0);  // a failure is told and not kept
+  get(0, 8, 0, 0), get(0, 8, 99, 0);  // none fits: an answer too
+  get(64, 2, 5, 0), get(64, 2, 6, 0);  // a device beyond those counted is asked every time
+}
+""")
+    assert out.split() == ["0:36:1", "0:36:1", "0:33:2", "0:36:2", "0:33:2", "700:-1:3", "0:17:4", "0:17:4", "0:0:5", "0:0:5", "0:5:6", "0:6:7"]
+
+
+def test_no_kernel_keeps_occupancy_by_process():
+    """Each query of a device's occupancy goes through the answers kept by device."""
+    import glob
+    import os
+    for path in glob.glob(os.path.join(os.path.dirname(_lib.__file__), "csrc", "*.cu")):
+        text = open(path).read()
+        assert text.count("cudaOccupancyMaxActiveClusters(") == text.count("kept.get("), path
