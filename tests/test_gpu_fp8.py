@@ -769,6 +769,205 @@ print("captured")
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
+def test_first_cut_of_a_process_in_a_capture(tmp_path):
+    """K long enough for every cut: clusters are counted and launched for the first time inside a capture, with the results of calls outside one."""
+    code = """
+import sys
+import torch
+from nano_intra_device_gb300 import _lib
+e = torch.float8_e4m3fn
+gen = torch.Generator("cuda").manual_seed(1)
+def case(m, n, k, epi, top=1e9):  # without a limit a few codes are NaN (beyond 464), and their rows or columns
+    two = 2 if epi >= 2 else 1
+    a = (torch.randn(m, k, device="cuda", generator=gen) * 100).clamp(-top, top).to(e)
+    b = (torch.randn(two * n, k, device="cuda", generator=gen) * 100).clamp(-top, top).to(e)
+    a_s, b_s = torch.rand(k // 128, m, device="cuda", generator=gen) / 100, torch.rand(two, (n + 127) // 128, k // 128, device="cuda", generator=gen) / 100
+    c = torch.zeros(m, n, device="cuda").to(e if epi == 3 else torch.bfloat16)
+    return dict(a=a, a_s=a_s, b=b, b_s=b_s, c=c, c_s=torch.zeros((n + 127) // 128, m, device="cuda") if epi == 3 else None, epilogue=epi)
+cases = [case(200, 528, 4096, 0), case(200, 528, 2048, 3), case(3, 528, 4096, 0), case(3, 528, 4096, 2)]
+cases += [case(200, 528, 4096, 0, 448), case(200, 528, 2048, 3, 448), case(3, 528, 4096, 0, 448), case(3, 528, 4096, 2, 448)]
+if sys.argv[1] == "captured":
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for c in cases:
+            _lib.gemm_fp8(**c)
+    g.replay()
+else:
+    for c in cases:
+        _lib.gemm_fp8(**c)
+torch.cuda.synchronize()
+_lib.fp8_poll()
+for i, c in enumerate(cases):
+    b = c["b"].float().view(-1, c["c"].shape[1], c["a"].shape[1])
+    w = [x * s.repeat_interleave(128, 0)[:len(x)].repeat_interleave(128, 1) for x, s in zip(b.double(), c["b_s"].double())]
+    y = [(c["a"].double() * c["a_s"].double().t().repeat_interleave(128, 1)) @ x.t() for x in w]
+    if c["epilogue"] >= 2:
+        y = [y[0] * torch.sigmoid(y[0]) * y[1]]
+    got = c["c"].double() * (c["c_s"].double().t().repeat_interleave(128, 1)[:, :c["c"].shape[1]] if c["c_s"] is not None else 1)
+    nan = torch.isnan(y[0])
+    assert i < 4 or not nan.any()
+    if c["epilogue"] == 3:  # a NaN makes its block of 128 NaN
+        nan = torch.cat([p.any(1, keepdim=True).expand_as(p) for p in nan.split(128, 1)], 1)
+    assert torch.equal(torch.isnan(got), nan)
+    d, want = (got - y[0])[~nan], y[0][~nan]
+    assert d.norm() <= 2.0 ** -4 * want.norm(), d.norm() / want.norm()
+torch.save([c["c"].float().cpu() for c in cases], sys.argv[2])
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    outs = []
+    for how in ("captured", "called"):
+        out = tmp_path / how
+        r = subprocess.run([sys.executable, "-c", code, how, str(out)], cwd=root, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stderr[-2000:]
+        outs.append(torch.load(out))
+    # equal bits, so the same cuts: a cut left out would add up in another order
+    assert all(torch.equal(a.nan_to_num(1e9), b.nan_to_num(1e9)) for a, b in zip(*outs))
+
+
+# ------------------------------------------------------------------ products cut along K
+
+CUT = [(200, 528, 2064), (200, 528, 4112)]  # tiles that leave room for two CTAs each, and for four (16 and 32 blocks of K)
+
+
+@pytest.mark.parametrize("epi", [STORE, RESID, SWIGLU, SWIGLU8])
+@pytest.mark.parametrize("m,n,k", CUT)
+def test_cut_products_repeat_in_a_graph_and_on_two_streams(m, n, k, epi):
+    ps = [Product(m, n, k, epi, seed=i) for i in (11, 12)]
+    want = [p.run()[0].float().clone() for p in ps]
+    ps[0].check(), ps[1].check()
+    for _ in range(20):
+        assert torch.equal(ps[0].run()[0].float(), want[0])
+    new = lambda p: (torch.zeros_like(p.c.float()).to(p.c.dtype), None if p.c_s is None else torch.zeros_like(p.c_s))  # noqa: E731
+    outs, streams = [[new(p) for _ in range(10)] for p in ps], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for p, o, st in zip(ps, outs, streams):
+            p.run(None, *o[i], stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(c.float(), w) for w, o in zip(want, outs) for c, _ in o)
+    out = new(ps[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            ps[0].run(None, *out)
+    for _ in range(3):
+        out[0].view(torch.uint8).zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0].float(), want[0])
+    _lib.fp8_poll()
+
+
+@pytest.mark.parametrize("m,k", [(200, 2048), (200, 4096), (40, 4096)])
+def test_a_chain_of_cut_products_over_the_same_buffers(m, k):
+    """Each call reads what the one ahead wrote, without a wait and captured, as with a wait after each."""
+    up, down = Product(m, k, k, SWIGLU8, seed=13), Product(m, k, k, RESID, seed=14)
+    up.b_s.mul_(0.02), down.b_s.mul_(0.02)
+    x0 = torch.randn(m, k, device=DEV).bfloat16()
+    x, g = x0.clone(), torch.ones(k, device=DEV, dtype=BF16)
+    q, s = torch.zeros(m, k, device=DEV).to(E4M3), torch.zeros(k // 128, m, device=DEV)
+    c, c_s = torch.zeros(m, k, device=DEV).to(E4M3), torch.zeros(k // 128, m, device=DEV)
+    calls = [lambda: _lib.rmsnorm_fp8(x, g, q, s, 1e-5),
+             lambda: _lib.gemm_fp8(q, s, up.b.view(-1, k), up.b_s.squeeze(0), c, c_s=c_s, epilogue=SWIGLU8),
+             lambda: _lib.gemm_fp8(c, c_s, down.b.view(-1, k), down.b_s.squeeze(0), x, r=x, epilogue=RESID)] * 6
+
+    def layers(wait):
+        x.copy_(x0)
+        for call in calls:
+            call()
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return x.clone()
+
+    want = layers(True)
+    assert torch.isfinite(want).all() and not torch.equal(want, x0)
+    for _ in range(5):
+        assert torch.equal(layers(False), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.copy_(x0)
+        for call in calls:
+            call()
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x, want)
+    _lib.fp8_poll()
+
+
+@pytest.mark.parametrize("epi", [STORE, RESID, SWIGLU, SWIGLU8])
+@pytest.mark.parametrize("m,n,k", CUT)
+def test_cut_products_under_limits_of_the_grid(m, n, k, epi):
+    """Limits that leave the cut in four, in two and none; with none the sums of K's parts are one sum."""
+    p = Product(m, n, k, epi)
+    for max_sms in (0, 151, 80, 40, 20, 10, 1):
+        p.c.view(torch.uint8).zero_()
+        p.run(max_sms=max_sms)
+        _lib.fp8_poll()
+        p.check()
+
+
+@pytest.mark.parametrize("epi", [STORE, SWIGLU8])
+@pytest.mark.parametrize("m,n,k", CUT)
+def test_cut_products_of_every_code(m, n, k, epi):
+    p = Product(m, n, k, epi, codes="every")
+    p.run()
+    p.check()
+
+
+@pytest.mark.parametrize("k", [2048, 4096])
+def test_cut_products_add_up_in_fp32(k):
+    """As test_gemm_adds_up_in_fp32, with the large products and their negatives in every CTA's part of K."""
+    p = Product(200, 128, k, STORE)
+    p.a_s.fill_(1.0), p.b_s.fill_(1.0)
+    a, b = torch.zeros(200, k, device=DEV), torch.zeros(128, k, device=DEV)
+    a[:, ::128], b[:, ::128] = 448, 448
+    b[:, 128::256] = -448
+    a[:, 1::2], b[:, 1::2] = 1, 1
+    p.a, p.b = a.to(E4M3), b.to(E4M3).view(1, 1, 128, k)
+    p.run()
+    assert (p.c.float() == k // 2).all()
+
+
+@pytest.mark.parametrize("epi", [STORE, SWIGLU, SWIGLU8])
+@pytest.mark.parametrize("k", [2064, 4112])
+def test_cut_products_keep_nan_scales_in_their_rows_and_columns(epi, k):
+    """A NaN in the part of K of one CTA, for a row in the columns or rows that another one finishes."""
+    p = Product(200, 384, k, epi)
+    clean = [None if t is None else t.clone() for t in p.run()]
+    p.a_s[1, 2] = p.a_s[-1, 70] = float("nan")
+    p.b_s[0, 0, 1, -1] = float("nan")
+    p.run()
+    bad = torch.zeros(200, 384, dtype=torch.bool, device=DEV)
+    bad[[2, 70]], bad[:, 128:256] = True, True
+    assert torch.isnan(p.c.float())[bad].all() and torch.equal(p.c.float()[~bad], clean[0].float()[~bad])
+    if epi == SWIGLU8:
+        rest = [i for i in range(200) if i not in (2, 70)]
+        assert torch.isnan(p.c_s[:, [2, 70]]).all() and torch.isnan(p.c_s[1]).all() and torch.equal(p.c_s[[0, 2]][:, rest], clean[1][[0, 2]][:, rest])
+
+
+@pytest.mark.parametrize("m", [3, 200])
+def test_cut_products_with_infinite_sums(m):
+    """Sums that leave fp32's range in one CTA's part of K: infinities in their rows, the others as ever."""
+    p = Product(m, 384, 4096, STORE)
+    p.a = p.a.float().abs().to(E4M3)
+    p.b = p.b.float().abs().to(E4M3)
+    clean = p.run()[0].clone()
+    p.a_s[5, 1] = 1e33  # times 223 and a block's sum of some 10^6
+    p.b_s[0, 0, :, 5] = 1e5 / 448
+    rest = [i for i in range(m) if i != 1]
+    want = p.run()[0].clone()
+    assert torch.isinf(want[1]).all() and torch.isfinite(clean).all() and torch.isfinite(want[rest]).all()
+    p.a_s[5, 1] = 1 / 150
+    p.run()
+    p.check()
+    assert torch.equal(p.c[rest], want[rest])
+
+
 # ------------------------------------------------------------------ together
 
 def quant_rows64(y):
