@@ -8,6 +8,7 @@
 #include "../../include/nanoflow.h"
 #include "by_device.h"
 #include "fp8.h"
+#include "fp8_choice.h"
 #include "internal.h"
 #include "kernels.h"
 
@@ -74,33 +75,6 @@ nf_status check_rows(int32_t rows, int32_t cols, const char* what) {
   return NF_OK;
 }
 
-// Whether a product goes to the kernel of few rows of A, which fills the GPU by cutting K
-// (the fewer tiles of weights, the more rows), or to tiles of 128 rows x 256, which read the
-// weights once for all rows.  Few rows / tiles, us, K 4096, by tiles of 128 weight rows:
-//   64 (8192): 64 rows 10.8 / 15.6, 128 rows 13.2 / 15.8; 256 rows of 6144 19.1 / 15.6;
-//   SwiGLU, 32 (2048): 128 rows 11.3 / 12.7; 64 (4096): 64 rows 12.0 / 14.5, 128 rows 15.4 / 14.6;
-//   112 (14336): 64 rows 14.8 / 16.9, 128 rows 19.5 / 17.4;
-//   224 (28672): 16 rows 23.2 / 30.5, 32 rows 23.5 / 23.4, 64 rows 25.1 / 23.8;
-//   224 (SwiGLU, 14336): 32 rows 23.6 / 24.1, 64 rows 25.8 / 24.2;
-//   1002 (128256): 16 rows 89 / 96, 32 rows 97 / 89.
-// By groups, with the rows' mean (a tile has room for twice as many, of SwiGLU for 64):
-//   8 of 1024 x 4096 (64): 64 rows 13.5 / 19.0; SwiGLU, 8 of 512 (64): 32 rows 12.5 / 19.4, 64
-//   rows 21.9 / 19.5; 8 of 2048 (128): 32 rows 16.4 / 20.0, 64 rows 19.9 / 20.6;
-//   8 of 14336 x 4096 SwiGLU: 1 row 73 / 102, 8 rows 139 / 140, 32 rows 165 / 142;
-//   64 of 2048 x 2048: 0.5 rows 26.1 / 28.0, 1 row 40 / 36, 8 rows 58 / 48 (a CTA a tile: short
-//   ones do not pay); 64 of 768 x 2048: 1 row 15.4 / 15.4, 2 rows 25.5 / 24.0.
-// A capped product takes the tiles, which loop.
-bool few_rows(int M, int N, int K, int groups, bool two, int sms) {
-  const int rows = (M + groups - 1) / groups;
-  const int64_t ops = two ? 2 : 1;
-  const int64_t tiles = (N + 127LL) / 128 * ops * (M < groups ? M : groups);
-  if (groups > 1) {
-    if (tiles > sms) return rows <= 16 && (M <= groups || K * ops >= 8192);
-    return rows <= (tiles <= sms / 2 && !two ? 64 : 32);
-  }
-  return rows <= (tiles <= sms / (two ? 4 : 2) ? 128 : tiles <= sms ? 64 : tiles <= 2 * sms ? 32 : 16);
-}
-
 // The product's checks, for one matrix (group_off NULL, groups 1) or by groups.
 nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s,
                 const int32_t* group_off, int32_t groups, void* C, float* c_s, const void* R,
@@ -130,7 +104,7 @@ nf_status gemm8(const void* A, const float* a_s, const void* B, const float* b_s
   if (nf_status e = device_number(&dev)) return e;
   begin_products(dev);
   const bool capped = max_sms > 0 && max_sms < sms;
-  const bool few = !capped && few_rows(M, N, K, groups, two, sms);
+  const bool few = !capped && nf::few_rows(M, N, K, groups, two, sms);
   nf::F8RowsChoice c{};
   if (few) NF_CUDA8(nf::gemm_f8_wrows_choice(epilogue, M, N, K, groups, &c));
   CUtensorMap ta, tb;
