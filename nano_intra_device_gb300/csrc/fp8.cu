@@ -1,5 +1,4 @@
 // C ABI of the 8-bit operators: argument checks, tensor maps, launches.
-#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -34,22 +33,22 @@ nf_status fail8(nf_status s, const char* fmt, ...) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// What nf_fp8_poll goes by.  The kernels count, for a device, the waits that gave up, and the
-// counts only grow; a host thread is told when they differ from what it saw last, so no
+// What nf_fp8_poll goes by.  A wait that gives up raises a flag of its device, a poll that finds
+// it counts it, and a host thread is told when the counts differ from what it saw last: no
 // thread's poll takes a report away from another's.  A thread that begins with a product
-// starts from the highest counts that any poll has read by then: its own timeouts come later.
-struct GaveUp {
-  uint64_t tiles = 0, rows = 0;  // by the two product kernels
+// starts from the counts of the last poll by then: its own flags are counted later.
+struct Flags {
+  uint32_t tiles = 0, rows = 0;  // by the two product kernels
   bool begun = false;            // (of a thread) holds what the thread starts from
 };
-std::mutex g_mu;
-GaveUp g_read[nf::MAX_DEVICES];               // under g_mu: the highest counts read by a poll
-thread_local GaveUp t_seen[nf::MAX_DEVICES];  // what this thread was told of
+std::mutex g_mu;                         // of the counting as well
+Flags g_counted[nf::MAX_DEVICES];        // under g_mu: as of the last poll
+thread_local Flags t_seen[nf::MAX_DEVICES];  // what this thread was told of
 
 void begin_products(int dev) {
   if (t_seen[dev].begun) return;
   std::lock_guard<std::mutex> lk(g_mu);
-  t_seen[dev] = g_read[dev];
+  t_seen[dev] = g_counted[dev];
   t_seen[dev].begun = true;
 }
 
@@ -231,20 +230,15 @@ nf_status nf_fp8_poll(void* stream) {
   NF_CUDA8(cudaStreamIsCapturing(st, &capture));
   if (capture != cudaStreamCaptureStatusNone)
     return fail8(NF_ERR_INVALID_ARG, "the stream is being captured: a poll waits for it");
-  GaveUp now;
-  NF_CUDA8(nf::read_gemm_f8_gave_up(&now.tiles, st));
-  NF_CUDA8(nf::read_gemm_f8_wrows_gave_up(&now.rows, st));
+  NF_CUDA8(cudaStreamSynchronize(st));  // (polls do not wait for one another's streams)
+  std::lock_guard<std::mutex> lk(g_mu);
+  Flags now;
+  NF_CUDA8(nf::count_gemm_f8_flags(&now.tiles, st));
+  NF_CUDA8(nf::count_gemm_f8_wrows_flags(&now.rows, st));
   NF_CUDA8(cudaStreamSynchronize(st));
-  GaveUp& seen = t_seen[dev];
-  const bool more = now.tiles != seen.tiles || now.rows != seen.rows;
-  seen = now;
-  seen.begun = true;
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    GaveUp& all = g_read[dev];
-    all.tiles = std::max(all.tiles, now.tiles);
-    all.rows = std::max(all.rows, now.rows);
-  }
+  now.begun = true;
+  const bool more = now.tiles != t_seen[dev].tiles || now.rows != t_seen[dev].rows;
+  t_seen[dev] = g_counted[dev] = now;
   if (!more) return NF_OK;
   return fail8(NF_ERR_TIMEOUT, "nf_gemm_fp8: a device-side wait timed out");
 }

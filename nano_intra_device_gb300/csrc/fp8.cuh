@@ -135,8 +135,11 @@ __device__ __forceinline__ uint32_t f8_codes4_near(float a, float b, float c, fl
   return lo | (hi << 16);
 }
 // silu(g) u = g u / (1 + 2^(-g log2 e)): exponential and reciprocal by the hardware's
-// approximations (2 and 1 units in the last place).  A g below -126 ln 2 gives zero, as
-// the reciprocal of anything above 2^126 does; infinite g: NaN or g u.
+// approximations (2 and 1 units in the last place).  The rounded product g log2 e weighs more
+// where the exponential does, at g < 0: ln 2 times its half step, and 2^-26 g of log2 e's own
+// rounding, are some 2^-21 of the value at g = -8, 2^-19 at -32 and 2^-18 at -88, beside 2^-9
+// of bf16's rounding and 2^-4 of e4m3's.  A g below -126 ln 2 gives zero, as the reciprocal of
+// anything above 2^126 does; infinite g: NaN or g u.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));

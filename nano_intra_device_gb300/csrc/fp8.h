@@ -12,7 +12,9 @@ constexpr int F8_MAX_GROUPS = 128;   // groups of rows of one product
 // After a wait gave up: the limit of the waits for what is in flight already (loads,
 // products), which takes microseconds, whatever the call's own limit is.
 constexpr unsigned long long F8_DRAIN_NS = 20000000ULL;
-constexpr int F8_MAX_COLS = 32768;   // columns of a row that one CTA norms or quantises
+// Columns of a row that one CTA norms, in registers.  Rows quantised without a norm are held
+// to the same limit, though their kernel would take more.
+constexpr int F8_MAX_COLS = 32768;
 
 enum { F8_STORE = 0, F8_RESID = 1, F8_SWIGLU = 2, F8_SWIGLU8 = 3 };
 
@@ -51,9 +53,10 @@ struct F8GemmArgs {
 // (SwiGLU: 64) rows, x 128 columns.
 cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& tmB,
                            const F8GemmArgs& args, int sms, cudaStream_t stream);
-// How often waits of the kernels of launch_gemm_f8 gave up on the current device since the
-// process began, copied to *count in the stream's order.
-cudaError_t read_gemm_f8_gave_up(uint64_t* count, cudaStream_t stream);
+// Takes the flag that a wait of the kernels of launch_gemm_f8 raised on the current device,
+// and copies to *count, in the stream's order, how many flags were taken since the process
+// began.  One call at a time on a device, until the stream has been waited for.
+cudaError_t count_gemm_f8_flags(uint32_t* count, cudaStream_t stream);
 
 // The same for few rows: tiles of 128 features x tok rows of A (tmX: the rows of A in
 // boxes of tok rows; tok 16, 32, 64 and, but for SwiGLU, 128), `units` clusters of
@@ -65,6 +68,6 @@ struct F8RowsChoice {
 cudaError_t gemm_f8_wrows_choice(int epi, int M, int N, int K, int groups, F8RowsChoice* choice);
 cudaError_t launch_gemm_f8_wrows(int epi, int tok, const CUtensorMap& tmW, const CUtensorMap& tmX,
                                  const F8GemmArgs& args, long long units, cudaStream_t stream);
-cudaError_t read_gemm_f8_wrows_gave_up(uint64_t* count, cudaStream_t stream);
+cudaError_t count_gemm_f8_wrows_flags(uint32_t* count, cudaStream_t stream);
 
 }  // namespace nf

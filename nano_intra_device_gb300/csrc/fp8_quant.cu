@@ -10,7 +10,7 @@
 // Bound by memory: one pass, 16-byte loads, a row of the norm in the registers of its
 // CTA between the sum of squares and the codes.  Reached (of 6.68 TB/s copied): norm with
 // residual, 4096 rows of 8192, 39 us = 6.0 TB/s; quantisation, 4096 rows of 14336, 28 us =
-// 6.3 TB/s, by an index 4094 rows of 4096 9.5 us; two matrices of 14336 x 4096, 56 us =
+// 6.3 TB/s, by an index 4094 rows of 4096 8.7 us; two matrices of 14336 x 4096, 56 us =
 // 6.3 TB/s.  Few rows: launch and latency, 1.4 to 2 us in a graph.
 #include "fp8.cuh"
 

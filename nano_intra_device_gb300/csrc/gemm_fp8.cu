@@ -22,10 +22,10 @@
 //    sixteen summing warps of 64 columns 718, the next block's loads ahead of this one's
 //    last sums 890, packed pairs of sums 893 (moves), one hand-over for all 256 columns
 //    884, B multicast to two CTAs 703 (shorter products 4 to 7 % slower).
-//  * A product with tiles for less than a half (a quarter) of the SMs is cut along K between
+//  * A product with tiles for at most a half (a quarter) of the SMs is cut along K between
 //    the two (four) CTAs of a cluster (SPLIT): each finishes its part of the tile's columns
 //    (SwiGLU: of its rows), with the others' sums from their shared memory.
-//  * Every wait is bounded; one that gives up is counted, and the kernel
+//  * Every wait is bounded; one that gives up flags the status word, and the kernel
 //    drains what it has in flight (bounded) and frees tensor memory.
 #include <type_traits>
 
@@ -75,9 +75,7 @@ struct Tail {
 constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 8 * STORE_BYTES + TAIL_BYTES;
 static_assert(sizeof(Tail) <= TAIL_BYTES && SMEM <= 232448, "shared memory");
 
-// Times that a wait of this file's kernels gave up on the device.  It only grows: callers
-// compare it with what they last saw.
-__device__ unsigned long long g_gave_up;
+__device__ uint32_t g_status;
 
 struct Tile {
   int m0, m_lim, tn, e;
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tail->issued = issued;
       tail->phases = phases;
       if (!ok) {
-        atomicAdd(&g_gave_up, 1ULL);
+        raise_status(&g_status, ST_TIMEOUT);
         *abort_flag = 1;
       }
     }
@@ -269,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok && one) {
-        atomicAdd(&g_gave_up, 1ULL);
+        raise_status(&g_status, ST_TIMEOUT);
         *abort_flag = 1;
       }
       if (one) tail->issuer[h] = any ? lane : 32;
@@ -302,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) {
-        atomicAdd(&g_gave_up, 1ULL);
+        raise_status(&g_status, ST_TIMEOUT);
         *abort_flag = 1;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -503,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       } else {
-        constexpr int CHUNKS = SW ? 2 : 4 / SPLIT;  // (SwiGLU: not cut)
+        constexpr int CHUNKS = SW ? 2 : 4 / SPLIT;  // (a cut SwiGLU product is finished above)
 #pragma unroll
         for (int h = 0; h < CHUNKS; ++h) {
           const int n0 = x.tn * TN + half * (TN / 2) + (rank * CHUNKS + h) * 32;
@@ -545,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     if (!ok) {
-      atomicAdd(&g_gave_up, 1ULL);
+      raise_status(&g_status, ST_TIMEOUT);
       *abort_flag = 1;
     }
   }
@@ -569,6 +567,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
   if (SPLIT > 1) cluster_leave();
+}
+
+// Counted where a poll finds it (counted by every thread that gives up, 4096 x 8192 x 28672
+// takes 870 us, so 790: the compiler orders the sums otherwise).
+__device__ uint32_t g_flags;
+__global__ void count_flag_kernel() {
+  if (atomicExch(&g_status, 0u)) ++g_flags;
 }
 
 // Clusters of SPLIT CTAs that the current device holds at once; asked once a device.
@@ -613,10 +618,10 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
                          ((args.N + tn - 1) / tn);
   if (most > 0x7fffffffLL || args.groups > F8_MAX_GROUPS) return cudaErrorInvalidValue;
   if (most <= 0) return cudaSuccess;
-  // Tiles for less than half of the SMs, and eight blocks of K at least for each of two
+  // Tiles for at most half of the SMs, and eight blocks of K at least for each of two
   // CTAs.  Whole / cut: 333 x 6144 x 4096 18.4 / 15.8 us, 333 x 4096 x 14336 49 / 31,
-  // 256 x 8192 x 28672 95 / 60; 512 x 2048 x 2048 11.5 either way, x 1024 8.4 / 9.5.  For less
-  // than a quarter of the SMs four; two / four: 256 x 4096 x 14336 35 / 24, 256 x 4096 x 4096
+  // 256 x 8192 x 28672 95 / 60; 512 x 2048 x 2048 11.5 either way, x 1024 8.4 / 9.5.  For at
+  // most a quarter of the SMs four; two / four: 256 x 4096 x 14336 35 / 24, 256 x 4096 x 4096
   // 14.4 either way, x 2048 11.4 / 12.5, 256 x 2048 x 4096 SwiGLU 15.5 / 13.0.
   // A tile more than clusters fit is a second wave: 38 tiles of 256 x 4864 x 4096 in two parts
   // 14.8, in four (152 SMs, in groups that hold 36 clusters of four) 25.1.
@@ -651,8 +656,10 @@ cudaError_t launch_gemm_f8(int epi, const CUtensorMap& tmA, const CUtensorMap& t
   }
 }
 
-cudaError_t read_gemm_f8_gave_up(uint64_t* count, cudaStream_t stream) {
-  return cudaMemcpyFromSymbolAsync(count, g_gave_up, sizeof(*count), 0, cudaMemcpyDeviceToHost, stream);
+cudaError_t count_gemm_f8_flags(uint32_t* count, cudaStream_t stream) {
+  count_flag_kernel<<<1, 1, 0, stream>>>();
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? cudaMemcpyFromSymbolAsync(count, g_flags, 4, 0, cudaMemcpyDeviceToHost, stream) : e;
 }
 
 }  // namespace nf

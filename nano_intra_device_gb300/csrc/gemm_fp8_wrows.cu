@@ -68,7 +68,7 @@ struct Tail {
 };
 static_assert(sizeof(Tail) <= TAIL_BYTES, "barrier block");
 
-__device__ unsigned long long g_gave_up;  // as in gemm_fp8.cu
+__device__ uint32_t g_status;
 
 template <int EPI, int TOK>
 __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       uint32_t st = 0, ph = 0;
       for (int i = 0; i < klen; ++i) {
         if (!mbar_wait(&tail->empty[st], ph ^ 1, tmo, abort_flag)) {
-          atomicAdd(&g_gave_up, 1ULL);
+          raise_status(&g_status, ST_TIMEOUT);
           *abort_flag = 1;
           break;
         }
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       for (int i = 0; i < klen; ++i) {
         if (!mbar_wait(&tail->tempty[acc], aph ^ 1, tmo, abort_flag) ||
             !mbar_wait(&tail->full[st], ph, tmo, abort_flag)) {
-          atomicAdd(&g_gave_up, 1ULL);
+          raise_status(&g_status, ST_TIMEOUT);
           *abort_flag = 1;
           break;
         }
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     // Column half * MINE + lane + 32 i of the accumulator: its row of A, its operand of B.
     constexpr int CI = (MINE + 31) / 32, AHEAD = 4;
     const float* bs = args.b_s + (static_cast<size_t>(e) * NA * nb + wt) * nk;
-    float px[AHEAD][CI], pw[AHEAD][CI];  // a ring, in place, as in gemm_fp8.cu
+    float px[AHEAD][CI], pw[AHEAD][CI];  // of the next blocks of K, each in its place of a ring
     auto fetch = [&](int i, int at) {
 #pragma unroll
       for (int j = 0; j < CI; ++j) {
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
       for (int j = 0; j < AHEAD; ++j)
         if (ok && i + j < klen) ok = block(i + j, j);
     if (!ok) {
-      atomicAdd(&g_gave_up, 1ULL);
+      raise_status(&g_status, ST_TIMEOUT);
       *abort_flag = 1;
     }
     // The exchange: this CTA's sums to its shared memory (every product that read the
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     // (a release at cluster scope, behind the barrier that all of the CTA's writes precede)
     if (warp == 2 && lane < S) mbar_arrive_remote(cluster_map(smem_u32(&tail->ready), lane));
     if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tail->ready, 0, tmo))) {
-      atomicAdd(&g_gave_up, 1ULL);
+      raise_status(&g_status, ST_TIMEOUT);
       *abort_flag = 1;
     } else {
       const int nv = min(TOK, m_lim - m0);
@@ -426,6 +426,11 @@ __global__ void __launch_bounds__(Cfg<EPI, TOK>::THREADS, Cfg<EPI, TOK>::PER_SM)
     tmem_dealloc(tmem_base, C::TMEM);
   }
   cluster_leave();
+}
+
+__device__ uint32_t g_flags;
+__global__ void count_flag_kernel() {
+  if (atomicExch(&g_status, 0u)) ++g_flags;
 }
 
 template <int EPI, int TOK>
@@ -552,8 +557,10 @@ cudaError_t launch_gemm_f8_wrows(int epi, int tok, const CUtensorMap& tmW, const
   return e < 0 ? cudaErrorInvalidValue : static_cast<cudaError_t>(e);
 }
 
-cudaError_t read_gemm_f8_wrows_gave_up(uint64_t* count, cudaStream_t stream) {
-  return cudaMemcpyFromSymbolAsync(count, g_gave_up, sizeof(*count), 0, cudaMemcpyDeviceToHost, stream);
+cudaError_t count_gemm_f8_wrows_flags(uint32_t* count, cudaStream_t stream) {
+  count_flag_kernel<<<1, 1, 0, stream>>>();
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? cudaMemcpyFromSymbolAsync(count, g_flags, 4, 0, cudaMemcpyDeviceToHost, stream) : e;
 }
 
 }  // namespace nf

@@ -10,7 +10,9 @@ Quantisation of given values is compared exactly (codes and scales).  Bounds els
   truncate: 2^-23 of the sum of magnitudes), then scaled and added up, one rounding each, over the blocks
   of K: (128 * 2^-23 + (blocks + 3) * 2^-24) of the sum of magnitudes, beside the stored value's half step
   2^-8.  SwiGLU: the products' errors through silu'(g) u and silu(g), |silu'| <= 1.1, |silu(g)| <= |g|,
-  and its own arithmetic: exp within 2^-21 (1 + |g| 2^-24 is covered), a quotient and two products, 2^-19 of the value.
+  and its own arithmetic, 2^-19 of the value: exp within 2^-21 up to |g| = 8, a quotient and two products.  At larger -g
+  the rounded product g log2 e moves the exponential by up to 2^-18 of a value that is below |g u| e^-8 there, which the
+  term above, 128 * 2^-23 |g u| at least, is larger than.
 """
 import numpy as np
 import pytest
