@@ -578,7 +578,7 @@ nf_status nf_attention_kv4(nf_kv4 h, const void* q, const nf_kv_cache* cache,
  * bytes of their weights at decode batches and by the tensor rate at larger
  * ones ("NanoFlow: Towards Optimal LLM Serving Throughput", "The Intra-Device
  * Parallelism Mechanism"); 8-bit operands halve the one, and the tensor core
- * takes them at twice the rate (1.4 to 1.6 times that of nf_gemm is reached).
+ * takes them at twice the rate (1.6 times that of nf_gemm is reached).
  * The entry points bring activations and weights into the format and multiply
  * them, for one matrix or by experts; they stand beside nf_rmsnorm and nf_gemm.
  *

@@ -25,8 +25,8 @@ namespace nf {
 //   23.8 / 23.9, of 8 of 8192 x 2048 15.6 / 17.9; of 64 of 1024 x 4096 41 / 44, of 2048 x 4096
 //   67 / 66, of 768 x 2048 SwiGLU 25.5 / 29.7.
 // A capped product takes the tiles, which loop (a unit of the other kernel is a cluster of its
-// own): 1 row of 4096 x 14336 13.5 us without a cap, 22.3 under one of 76 SMs or more, 30.7
-// under 38; 64 rows 15.6, 22.8, 31.6.
+// own): 1 row of 4096 x 14336 13.5 us without a cap, 22.5 under one of 76 SMs or more, 30.5
+// under 38; 64 rows 15.6, 23.0, 31.4.
 inline bool few_rows(int M, int N, int K, int groups, bool two, int sms) {
   const int rows = (M + groups - 1) / groups;
   const int64_t ops = two ? 2 : 1;

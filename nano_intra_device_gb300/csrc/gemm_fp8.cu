@@ -15,7 +15,8 @@
 //  * What bounds it: the hand-over between products and sums.  A block of K is 528 cycles
 //    of products (two halves of four instructions), but a half's accumulator goes issue,
 //    completion, sums' loads, release, issue, some 1500 cycles for two blocks; about 800
-//    cycles a block are reached, 57 % of the tensor pipe.  In long runs the power limit
+//    cycles a block are reached, 57 % of the tensor pipe.  (What an SM takes in, 61 bytes a
+//    cycle then, may bind beside it: not measured apart.)  In long runs the power limit
 //    counts as well: 4096 x 8192 x 28672 takes 685 to 705 us (2.8 PFLOP/s) for the first dozens
 //    of calls and 800 us (1590 MHz, 1360 W) after seconds.  Measured and not kept, on that
 //    product at 711: one issuing warp for both halves 946, one for each accumulator 748,
